@@ -1,0 +1,378 @@
+// rotary.cu -- rotary positions on the three axes of a video grid, and the append of rotated
+// keys (and values) to a paged cache.
+//
+// A pair (x0, x1) of a head's values turns by its axis's angle a = x_axis * theta^(-j / n):
+//   y0 = x0 cos a - x1 sin a,   y1 = x1 cos a + x0 sin a   (fp32, rounded once),
+// the inverse (and so the backward pass) with -sin a.  cos and sin come from a table built
+// in 64 bits, one row per position of each axis: 146 rows for 21 x 45 x 80 tokens, resident
+// in L1.  Pure data movement otherwise: each value is read once and written once.
+//
+// One thread owns one 16-byte piece of a token's row (with halves layout the piece and its
+// partner P values further) and walks the heads with it: the token's place and the
+// piece's cos / sin are found once for all heads, and kBatch loads are in flight at a time.
+// Consecutive threads hold consecutive pieces, so rows move whole.  When there are few
+// tokens (a decoding step) the heads are dealt over blocks instead, so that the launch
+// still covers the GPU.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "stream.h"
+#include "svga_device.cuh"
+
+namespace svga {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // heads whose loads are in flight together
+
+struct Orders {
+    uint8_t order[kMaxHeads];
+};
+struct NoOrders {
+    uint8_t unused;
+};
+
+enum { DST_PLAIN = 0, DST_ORDERED = 1, DST_PAGED = 2 };
+enum { LAY_INTERLEAVED = 0, LAY_HALVES = 1, LAY_HALVES_ODD = 2 };
+
+struct RotParams {
+    View src, dst;
+    View src2;  // paged: the values (copied, not turned)
+    int batch, heads, tokens, d, units;
+    int heads_per_thread;
+    int F, gh, gw, S;
+    int pf, ph, P;  // pairs of axis 0, of axis 1, of all
+    const float2 *table;
+    const int32_t *positions;
+    long long first;
+    int inverse, turn;
+    int32_t *status;
+    // paged
+    char *k_pages, *v_pages;
+    int pages, page_size, max_pages;
+    const int32_t *page_table, *lens, *new_lens;
+};
+
+template <typename T>
+struct Vec {
+    static constexpr int N = 16 / sizeof(T);
+    T x[N];
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float &y, float x) { y = x; }
+__device__ __forceinline__ void from_f(__half &y, float x) { y = __float2half_rn(x); }
+__device__ __forceinline__ void from_f(__nv_bfloat16 &y, float x) { y = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ void set_status(int32_t *status)
+{
+    if (status) atomicCAS(status, 0, (int32_t)SVGA_ERR_INVALID_ARG);
+}
+
+// cos and sin of pair i at place (f, r, c)
+__device__ __forceinline__ float2 pair_cs(const RotParams &p, int i, int f, int r, int c)
+{
+    const int pw = p.P - p.pf - p.ph;
+    int at;
+    if (i < p.pf)
+        at = f * p.pf + i;
+    else if (i < p.pf + p.ph)
+        at = p.F * p.pf + r * p.ph + (i - p.pf);
+    else
+        at = p.F * p.pf + p.gh * p.ph + c * pw + (i - p.pf - p.ph);
+    return __ldg(p.table + at);
+}
+
+template <typename T, int LAY, int DST, typename Ord>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
+                                                          const __grid_constant__ Ord ord)
+{
+    constexpr int V = LAY == LAY_HALVES_ODD ? 1 : Vec<T>::N;  // values of a piece
+    const long long idx = blockIdx.x * (long long)kThreads + threadIdx.x;
+    // 32-bit divisions where the piece index fits (64-bit ones cost a tenth of the kernel)
+    const bool small = (long long)p.batch * p.tokens * p.units <= 0x7fffffffll;
+    const long long tok_all = small ? (int)idx / p.units : idx / p.units;
+    if (tok_all >= (long long)p.batch * p.tokens) return;
+    const int unit = (int)(idx - tok_all * p.units);
+    const int b = small ? (int)tok_all / p.tokens : (int)(tok_all / p.tokens);
+    const int t = (int)(tok_all - (long long)b * p.tokens);
+    const bool values = DST == DST_PAGED && blockIdx.z == 1;
+    const bool turn = p.turn && !values;
+
+    // the token's place in the grid
+    long long pos;
+    if (DST == DST_PAGED) {
+        const int n = p.new_lens ? __ldg(p.new_lens + b) : p.tokens;
+        const int len = __ldg(p.lens + b);
+        if (n < 0 || n > p.tokens || len < 0) {
+            if (unit == 0) set_status(p.status);
+            return;
+        }
+        if (t >= n) return;
+        pos = (long long)len - n + t;
+    } else {
+        pos = p.positions ? (long long)__ldg(p.positions + tok_all) : p.first + t;
+    }
+    int f = 0, s = 0, row = 0, col = 0;
+    if (turn || DST == DST_ORDERED) {
+        if (pos < 0 || pos >= (long long)p.F * p.S) {
+            if (unit == 0) set_status(p.status);
+            return;
+        }
+        f = (int)(pos / p.S);
+        s = (int)(pos - (long long)f * p.S);
+        row = s / p.gw;
+        col = s - row * p.gw;
+    }
+    long long paged_row = 0;  // row of head 0 in the page array
+    if (DST == DST_PAGED) {
+        const long long slot = pos < 0 ? -1 : pos / p.page_size;
+        const int page = slot >= 0 && slot < p.max_pages
+                             ? __ldg(p.page_table + (long long)b * p.max_pages + slot)
+                             : -1;
+        if (page < 0 || page >= p.pages) {
+            if (unit == 0) set_status(p.status);
+            return;
+        }
+        paged_row = (long long)page * p.heads * p.page_size + (pos - slot * p.page_size);
+    }
+
+    // the piece: values lo .. lo + V - 1 and, with halves, hi .. hi + V - 1
+    int lo, hi = -1, pair0 = -1;  // pair0 < 0: copied unchanged
+    if (LAY == LAY_INTERLEAVED) {
+        lo = unit * V;
+        if (turn && lo / 2 < p.P) pair0 = lo / 2;
+    } else {
+        const int n = p.P / V;  // pieces of the turned half
+        if (unit < n) {
+            lo = unit * V;
+            hi = lo + p.P;
+            if (turn) pair0 = lo;
+        } else {
+            lo = 2 * p.P + (unit - n) * V;
+        }
+    }
+    constexpr int NP = LAY == LAY_INTERLEAVED ? (V + 1) / 2 : V;  // pairs of a piece
+    float cs[NP], sn[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        cs[j] = 1.f;
+        sn[j] = 0.f;
+        if (pair0 >= 0 && pair0 + j < p.P) {
+            const float2 x = pair_cs(p, pair0 + j, f, row, col);
+            cs[j] = x.x;
+            sn[j] = p.inverse ? -x.y : x.y;
+        }
+    }
+
+    struct alignas(V * sizeof(T)) Piece {
+        T x[V];
+    };
+    const View &sv = values ? p.src2 : p.src;
+    const T *src = reinterpret_cast<const T *>(sv.p) + b * sv.sb;
+    T *dst = DST == DST_PAGED ? reinterpret_cast<T *>(values ? p.v_pages : p.k_pages)
+                              : reinterpret_cast<T *>(p.dst.p) + b * p.dst.sb;
+    const int h0 = blockIdx.y * p.heads_per_thread;
+    const int h1 = min(h0 + p.heads_per_thread, p.heads);
+    for (int h = h0; h < h1; h += kBatch) {
+        Piece a[kBatch], c[kBatch];
+        int at[kBatch];  // the ordered side's row
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (h + u >= h1) break;
+            at[u] = t;
+            if constexpr (DST == DST_ORDERED)
+                at[u] = coord_to_pos(ord.order[h + u], f, s, p.F, p.S);
+            const T *x = src + (h + u) * sv.sh + (p.inverse ? at[u] : t) * sv.st;
+            a[u] = *reinterpret_cast<const Piece *>(x + lo);
+            if (LAY != LAY_INTERLEAVED && hi >= 0) c[u] = *reinterpret_cast<const Piece *>(x + hi);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (h + u >= h1) break;
+            if (pair0 >= 0) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    if (LAY == LAY_INTERLEAVED) {
+                        if (pair0 + j >= p.P) continue;
+                        if constexpr (V > 1) {
+                            const float x0 = to_f(a[u].x[2 * j]), x1 = to_f(a[u].x[2 * j + 1]);
+                            from_f(a[u].x[2 * j], x0 * cs[j] - x1 * sn[j]);
+                            from_f(a[u].x[2 * j + 1], x1 * cs[j] + x0 * sn[j]);
+                        }
+                    } else {
+                        const float x0 = to_f(a[u].x[j]), x1 = to_f(c[u].x[j]);
+                        from_f(a[u].x[j], x0 * cs[j] - x1 * sn[j]);
+                        from_f(c[u].x[j], x1 * cs[j] + x0 * sn[j]);
+                    }
+                }
+            }
+            T *y = DST == DST_PAGED
+                       ? dst + (paged_row + (long long)(h + u) * p.page_size) * p.d
+                       : dst + (h + u) * p.dst.sh + (p.inverse ? t : at[u]) * p.dst.st;
+            *reinterpret_cast<Piece *>(y + lo) = a[u];
+            if (LAY != LAY_INTERLEAVED && hi >= 0) *reinterpret_cast<Piece *>(y + hi) = c[u];
+        }
+    }
+}
+
+// Table entry (position x, pair j of an axis with n pairs): the angle x * theta^(-j / n) in
+// 64 bits.  One thread per entry; built once per grid.
+__global__ void __launch_bounds__(kThreads) rotary_table_kernel(int F, int gh, int gw, int pf,
+                                                                int ph, int pw, double theta,
+                                                                float2 *table)
+{
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    const int nf = F * pf, nh = gh * ph, nw = gw * pw;
+    if (i >= nf + nh + nw) return;
+    int k = i, n = pf;
+    if (i >= nf + nh) {
+        k = i - nf - nh;
+        n = pw;
+    } else if (i >= nf) {
+        k = i - nf;
+        n = ph;
+    }
+    const int x = k / n, j = k - x * n;
+    double sn, cs;
+    sincos((double)x * pow(theta, -(double)j / n), &sn, &cs);
+    table[i] = make_float2((float)cs, (float)sn);
+}
+
+View to_view(const svga_view &v)
+{
+    return {static_cast<char *>(v.data), v.stride_batch, v.stride_head, v.stride_token};
+}
+
+// Grid of a launch: pieces over x, heads over y where the tokens alone give too few
+// blocks.  Measured on 64 sequences of one token with 16 heads of 64: 16 heads a thread
+// leave 2 blocks, one head a thread gives 32; at 75,600 tokens the table look-ups are
+// shared by all heads of a thread.
+template <typename T, int LAY, int DST, typename Ord>
+svga_status launch(RotParams &p, const Ord &ord, cudaStream_t st)
+{
+    constexpr int V = LAY == LAY_HALVES_ODD ? 1 : Vec<T>::N;
+    p.units = LAY == LAY_INTERLEAVED ? p.d / V : p.P / V + (p.d - 2 * p.P) / V;
+    const long long pieces = (long long)p.batch * p.tokens * p.units;
+    const long long blocks = (pieces + kThreads - 1) / kThreads;
+    if (blocks == 0 || p.heads == 0) return SVGA_OK;
+    if (blocks > 0x7fffffffll) {
+        set_error("rotary: %lld blocks do not fit one launch", blocks);
+        return SVGA_ERR_SHAPE;
+    }
+    int hpt = p.heads;
+    while (hpt > 1 && blocks * ((p.heads + hpt - 1) / hpt) < 2 * 148) hpt = (hpt + 1) / 2;
+    p.heads_per_thread = hpt;
+    const dim3 grid((unsigned)blocks, (unsigned)((p.heads + hpt - 1) / hpt),
+                    DST == DST_PAGED ? 2 : 1);
+    rotary_kernel<T, LAY, DST, Ord><<<grid, kThreads, 0, st>>>(p, ord);
+    return check_launch_of("rotary");
+}
+
+template <typename T, int DST, typename Ord>
+svga_status launch_layout(RotParams &p, bool interleaved, const Ord &ord, cudaStream_t st)
+{
+    if (interleaved) return launch<T, LAY_INTERLEAVED, DST>(p, ord, st);
+    // halves: pieces of 16 bytes need P and the rest behind 2P to be whole pieces
+    if (p.P % Vec<T>::N == 0) return launch<T, LAY_HALVES, DST>(p, ord, st);
+    return launch<T, LAY_HALVES_ODD, DST>(p, ord, st);
+}
+
+template <int DST, typename Ord>
+svga_status launch_type(RotParams &p, svga_dtype dt, bool interleaved, const Ord &ord,
+                        cudaStream_t st)
+{
+    if (dt == SVGA_BF16) return launch_layout<__nv_bfloat16, DST>(p, interleaved, ord, st);
+    if (dt == SVGA_F16) return launch_layout<__half, DST>(p, interleaved, ord, st);
+    if constexpr (DST == DST_PAGED) {
+        set_error("a paged cache holds bf16 or fp16");
+        return SVGA_ERR_UNSUPPORTED;
+    } else {
+        return launch_layout<float, DST>(p, interleaved, ord, st);
+    }
+}
+
+void set_spec(RotParams &p, const svga_rotary_spec *spec, const float *table)
+{
+    p.F = p.gh = p.gw = p.S = 1;
+    if (!spec) return;
+    p.F = spec->num_frames;
+    p.gh = spec->grid_h;
+    p.gw = spec->grid_w;
+    p.S = p.gh * p.gw;
+    p.pf = spec->pairs[0];
+    p.ph = spec->pairs[1];
+    p.P = p.pf + p.ph + spec->pairs[2];
+    p.table = reinterpret_cast<const float2 *>(table);
+    p.turn = 1;
+}
+
+}  // namespace
+
+svga_status launch_rotary_table(const svga_rotary_spec *s, double theta, float *table,
+                                void *stream)
+{
+    const int n = s->num_frames * s->pairs[0] + s->grid_h * s->pairs[1] + s->grid_w * s->pairs[2];
+    if (n == 0) return SVGA_OK;
+    rotary_table_kernel<<<(n + kThreads - 1) / kThreads, kThreads, 0,
+                          static_cast<cudaStream_t>(stream)>>>(
+        s->num_frames, s->grid_h, s->grid_w, s->pairs[0], s->pairs[1], s->pairs[2], theta,
+        reinterpret_cast<float2 *>(table));
+    return check_launch_of("rotary table");
+}
+
+svga_status launch_rotary(const svga_view &src, const svga_view &dst, int batch, int heads,
+                          int tokens, int d, svga_dtype dt, const svga_rotary_spec *spec,
+                          const float *table, const int32_t *positions, long long first_token,
+                          int inverse, int32_t *status, void *stream)
+{
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    RotParams p{};
+    p.src = to_view(src);
+    p.dst = to_view(dst);
+    p.batch = batch;
+    p.heads = heads;
+    p.tokens = tokens;
+    p.d = d;
+    set_spec(p, spec, table);
+    p.positions = positions;
+    p.first = first_token;
+    p.inverse = inverse;
+    p.status = status;
+    if (spec->order) {
+        Orders o;
+        for (int h = 0; h < heads; ++h) o.order[h] = (uint8_t)spec->order[h];
+        return launch_type<DST_ORDERED>(p, dt, spec->interleaved != 0, o, st);
+    }
+    return launch_type<DST_PLAIN>(p, dt, spec->interleaved != 0, NoOrders{0}, st);
+}
+
+svga_status launch_append(const svga_view &k, const svga_view &v, int tokens,
+                          const int32_t *new_lens, const svga_paged_cache *c,
+                          const svga_rotary_spec *spec, const float *table, void *stream)
+{
+    RotParams p{};
+    p.src = to_view(k);
+    p.src2 = to_view(v);
+    p.batch = c->batch;
+    p.heads = c->kv_heads;
+    p.tokens = tokens;
+    p.d = c->head_dim;
+    set_spec(p, spec, table);
+    p.status = c->status;
+    p.k_pages = static_cast<char *>(c->k_pages);
+    p.v_pages = static_cast<char *>(c->v_pages);
+    p.pages = c->pages;
+    p.page_size = c->page_size;
+    p.max_pages = c->max_pages;
+    p.page_table = c->page_table;
+    p.lens = c->lens;
+    p.new_lens = new_lens;
+    return launch_type<DST_PAGED>(p, c->dtype, !spec || spec->interleaved != 0, NoOrders{0},
+                                  static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace svga

@@ -1,0 +1,145 @@
+// stream.h -- what the streaming attention calls share: the window mask's arithmetic and the
+// parameters their kernels take.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+#include "svga_internal.h"
+
+namespace svga {
+
+constexpr int kMaxMask = 1 << 24;  // largest window, sinks, block and token count
+
+// ------------------------------------------------------------------------- the mask
+// The keys query position p keeps are [lo, hi) and [0, sk); all three never decrease
+// with p, so a run of queries keeps nothing outside [lo(first), hi(last)) and
+// [0, sk(last)), and everything inside [lo(last), hi(first)) and [0, sk(first)).
+struct MaskRange {
+    int lo, hi, sk;
+};
+
+struct Mask {
+    int causal, window, sinks, block;
+};
+
+__host__ __device__ __forceinline__ int floor_div(int a, int b)
+{
+    const int q = a / b;
+    return (a % b != 0 && a < 0) ? q - 1 : q;
+}
+
+__host__ __device__ __forceinline__ int clamp_tokens(long long x, int n)
+{
+    return x < 0 ? 0 : (x > n ? n : (int)x);
+}
+
+__host__ __device__ __forceinline__ MaskRange mask_range(const Mask &m, int p, int nk)
+{
+    // block indices times block pass 32 bits: window and block are up to 2^24 each
+    const long long b = m.block == 1 ? p : floor_div(p, m.block);
+    const int own_end = clamp_tokens((b + 1) * m.block, nk);  // end of the query's own block
+    MaskRange r;
+    if (m.window < 0) {
+        r.hi = m.causal ? own_end : nk;
+        r.lo = 0;
+        r.sk = 0;
+        return r;
+    }
+    r.hi = m.causal ? own_end : clamp_tokens((b + m.window + 1) * m.block, nk);
+    const int lo = clamp_tokens((b - m.window) * m.block, nk);
+    r.lo = lo < r.hi ? lo : r.hi;
+    const int sk = m.causal ? own_end : nk;
+    r.sk = m.sinks < sk ? m.sinks : sk;
+    return r;
+}
+
+// The queries that keep key j (0 <= j < nk) are the rows [first, end) of 0 .. nq - 1, with
+// off = nk - nq: the inverse of mask_range, contiguous for every mask.
+__host__ __device__ __forceinline__ void mask_rows(const Mask &m, int j, int nq, int off,
+                                                   int &first, int &end)
+{
+    const long long b = m.block == 1 ? j : j / m.block;
+    const bool sink = m.window >= 0 && j < m.sinks;
+    long long a = 0, e = (long long)nq + off;  // positions
+    bool all_before = false;
+    if (m.causal)
+        a = b * m.block;
+    else if (m.window >= 0 && !sink)
+        a = (b - m.window) * m.block;
+    else
+        all_before = true;
+    if (m.window >= 0 && !sink) e = (b + m.window + 1) * m.block;
+    first = all_before ? 0 : clamp_tokens(a - off, nq);
+    end = clamp_tokens(e - off, nq);
+    if (end < first) end = first;
+}
+
+// The 128-key chunks one run of query positions [p0, p1] visits: [0, a) for the sinks and
+// [w0, w1) for the window (overlapping chunks count once), and the ones every query of
+// the run keeps whole.
+struct ChunkList {
+    int a, w0, w1;   // visited
+    int fa, f0, f1;  // full: c < fa, or f0 <= c < f1
+    __host__ __device__ __forceinline__ bool visits(int c) const
+    {
+        return c < a || (c >= w0 && c < w1);
+    }
+    __host__ __device__ __forceinline__ bool full(int c) const
+    {
+        return c < fa || (c >= f0 && c < f1);
+    }
+};
+
+template <int KN>
+__host__ __device__ __forceinline__ ChunkList chunk_list(const Mask &m, int p0, int p1, int nk)
+{
+    const MaskRange r0 = mask_range(m, p0, nk), r1 = mask_range(m, p1, nk);
+    ChunkList c;
+    c.a = (r1.sk + KN - 1) / KN;
+    c.w0 = r0.lo / KN;
+    c.w1 = r1.hi > r0.lo ? (r1.hi + KN - 1) / KN : c.w0;
+    c.fa = r0.sk / KN;
+    c.f0 = r1.lo <= r0.sk ? 0 : (r1.lo + KN - 1) / KN;  // sinks that reach the window join it
+    c.f1 = r0.hi / KN;
+    return c;
+}
+
+// ------------------------------------------------------------------- kernel parameters
+// A strided tensor in kernel parameters (strides in elements).
+struct View {
+    char *p;
+    long long sb, sh, st;
+};
+
+// tensor_map.cu: 4-D map (d, token, head, batch) of a strided view of 16-bit elements, box
+// 64 columns x box_rows tokens, 128-byte swizzle.  A broadcast (stride 0) or one-entry
+// dimension is mapped with extent 1: coordinates in it are multiplied by *mul_h / *mul_b
+// (0 or 1).  False: the driver refused it.
+bool make_view_map(void *map, const svga_view &v, int batch, int heads, int tokens, int d,
+                   svga_dtype dt, int box_rows, int *mul_h, int *mul_b);
+// 2-D map (d, rows) of contiguous rows of 16-bit elements, box 64 columns x box_rows.
+bool make_rows_map(void *map, const void *base, long long rows, int d, svga_dtype dt,
+                   int box_rows);
+void *encode_tiled_entry();  // cuTensorMapEncodeTiled, or NULL
+
+// rotary.cu
+svga_status launch_rotary_table(const svga_rotary_spec *spec, double theta, float *table,
+                                void *stream);
+svga_status launch_rotary(const svga_view &src, const svga_view &dst, int batch, int heads,
+                          int tokens, int d, svga_dtype dt, const svga_rotary_spec *spec,
+                          const float *table, const int32_t *positions, long long first_token,
+                          int inverse, int32_t *status, void *stream);
+svga_status launch_append(const svga_view &k, const svga_view &v, int tokens,
+                          const int32_t *new_lens, const svga_paged_cache *cache,
+                          const svga_rotary_spec *spec, const float *table, void *stream);
+
+// decode.cu
+svga_status launch_decode(const svga_view &q, const svga_view &o, float *lse, int q_heads,
+                          const svga_paged_cache *cache, const svga_window_mask *mask,
+                          float scale, void *stream);
+
+svga_status check_launch_of(const char *what);  // cudaGetLastError as a status
+
+inline Mask to_mask(const svga_window_mask &m) { return {m.causal, m.window, m.sinks, m.block}; }
+
+}  // namespace svga

@@ -37,7 +37,9 @@ EXPORTED = ["svga_problem_rows", "svga_block_map_size", "svga_build_block_map",
             "svga_permute_tokens_mapped", "svga_unpermute_tokens_mapped",
             "svga_dense_attention_fwd",
             "svga_classify_size", "svga_classify_heads", "svga_kept_fraction",
-            "svga_autotune_size", "svga_autotune_heads", "svga_last_error",
+            "svga_autotune_size", "svga_autotune_heads",
+            "svga_rotary_table_size", "svga_rotary_table", "svga_rotary",
+            "svga_cache_append", "svga_cache_decode", "svga_last_error",
             "svga_status_string", "svga_version"]
 
 
@@ -64,6 +66,31 @@ class BlockMapC(ctypes.Structure):
                 ("bnd_idx", ctypes.c_void_p), ("full_cap", ctypes.c_int64),
                 ("bnd_cap", ctypes.c_int64), ("plan", ctypes.c_void_p),
                 ("plan_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p)]
+
+
+class View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("stride_token", ctypes.c_int64)]
+
+
+class RotarySpecC(ctypes.Structure):
+    _fields_ = [("num_frames", ctypes.c_int), ("grid_h", ctypes.c_int), ("grid_w", ctypes.c_int),
+                ("pairs", ctypes.c_int * 3), ("interleaved", ctypes.c_int),
+                ("order", ctypes.POINTER(ctypes.c_int32))]
+
+
+class WindowMaskC(ctypes.Structure):
+    _fields_ = [("causal", ctypes.c_int), ("window", ctypes.c_int), ("sinks", ctypes.c_int),
+                ("block", ctypes.c_int)]
+
+
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
 
 
 _lib = None
@@ -105,6 +132,13 @@ def load() -> ctypes.CDLL:
         lib.svga_permute_tokens_mapped.argtypes = [P, P, PP, ctypes.POINTER(BlockMapC), P]
         lib.svga_validate_block_map.argtypes = [PP, ctypes.POINTER(BlockMapC), P]
         lib.svga_unpermute_tokens_mapped.argtypes = [P, P, PP, ctypes.POINTER(BlockMapC), P]
+        PV, PR = ctypes.POINTER(View), ctypes.POINTER(RotarySpecC)
+        PC, PM = ctypes.POINTER(PagedCacheC), ctypes.POINTER(WindowMaskC)
+        lib.svga_rotary_table_size.argtypes = [PR, ctypes.POINTER(SZ)]
+        lib.svga_rotary_table.argtypes = [PR, ctypes.c_double, P, P]
+        lib.svga_rotary.argtypes = [PV, PV, I, I, I, I, I, PR, P, P, ctypes.c_int64, I, P, P]
+        lib.svga_cache_append.argtypes = [PV, PV, I, P, PC, PR, P, P]
+        lib.svga_cache_decode.argtypes = [PV, PV, P, I, PC, PM, F, P]
         lib.svga_last_error.restype = ctypes.c_char_p
         lib.svga_last_error.argtypes = []
         lib.svga_status_string.restype = ctypes.c_char_p
@@ -478,6 +512,216 @@ def svga_unpermute_tokens_mapped(src: torch.Tensor, dst: torch.Tensor, problem: 
     _check(load().svga_unpermute_tokens_mapped(ps, pd, ctypes.byref(problem.c),
                                                ctypes.byref(bmap.c), _stream(stream)))
     return dst
+
+
+# ---- streaming (causal) video attention: strided tensors, bf16 or fp16 ----------------
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class _Strided:
+    """The tensor arguments of one streaming call, checked for what the C ABI cannot see:
+    type, shape, values of a row contiguous, and one CUDA device for all.  Strides and
+    alignment are the library's to check.  Used as a context around the launch it makes
+    that device current, whichever was before."""
+
+    def __init__(self):
+        self.device = None
+        self.seen = []
+
+    def _add(self, t, name, dtype, shape):
+        if not isinstance(t, torch.Tensor):
+            raise SvgaError(1, f"{name} must be a torch.Tensor, got {type(t).__name__}")
+        if t.dtype != dtype:
+            raise SvgaError(1, f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise SvgaError(2, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        self.seen.append((name, t.device))
+
+    def view(self, t, name, dtype, shape) -> View:
+        """[batch, heads, tokens, head_dim]"""
+        self._add(t, name, dtype, shape)
+        sb, sh, st, sd = t.stride()
+        if sd != 1 and t.numel() > 0:
+            raise SvgaError(1, f"{name}: the values of a row must be contiguous")
+        return View(t.data_ptr(), sb, sh, st)
+
+    def flat(self, t, name, dtype, shape, optional=False):
+        """A contiguous array, or NULL where it may be left out."""
+        if t is None and optional:
+            return None
+        self._add(t, name, dtype, shape)
+        if not t.is_contiguous():
+            raise SvgaError(1, f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def done(self):
+        for name, dev in self.seen:
+            if dev.type != "cuda":
+                raise SvgaError(1, f"{name} must be on a CUDA device")
+            if self.device is None:
+                self.device = dev
+            elif dev != self.device:
+                raise SvgaError(1, f"{name} is on {dev}, {self.seen[0][0]} on {self.device}")
+        return self
+
+    def stream(self, stream):
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        if stream.device != self.device:
+            raise SvgaError(1, f"the stream is on {stream.device}, the tensors on {self.device}")
+        return stream.cuda_stream
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.device)
+        return self
+
+    def __exit__(self, *exc):
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.before)
+
+
+def _dtype_of(t, name, dims, f32=False):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise SvgaError(2, f"{name} must be a tensor of {dims} dimensions")
+    if t.dtype not in DTYPES or (t.dtype == torch.float32 and not f32):
+        raise SvgaError(1, f"{name} must be bf16 or fp16{' or fp32' if f32 else ''}, got {t.dtype}")
+    return DTYPES[t.dtype]
+
+
+@dataclass
+class RotarySpec:
+    """Rotary positions on the three axes of a grid (svga_rotary_spec): frames x grid_h x
+    grid_w tokens, pairs = turned pairs of the frame, row and column axis; order = a token
+    order per head, for rotating straight into (or back out of) svga_permute_tokens's
+    layout."""
+    num_frames: int
+    grid_h: int
+    grid_w: int
+    pairs: Sequence[int]
+    interleaved: bool = True
+    order: Optional[Sequence[int]] = None
+
+    def __post_init__(self):
+        self._od = None if self.order is None else (ctypes.c_int32 * len(self.order))(*self.order)
+        self.c = RotarySpecC(self.num_frames, self.grid_h, self.grid_w,
+                             (ctypes.c_int * 3)(*self.pairs), int(self.interleaved), self._od)
+
+    @property
+    def table_shape(self):
+        """(cos, sin) rows of the table: the frame axis, then rows, then columns."""
+        return (self.num_frames * self.pairs[0] + self.grid_h * self.pairs[1] +
+                self.grid_w * self.pairs[2], 2)
+
+
+def svga_rotary_table_size(spec: RotarySpec) -> int:
+    n = ctypes.c_size_t()
+    _check(load().svga_rotary_table_size(ctypes.byref(spec.c), ctypes.byref(n)))
+    return n.value
+
+
+def svga_rotary_table(spec: RotarySpec, theta: float, table: torch.Tensor,
+                      stream=None) -> torch.Tensor:
+    """Fill table (fp32 [rows, 2], rows = spec.table_shape[0]) with the axes' cos and sin."""
+    a = _Strided()
+    pt = a.flat(table, "table", torch.float32, spec.table_shape)
+    with a.done():
+        _check(load().svga_rotary_table(ctypes.byref(spec.c), float(theta), pt, a.stream(stream)))
+    return table
+
+
+def svga_rotary(src, dst, spec: RotarySpec, table, positions=None, first_token: int = 0,
+                inverse: bool = False, status=None, stream=None) -> torch.Tensor:
+    """Rotate src into dst, [batch, heads, tokens, head_dim] each, strided; inverse turns
+    back (the backward pass).  positions: int32 [batch, tokens], or first_token."""
+    dt = _dtype_of(src, "src", 4, f32=True)
+    B, H, T, d = src.shape
+    a = _Strided()
+    vs, vd = a.view(src, "src", src.dtype, src.shape), a.view(dst, "dst", src.dtype, src.shape)
+    pt = a.flat(table, "table", torch.float32, spec.table_shape)
+    pp = a.flat(positions, "positions", torch.int32, (B, T), optional=True)
+    ps = a.flat(status, "status", torch.int32, (1,), optional=True)
+    if spec.order is not None and len(spec.order) != H:
+        raise SvgaError(2, f"order names {len(spec.order)} heads, src has {H}")
+    with a.done():
+        _check(load().svga_rotary(ctypes.byref(vs), ctypes.byref(vd), B, H, T, d, dt,
+                                  ctypes.byref(spec.c), pt, pp, int(first_token), int(inverse),
+                                  ps, a.stream(stream)))
+    return dst
+
+
+@dataclass
+class WindowMask:
+    """The mask of the window calls (svga_window_mask): block = 1 counts the window in
+    tokens, block = grid_h * grid_w in frames; window = -1 is unbounded."""
+    causal: bool = True
+    window: int = -1
+    sinks: int = 0
+    block: int = 1
+
+    def __post_init__(self):
+        self.c = WindowMaskC(int(self.causal), self.window, self.sinks, self.block)
+
+
+def _paged_cache(a: _Strided, k_pages, v_pages, page_table, lens, batch, status):
+    dt = _dtype_of(k_pages, "k_pages", 4)
+    n, heads, page, d = k_pages.shape
+    pk = a.flat(k_pages, "k_pages", k_pages.dtype, k_pages.shape)
+    pv = a.flat(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise SvgaError(2, "page_table must be an int32 tensor [batch, pages a sequence]")
+    most = page_table.shape[1]
+    pt = a.flat(page_table, "page_table", torch.int32, (batch, most))
+    pl = a.flat(lens, "lens", torch.int32, (batch,))
+    ps = a.flat(status, "status", torch.int32, (1,), optional=True)
+    return PagedCacheC(pk, pv, n, heads, page, d, dt, batch, most, pt, pl, ps)
+
+
+def svga_cache_append(k, v, k_pages, v_pages, page_table, lens, new_lens=None,
+                      rotary: Optional[RotarySpec] = None, table=None, status=None,
+                      stream=None) -> None:
+    """Write k and v ([batch, kv_heads, tokens, head_dim], strided) behind each sequence's
+    end; lens counts the new rows already.  With rotary and its table, keys turn on the way."""
+    _dtype_of(k, "k", 4)
+    B, H, T, d = k.shape
+    a = _Strided()
+    c = _paged_cache(a, k_pages, v_pages, page_table, lens, B, status)
+    shape = (B, k_pages.shape[1], T, k_pages.shape[3])
+    vk, vv = a.view(k, "k", k_pages.dtype, shape), a.view(v, "v", k_pages.dtype, shape)
+    pn = a.flat(new_lens, "new_lens", torch.int32, (B,), optional=True)
+    pt = None
+    if rotary is not None:
+        pt = a.flat(table, "table", torch.float32, rotary.table_shape)
+    elif table is not None:
+        raise SvgaError(1, "a table without a RotarySpec")
+    with a.done():
+        _check(load().svga_cache_append(ctypes.byref(vk), ctypes.byref(vv), T, pn,
+                                        ctypes.byref(c),
+                                        None if rotary is None else ctypes.byref(rotary.c), pt,
+                                        a.stream(stream)))
+
+
+def svga_cache_decode(q, k_pages, v_pages, page_table, lens, o, lse, mask: WindowMask,
+                      scale: float, status=None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence over its pages.  q, o: [batch, q_heads,
+    head_dim], strided; lse: fp32 [batch, q_heads] or None."""
+    _dtype_of(q, "q", 3)
+    B, H, d = q.shape
+    a = _Strided()
+    c = _paged_cache(a, k_pages, v_pages, page_table, lens, B, status)
+    shape = (B, H, 1, k_pages.shape[3])
+    if not isinstance(o, torch.Tensor) or o.dim() != 3:
+        raise SvgaError(2, "o must be a tensor of 3 dimensions")
+    vq = a.view(q.unsqueeze(2), "q", k_pages.dtype, shape)
+    vo = a.view(o.unsqueeze(2), "o", k_pages.dtype, shape)
+    pl = a.flat(lse, "lse", torch.float32, (B, H), optional=True)
+    with a.done():
+        _check(load().svga_cache_decode(ctypes.byref(vq), ctypes.byref(vo), pl, H,
+                                        ctypes.byref(c), ctypes.byref(mask.c), float(scale),
+                                        a.stream(stream)))
+    return o
 
 
 def version() -> int:

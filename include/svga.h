@@ -443,6 +443,140 @@ SVGA_API svga_status svga_unpermute_tokens_mapped(const void *src, void *dst,
                                          const svga_problem *problem,
                                          const svga_block_map *map, svga_stream_t stream);
 
+/* ---- Streaming (causal) video attention ------------------------------------------
+ * The calls above attend in both directions over a whole clip.  The calls below are what
+ * a causal generator trains and serves with: rotary positions on three axes, attention
+ * under a causal window with sinks (the mask of a spatial head with its anchor frame,
+ * made causal and cut at any block of tokens) with its gradient, and the same attention
+ * over a paged key-value cache.  Differences from the conventions at the top:
+ *   - element types are bf16 or fp16 (rotary: fp32 too), named by an svga_dtype;
+ *   - tensors are strided views [batch, heads, tokens, head_dim] with head_dim
+ *     contiguous, 16-byte aligned, every stride a multiple of 16 bytes, so the
+ *     [batch, tokens, heads, head_dim] output of a projection needs no copy;
+ *   - a status word (DEVICE int32 or NULL) is not cleared by a call: it keeps the first
+ *     failure found on the device since the caller set it to 0;
+ *   - nothing synchronises and nothing is allocated: every call can be captured. */
+
+typedef enum { SVGA_BF16 = 0, SVGA_F16 = 1, SVGA_F32 = 2 } svga_dtype;
+
+/* Strided view of [batch, heads, tokens, head_dim]; strides in elements.  A stride of 0
+ * (a broadcast dimension) is allowed where the view is only read. */
+typedef struct {
+    void *data;
+    int64_t stride_batch, stride_head, stride_token;
+} svga_view;
+
+/* Rotary positions on the three axes of a video grid.  Token t sits at frame
+ * t / (grid_h*grid_w), row and column likewise.  Axis a (0 frame, 1 row, 2 column) owns
+ * pairs[a] consecutive pairs of a head's values; pair j of the axis turns by the angle
+ * x_a * theta^(-j / pairs[a]):
+ *   y0 = x0 cos - x1 sin,   y1 = x1 cos + x0 sin.
+ * With P = pairs[0] + pairs[1] + pairs[2] <= head_dim / 2, pair i is (2i, 2i + 1) when
+ * interleaved and (i, i + P) otherwise; values 2P and up pass unchanged.
+ *   order: HOST int32 [heads] of SVGA_ORDER_* or NULL.  With it, the rotated side of the
+ *          call is in each head's token order (svga_permute_tokens fused with the
+ *          rotation); the other side is frame-major. */
+typedef struct {
+    int num_frames;
+    int grid_h;
+    int grid_w;
+    int pairs[3];
+    int interleaved;
+    const int32_t *order;
+} svga_rotary_spec;
+
+/* Bytes of the table: fp32 (cos, sin) pairs, num_frames * pairs[0] of the frame axis, then
+ * grid_h * pairs[1], then grid_w * pairs[2], position-major on each axis.  Host-only. */
+SVGA_API svga_status svga_rotary_table_size(const svga_rotary_spec *spec, size_t *bytes);
+
+/* Fill the table (16-byte aligned).  Angles are formed and evaluated in 64 bits and
+ * rounded once, so far positions lose nothing.  theta > 1. */
+SVGA_API svga_status svga_rotary_table(const svga_rotary_spec *spec, double theta, float *table,
+                                       svga_stream_t stream);
+
+/* Rotate src into dst, both [batch, heads, tokens, head_dim] of `dtype` (64 or 128 values
+ * a head), arithmetic in fp32, one rounding.  inverse = 1 turns back, which is also the
+ * backward pass: dst = the gradient of the forward call's src, src = that of its dst.
+ *   positions   : DEVICE int32 [batch][tokens] token indices in the grid, or NULL: token i
+ *                 of every sequence is token first_token + i
+ *   spec->order : needs tokens = num_frames * grid_h * grid_w, positions = NULL and
+ *                 first_token = 0; forward writes dst[b, h, pos(t)] = R src[b, h, t],
+ *                 inverse writes dst[b, h, t] = R^-1 src[b, h, pos(t)]
+ *   status      : SVGA_ERR_INVALID_ARG when a position lies outside the grid; that
+ *                 token's rows are left as they were
+ * src and dst may be the same view (without order); otherwise their extents must not
+ * overlap. */
+SVGA_API svga_status svga_rotary(const svga_view *src, const svga_view *dst, int batch, int heads,
+                                 int tokens, int head_dim, svga_dtype dtype,
+                                 const svga_rotary_spec *spec, const float *table,
+                                 const int32_t *positions, int64_t first_token, int inverse,
+                                 int32_t *status, svga_stream_t stream);
+
+/* The mask of the window calls.  A sequence has nq queries and nk keys; query i sits at
+ * position p = i + nk - nq (queries end where the keys end).  With b(x) = floor(x / block):
+ *   key j is kept  iff  (causal = 0 or b(j) <= b(p)) and
+ *                       (window < 0 or |b(p) - b(j)| <= window or j < sinks).
+ * block = 1 is the usual token-causal window; block = grid_h * grid_w is frame-causal,
+ * every token seeing its own frame whole.  window counts blocks and is inclusive, like
+ * band; sinks counts tokens that stay visible.  A query at a negative position (more
+ * queries than keys) may keep nothing: its O is 0 and its lse -inf. */
+typedef struct {
+    int causal; /* 0 or 1 */
+    int window; /* -1: unbounded; else 0 .. 2^24 blocks */
+    int sinks;  /* 0 .. 2^24 tokens */
+    int block;  /* 1 .. 2^24 tokens */
+} svga_window_mask;
+
+/* A paged key-value cache: k_pages and v_pages are contiguous
+ * [pages, kv_heads, page_size, head_dim] of bf16 or fp16; position x of sequence b lives in
+ * page page_table[b][x / page_size], row x % page_size.
+ *   page_size  : a multiple of 16, 16 .. 1024;  head_dim 64 or 128
+ *   page_table : DEVICE int32 [batch][max_pages]; entries past a sequence's length are
+ *                not read
+ *   lens       : DEVICE int32 [batch], each sequence's length (0 .. max_pages * page_size)
+ *   status     : SVGA_ERR_INVALID_ARG when a length, or a page a length needs, is out of
+ *                range: svga_cache_append leaves such a row unwritten, svga_cache_decode
+ *                treats a length out of range as 0 and a page's keys as masked. */
+typedef struct {
+    void *k_pages;
+    void *v_pages;
+    int pages;
+    int kv_heads;
+    int page_size;
+    int head_dim;
+    svga_dtype dtype;
+    int batch;
+    int max_pages;
+    const int32_t *page_table;
+    const int32_t *lens;
+    int32_t *status;
+} svga_paged_cache;
+
+/* Write new rows of k and v ([batch, kv_heads, tokens, head_dim]) to the end of each
+ * sequence: cache->lens are the lengths AFTER the append, row i of sequence b goes to
+ * position lens[b] - n + i with n = new_lens[b] (DEVICE int32 [batch], 0 .. tokens) or
+ * `tokens` when new_lens is NULL; rows n and up are not read.  With spec and table
+ * (spec->order NULL) keys are rotated at their position on the way, as svga_rotary does;
+ * both NULL: copied.  Two sequences must not append to one page (a page shared by a fork
+ * is copied first); the same row written twice holds one of the two. */
+SVGA_API svga_status svga_cache_append(const svga_view *k, const svga_view *v, int tokens,
+                                       const int32_t *new_lens, const svga_paged_cache *cache,
+                                       const svga_rotary_spec *spec, const float *table,
+                                       svga_stream_t stream);
+
+/* Attention of one new token per sequence over the cache: the row
+ * svga_window_attention_fwd gives for its last query (position lens[b] - 1; the mask's
+ * causal flag changes nothing there).  q, o: [batch, q_heads, head_dim] of the cache's
+ * type, q_heads a multiple of kv_heads; strides of batch and head as in svga_view
+ * (stride_token is not read).  lse: fp32 contiguous [batch, q_heads] or NULL.  An empty
+ * sequence gives O = 0 and lse = -inf.  Rows of a page past the length are read but change
+ * nothing, NaN included.  One launch, no workspace: the CTAs of a cluster split the keys
+ * and join over distributed shared memory, in a fixed order. */
+SVGA_API svga_status svga_cache_decode(const svga_view *q, const svga_view *o, float *lse,
+                                       int q_heads, const svga_paged_cache *cache,
+                                       const svga_window_mask *mask, float scale,
+                                       svga_stream_t stream);
+
 /* Message of the last failed call on this thread ("" if none). */
 SVGA_API const char *svga_last_error(void);
 
