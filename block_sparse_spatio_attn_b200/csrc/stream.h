@@ -111,6 +111,13 @@ struct View {
     long long sb, sh, st;
 };
 
+struct WindowShape {
+    int batch, hq, hk, group, tq, tk;
+    Mask mask;
+    const int32_t *q_lens, *k_lens;
+    int32_t *status;
+};
+
 // tensor_map.cu: 4-D map (d, token, head, batch) of a strided view of 16-bit elements, box
 // 64 columns x box_rows tokens, 128-byte swizzle.  A broadcast (stride 0) or one-entry
 // dimension is mapped with extent 1: coordinates in it are multiplied by *mul_h / *mul_b
@@ -138,8 +145,29 @@ svga_status launch_decode(const svga_view &q, const svga_view &o, float *lse, in
                           const svga_paged_cache *cache, const svga_window_mask *mask,
                           float scale, void *stream);
 
+// window_fwd.cu, window_bwd.cu
+size_t window_fwd_workspace(const svga_window_problem *p);
+size_t window_bwd_workspace(const svga_window_problem *p);
+svga_status launch_window_fwd(const svga_view &q, const svga_view &k, const svga_view &v,
+                              const svga_view &o, float *lse, const svga_window_problem *p,
+                              float scale, void *ws, void *stream);
+svga_status launch_window_bwd(const svga_view &d_o, const svga_view &q, const svga_view &k,
+                              const svga_view &v, const svga_view &o, const float *lse,
+                              const svga_view &dq, const svga_view &dk, const svga_view &dv,
+                              const svga_window_problem *p, float scale, void *ws, void *stream);
+
 svga_status check_launch_of(const char *what);  // cudaGetLastError as a status
 
-inline Mask to_mask(const svga_window_mask &m) { return {m.causal, m.window, m.sinks, m.block}; }
+inline Mask to_mask(const svga_window_mask &m)
+{
+    return {m.causal, m.window, m.sinks, m.block};
+}
+
+inline WindowShape to_shape(const svga_window_problem *p)
+{
+    return {p->batch,  p->q_heads,  p->kv_heads,      p->q_heads / p->kv_heads,
+            p->q_tokens, p->k_tokens, to_mask(p->mask), p->q_lens,
+            p->k_lens, p->status};
+}
 
 }  // namespace svga

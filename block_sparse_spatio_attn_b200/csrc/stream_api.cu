@@ -124,6 +124,50 @@ svga_status check_mask(const svga_window_mask *m)
     return SVGA_OK;
 }
 
+svga_status check_window(const svga_window_problem *p)
+{
+    if (!p) return bad(SVGA_ERR_INVALID_ARG, "%sproblem is NULL");
+    svga_status rc;
+    if (p->batch < 0 || p->batch > 65535 || p->q_heads < 1 || p->kv_heads < 1 ||
+        p->q_heads > kMaxHeads || p->q_heads % p->kv_heads != 0) {
+        set_error("batch %d (0 .. 65535), q_heads %d (1 .. %d) or kv_heads %d (a divisor of q_heads) "
+                  "out of range",
+                  p->batch, p->q_heads, kMaxHeads, p->kv_heads);
+        return SVGA_ERR_SHAPE;
+    }
+    if (p->q_tokens < 0 || p->k_tokens < 0 || p->q_tokens > kMaxTokens ||
+        p->k_tokens > kMaxTokens) {
+        set_error("q_tokens %d or k_tokens %d outside 0 .. %d", p->q_tokens, p->k_tokens,
+                  kMaxTokens);
+        return SVGA_ERR_SHAPE;
+    }
+    if ((rc = check_head_dim(p->head_dim)) != SVGA_OK ||
+        (rc = check_dtype(p->dtype, false)) != SVGA_OK || (rc = check_mask(&p->mask)) != SVGA_OK ||
+        (rc = check_word(p->q_lens, "q_lens")) != SVGA_OK ||
+        (rc = check_word(p->k_lens, "k_lens")) != SVGA_OK ||
+        (rc = check_word(p->status, "status")) != SVGA_OK)
+        return rc;
+    const long long blocks = (long long)p->batch * p->q_heads *
+                             ((std::max(p->q_tokens, p->k_tokens) + 127) / 128);
+    if (blocks > 0x7fffffffll / 64) {
+        set_error("%lld 128-row blocks (batch x heads x tokens) do not fit one launch", blocks);
+        return SVGA_ERR_SHAPE;
+    }
+    return SVGA_OK;
+}
+
+svga_status check_workspace(const void *ws, size_t have, size_t need)
+{
+    if (need == 0) return SVGA_OK;
+    if (!ws || !aligned(ws, 256) || have < need) {
+        set_error("workspace missing, not 256-byte aligned or smaller than the %zu bytes "
+                  "svga_window_attention_size says",
+                  need);
+        return SVGA_ERR_WORKSPACE;
+    }
+    return SVGA_OK;
+}
+
 svga_status check_spec(const svga_rotary_spec *s, int head_dim)
 {
     if (!s) return bad(SVGA_ERR_INVALID_ARG, "%sspec is NULL");
@@ -280,6 +324,66 @@ svga_status svga_rotary(const svga_view *src, const svga_view *dst, int batch, i
     }
     return launch_rotary(*src, *dst, batch, heads, tokens, head_dim, dtype, spec, table, positions,
                          first_token, inverse, status, stream);
+}
+
+svga_status svga_window_attention_size(const svga_window_problem *problem, size_t *fwd_bytes,
+                                       size_t *bwd_bytes)
+{
+    const svga_status rc = check_window(problem);
+    if (rc != SVGA_OK) return rc;
+    if (fwd_bytes) *fwd_bytes = window_fwd_workspace(problem);
+    if (bwd_bytes) *bwd_bytes = window_bwd_workspace(problem);
+    return SVGA_OK;
+}
+
+svga_status svga_window_attention_fwd(const svga_view *q, const svga_view *k, const svga_view *v,
+                                      const svga_view *o, float *lse,
+                                      const svga_window_problem *p, float scale, void *workspace,
+                                      size_t workspace_bytes, svga_stream_t stream)
+{
+    svga_status rc;
+    if ((rc = check_window(p)) != SVGA_OK || (rc = check_scale(scale)) != SVGA_OK) return rc;
+    const int B = p->batch, H = p->q_heads, G = p->kv_heads, d = p->head_dim;
+    if ((rc = check_view(q, "q", B, H, p->q_tokens, d, p->dtype, false)) != SVGA_OK ||
+        (rc = check_view(k, "k", B, G, p->k_tokens, d, p->dtype, false)) != SVGA_OK ||
+        (rc = check_view(v, "v", B, G, p->k_tokens, d, p->dtype, false)) != SVGA_OK ||
+        (rc = check_view(o, "o", B, H, p->q_tokens, d, p->dtype, true)) != SVGA_OK)
+        return rc;
+    if (lse && !aligned(lse, 4)) return bad(SVGA_ERR_ALIGNMENT, "%slse is not 4-byte aligned");
+    if ((rc = check_workspace(workspace, workspace_bytes, window_fwd_workspace(p))) != SVGA_OK)
+        return rc;
+    if (B == 0 || p->q_tokens == 0) return SVGA_OK;
+    return launch_window_fwd(*q, *k, *v, *o, lse, p, scale, workspace, stream);
+}
+
+svga_status svga_window_attention_bwd(const svga_view *d_o, const svga_view *q, const svga_view *k,
+                                      const svga_view *v, const svga_view *o, const float *lse,
+                                      const svga_view *dq, const svga_view *dk,
+                                      const svga_view *dv, const svga_window_problem *p,
+                                      float scale, void *workspace, size_t workspace_bytes,
+                                      svga_stream_t stream)
+{
+    svga_status rc;
+    if ((rc = check_window(p)) != SVGA_OK || (rc = check_scale(scale)) != SVGA_OK) return rc;
+    const int B = p->batch, H = p->q_heads, G = p->kv_heads, d = p->head_dim;
+    const struct {
+        const svga_view *v;
+        const char *name;
+        int heads, tokens;
+        bool write;
+    } views[] = {{d_o, "d_o", H, p->q_tokens, false}, {q, "q", H, p->q_tokens, false},
+                 {k, "k", G, p->k_tokens, false},     {v, "v", G, p->k_tokens, false},
+                 {o, "o", H, p->q_tokens, false},     {dq, "dq", H, p->q_tokens, true},
+                 {dk, "dk", G, p->k_tokens, true},    {dv, "dv", G, p->k_tokens, true}};
+    for (const auto &x : views)
+        if ((rc = check_view(x.v, x.name, B, x.heads, x.tokens, d, p->dtype, x.write)) != SVGA_OK)
+            return rc;
+    if (B > 0 && p->q_tokens > 0 && !lse) return bad(SVGA_ERR_INVALID_ARG, "%slse is NULL");
+    if (!aligned(lse, 4)) return bad(SVGA_ERR_ALIGNMENT, "%slse is not 4-byte aligned");
+    if ((rc = check_workspace(workspace, workspace_bytes, window_bwd_workspace(p))) != SVGA_OK)
+        return rc;
+    if (B == 0 || (p->q_tokens == 0 && p->k_tokens == 0)) return SVGA_OK;
+    return launch_window_bwd(*d_o, *q, *k, *v, *o, lse, *dq, *dk, *dv, p, scale, workspace, stream);
 }
 
 svga_status svga_cache_append(const svga_view *k, const svga_view *v, int tokens,

@@ -1,0 +1,875 @@
+// window_bwd.cu -- attention under a causal window with sinks, backward (sm_100a).
+//
+// With P = exp(scale Q K^T - lse) on the kept pairs and D = rowsum(dO o O):
+//   dV = P^T dO,   dS = P o (dO V^T - D),   dQ = scale dS K,   dK = scale dS^T Q.
+//
+// Three kernels:
+//   rows    D and lse of every query row in the exp2 domain, negated, 1 KB per 128 rows;
+//   dkdv    one CTA per 128 keys of a key head; walks the query blocks that keep any of
+//           them, over all query heads of the group, with dK and dV in TMEM throughout, so
+//           shared heads are summed without atomics and the order is fixed;
+//   dq      one CTA per 128 queries; walks their key chunks with dQ in TMEM.
+// S and dO V^T are computed in both: 7 products instead of the 5 a single pass needs.  The
+// single pass would add each dQ tile into memory from every CTA: 64 KB of fp32 atomics a
+// tile pair, more than L2 takes at this rate, in an order that changes the bits.
+//
+// dkdv works on transposed tiles, S^T = K Q^T and dP^T = V dO^T (TMEM lane = key), so that P^T
+// and dS^T are in place as the A operands of dV += P^T dO and dK += dS^T Q: nothing is
+// transposed through shared memory.  TMEM: S^T | dP^T | dV | dK, 128 columns each; P^T and
+// dS^T are written over the first half of what each softmax group read of S^T and dP^T.  All
+// four products are issued by one thread in the order
+//   ... dV(i), S(i+1), dK(i), dP(i+1), ...
+// so while the softmax threads turn S(i+1) into P(i+1) the tensor pipe runs dK(i) and
+// dP(i+1), and while they turn dP(i+1) into dS(i+1) it runs dV(i+1) and S(i+2).
+// dq has room for two S tiles (S0 | S1 | dP | dQ): S runs a chunk ahead.
+// In both, warps 4-7 and 8-11 hold a lane's columns 0-63 and 64-127; P stays in registers
+// in fp32 between the two steps of a tile.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "stream.h"
+#include "svga_device.cuh"
+
+namespace svga {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kT = 128;  // rows and keys of a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kNegInfBits = 0xff800000u;
+constexpr int kRegsLaunch = 168, kRegsLow = 96, kRegsHigh = 200;
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "register split");
+
+struct BwdParams {
+    WindowShape s;
+    View d_o, o, dq, dk, dv;
+    const float *lse;
+    float *stats;  // [batch * hq][query block][2][128]: -lse log2(e), -D
+    float scale, scale_log2;
+    int n_qblk, n_kblk, d;
+    int q_mb, q_mh, o_mb, o_mh, k_mb, k_mh, v_mb, v_mh;  // coordinate multipliers (o: dO)
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int kTile = kT * D * 2;   // a 128-row tile of Q, K, V or dO
+    static constexpr int kChunk = kT * 128;    // 64 columns of it
+    static constexpr int kStats = 2 * kT * 4;  // a query block's statistics
+    // dkdv: K, V, two stages of Q and dO with their statistics
+    static constexpr int kKvStages = 2;
+    static constexpr int kKvData = 2 * kTile + kKvStages * (2 * kTile + kStats);
+    // dq: Q, dO, three stages of K, two of V
+    static constexpr int kKStages = 3, kVStages = 2;
+    static constexpr int kDqData = (2 + kKStages + kVStages) * kTile;
+    static constexpr int kBars = 512;
+    // one CTA per SM (each takes the whole TMEM): never less than half the shared memory
+    static constexpr int alloc(int data)
+    {
+        return data + kBars + 1024 < 120 * 1024 ? 120 * 1024 : data + kBars + 1024;
+    }
+    static constexpr int kKvAlloc = alloc(kKvData), kDqAlloc = alloc(kDqData);
+    static_assert(kKvAlloc <= 227 * 1024 && kDqAlloc <= 227 * 1024, "shared memory budget");
+};
+
+__device__ __forceinline__ int clamped_len(const int32_t *lens, int b, int most)
+{
+    return lens ? min(max(__ldg(lens + b), 0), most) : most;
+}
+
+__device__ __forceinline__ uint32_t bits_below(int n)
+{
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack_16x2(uint32_t x)
+{
+    if constexpr (F16) {
+        const __half2 h = *reinterpret_cast<const __half2 *>(&x);
+        return __half22float2(h);
+    } else {
+        return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    }
+}
+
+// 64 columns of a TMEM tile into registers
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
+{
+    tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+    tmem_ld32(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+}
+
+// ----------------------------------------------------------------------------- rows
+// D / 8 threads a row.  Bound by HBM: dO and O are read once.  Rows past the sequence's
+// end get -inf and 0: their P and dS are 0.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) bwd_rows_kernel(const BwdParams p)
+{
+    constexpr int kPer = D / 8;
+    const long long i = blockIdx.x * 256ll + threadIdx.x;
+    const long long row = i / kPer, bh = row / (p.n_qblk * kT);
+    if (bh >= (long long)p.s.batch * p.s.hq) return;
+    const int b = (int)(bh / p.s.hq), h = (int)(bh - (long long)b * p.s.hq);
+    const int t = (int)(row - bh * p.n_qblk * kT), c = 8 * (int)(i % kPer);
+    const bool there = t < clamped_len(p.s.q_lens, b, p.s.tq);
+    float sum = 0.f;
+    if (there) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(
+            p.d_o.p + 2 * (b * p.d_o.sb + h * p.d_o.sh + t * p.d_o.st + c));
+        const uint4 y = *reinterpret_cast<const uint4 *>(
+            p.o.p + 2 * (b * p.o.sb + h * p.o.sh + t * p.o.st + c));
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 u = unpack_16x2<F16>(xs[k]), v = unpack_16x2<F16>(ys[k]);
+            sum += u.x * v.x + u.y * v.y;
+        }
+    }
+#pragma unroll
+    for (int k = kPer / 2; k > 0; k /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (c != 0) return;
+    const float lse = there ? __ldg(p.lse + bh * p.s.tq + t) : -INFINITY;
+    float *out = p.stats + ((bh * p.n_qblk + t / kT) * 2) * kT + t % kT;
+    out[0] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // an empty row keeps nothing
+    out[kT] = -sum;
+}
+
+// Writes NCOL fp32 columns of a TMEM row times `f` as 16-bit values; NULL dst: only loads.
+template <int NCOL, bool F16>
+__device__ __forceinline__ void store_row(uint32_t taddr, char *dst, float f, bool any)
+{
+#pragma unroll 1
+    for (int j = 0; j < NCOL / 32; ++j) {
+        uint32_t o[32];
+        if (any) {
+            tmem_ld32(taddr + j * 32, o);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = 0u;
+        }
+        if (!dst) continue;
+        uint4 *to = reinterpret_cast<uint4 *>(dst + 64 * j);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = pack_16x2<F16>(__uint_as_float(o[8 * c + 2 * i]) * f,
+                                      __uint_as_float(o[8 * c + 2 * i + 1]) * f);
+            to[c] = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+    }
+}
+
+// Rows [first, 128) of a swizzled 128-row tile read as 0 (whole rows: the swizzle permutes
+// inside a row's 128 bytes).
+template <int D>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane)
+{
+    for (int u = first * 8 + lane; u < kT * 8; u += 32)
+        for (int c = 0; c < D / 64; ++c)
+            st_shared_v4(tile + c * Cfg<D>::kChunk + u * 16, 0u, 0u, 0u, 0u);
+}
+
+// One product of a 128 x N tile over 128 (A in TMEM) or D (A in shared memory) terms.
+template <int D>
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id)
+{
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t at = ((kk >> 2) * Cfg<D>::kChunk + (kk & 3) * 32) >> 4;
+        mma_ss(d, a + at, b + at, id, kk > 0 ? 1u : 0u);
+    }
+}
+
+// A: 128 terms as packed 16-bit pairs, terms 0-63 in columns a .. a + 31, 64-127 in a + 64 ..
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                           bool accumulate)
+{
+#pragma unroll
+    for (int kk = 0; kk < kT / 16; ++kk)
+        mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + (uint32_t)(kk * (2048 >> 4)), id,
+               (accumulate || kk > 0) ? 1u : 0u);
+}
+
+// ----------------------------------------------------------------------------- dkdv
+struct KvBars {
+    uint64_t kv_full;
+    uint64_t q_full[2], q_empty[2];  // stages of Q, dO and their statistics
+    uint64_t s_full, dp_full;        // S^T / dP^T of a step is in TMEM
+    uint64_t p_ready, ds_ready;      // P^T / dS^T is (8 warps)
+    uint64_t acc_done;               // every product is done
+    uint64_t drain;
+    uint64_t zero_req, zero_done;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(KvBars) <= 512, "barrier space");
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const BwdParams p)
+{
+    using C = Cfg<D>;
+    constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    uint8_t *sK = smem, *sV = smem + C::kTile;
+    uint8_t *sQ = smem + 2 * C::kTile;                       // [stage]
+    uint8_t *sO = sQ + C::kKvStages * C::kTile;              // [stage]
+    uint8_t *sStats = sO + C::kKvStages * C::kTile;          // [stage]
+    KvBars *bar = reinterpret_cast<KvBars *>(smem + C::kKvData);
+    volatile int *abort_flag = &bar->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // this CTA's keys, and the query blocks that keep any of them
+    const int bh = p.s.batch * p.s.hk;
+    const int kblk = blockIdx.x / bh, r = blockIdx.x - kblk * bh;
+    const int b = r / p.s.hk, hk = r - b * p.s.hk;
+    const int nq = clamped_len(p.s.q_lens, b, p.s.tq), nk = clamped_len(p.s.k_lens, b, p.s.tk);
+    const int k0 = kblk * kT, k1 = min(k0 + kT, nk), off = nk - nq;
+    if (k0 >= nk) return;
+    int first, end, x, end1;
+    mask_rows(p.s.mask, k0, nq, off, first, end);  // a sink among the keys is the first one
+    mask_rows(p.s.mask, k1 - 1, nq, off, x, end1);
+    end = max(end, end1);
+    const int qb0 = first / kT, n_blk = end > first ? (end + kT - 1) / kT - qb0 : 0;
+    const int steps = n_blk * p.s.group;
+    // the query block whose last rows lie past the sequence's end but inside the tensor
+    const int ragged =
+        (p.s.q_lens && nq < p.s.tq && nq % kT && nq / kT == qb0 + n_blk - 1) ? n_blk - 1 : -1;
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar->kv_full), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar->q_full[i]), 1);
+            mbar_init(smem_u32(&bar->q_empty[i]), 1);
+        }
+        mbar_init(smem_u32(&bar->s_full), 1);
+        mbar_init(smem_u32(&bar->dp_full), 1);
+        mbar_init(smem_u32(&bar->p_ready), 8);
+        mbar_init(smem_u32(&bar->ds_ready), 8);
+        mbar_init(smem_u32(&bar->acc_done), 1);
+        mbar_init(smem_u32(&bar->drain), 1);
+        mbar_init(smem_u32(&bar->zero_req), 1);
+        mbar_init(smem_u32(&bar->zero_done), 1);
+        bar->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bar->tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem_base;
+
+    if (warp < 4) {
+        setmaxnreg_dec<kRegsLow>();
+        if (warp == 0 && lane == 0 && steps > 0) {
+            // -------------------------------------------------------- TMA producer
+            const uint32_t kvf = smem_u32(&bar->kv_full);
+            mbar_arrive_expect_tx(kvf, 2 * C::kTile);
+            for (int c = 0; c < D / 64; ++c) {
+                tma_load_4d(smem_u32(sK + c * C::kChunk), &tmK, kvf, 64 * c, k0, hk * p.k_mh,
+                            b * p.k_mb);
+                tma_load_4d(smem_u32(sV + c * C::kChunk), &tmV, kvf, 64 * c, k0, hk * p.v_mh,
+                            b * p.v_mb);
+            }
+            int issued = 0, g = 0, blk = 0;
+            for (int i = 0; i < steps; ++i) {
+                const int s = i & 1, round = i >> 1;
+                if (round > 0 &&
+                    !mbar_wait(smem_u32(&bar->q_empty[s]), (round - 1) & 1, abort_flag))
+                    break;
+                const uint32_t fb = smem_u32(&bar->q_full[s]);
+                const int h = hk * p.s.group + g, row = (qb0 + blk) * kT;
+                mbar_arrive_expect_tx(fb, 2 * C::kTile + C::kStats);
+                for (int c = 0; c < D / 64; ++c) {
+                    tma_load_4d(smem_u32(sQ + s * C::kTile + c * C::kChunk), &tmQ, fb, 64 * c, row,
+                                h * p.q_mh, b * p.q_mb);
+                    tma_load_4d(smem_u32(sO + s * C::kTile + c * C::kChunk), &tmO, fb, 64 * c, row,
+                                h * p.o_mh, b * p.o_mb);
+                }
+                bulk_load(smem_u32(sStats + s * C::kStats),
+                          p.stats + (((long long)b * p.s.hq + h) * p.n_qblk + qb0 + blk) * 2 * kT,
+                          C::kStats, fb);
+                issued = i + 1;
+                if (++blk == n_blk) {
+                    blk = 0;
+                    ++g;
+                }
+            }
+            // every copy lands before the CTA can exit, whichever role aborts
+            mbar_wait_bounded(kvf, 0);
+            for (int i = max(issued - 2, 0); i < issued; ++i)
+                mbar_wait_bounded(smem_u32(&bar->q_full[i & 1]), (i >> 1) & 1);
+        } else if (warp == 1 && lane == 0 && steps > 0) {
+            // ---------------------------------------------------------- MMA issuer
+            constexpr uint32_t idS = idesc_16_f32(F16, kT, kT, 0, 0);
+            constexpr uint32_t idA = idesc_16_f32(F16, kT, D, 0, 1);
+            const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);         // rows of terms
+            const uint64_t nmaj = smem_desc_sw128(0, C::kChunk, 1024);  // terms down the rows
+            const uint32_t aK = smem_u32(sK) >> 4, aV = smem_u32(sV) >> 4;
+            const uint32_t aQ = smem_u32(sQ) >> 4, aO = smem_u32(sO) >> 4;
+            int blk = 0;  // block of the next step whose stage is taken in
+            auto take = [&](int i) {  // stage of step i has landed and is clean
+                bool ok = mbar_wait(smem_u32(&bar->q_full[i & 1]), (i >> 1) & 1, abort_flag);
+                if (ok && blk == ragged) {  // warp 2 clears the rows past the end
+                    const int time = i / n_blk;
+                    mbar_arrive(smem_u32(&bar->zero_req));
+                    ok = mbar_wait(smem_u32(&bar->zero_done), time & 1, abort_flag);
+                }
+                if (++blk == n_blk) blk = 0;
+                return ok;
+            };
+            auto issue_s = [&](int i) {
+                product_ss<D>(tmem + kS, kmaj + aK, kmaj + aQ + (i & 1) * (C::kTile >> 4), idS);
+                mma_commit(smem_u32(&bar->s_full));
+            };
+            auto issue_dp = [&](int i) {
+                product_ss<D>(tmem + kDP, kmaj + aV, kmaj + aO + (i & 1) * (C::kTile >> 4), idS);
+                mma_commit(smem_u32(&bar->dp_full));
+            };
+            bool ok = mbar_wait(smem_u32(&bar->kv_full), 0, abort_flag) && take(0);
+            if (ok) {
+                issue_s(0);
+                issue_dp(0);
+            }
+            for (int i = 0; ok && i < steps; ++i) {
+                const uint32_t st = (i & 1) * (C::kTile >> 4);
+                if (!(ok = mbar_wait(smem_u32(&bar->p_ready), i & 1, abort_flag))) break;
+                tc_fence_after();
+                product_ts(tmem + kDV, tmem + kS, nmaj + aO + st, idA, i > 0);
+                if (i + 1 < steps) {
+                    if (!(ok = take(i + 1))) break;
+                    issue_s(i + 1);
+                }
+                if (!(ok = mbar_wait(smem_u32(&bar->ds_ready), i & 1, abort_flag))) break;
+                tc_fence_after();
+                product_ts(tmem + kDK, tmem + kDP, nmaj + aQ + st, idA, i > 0);
+                mma_commit(smem_u32(&bar->q_empty[i & 1]));
+                if (i + 1 < steps) issue_dp(i + 1);
+            }
+            if (ok) {
+                mma_commit(smem_u32(&bar->acc_done));
+            } else {
+                mma_commit(smem_u32(&bar->drain));
+                mbar_wait_bounded(smem_u32(&bar->drain), 0);
+            }
+        } else if (warp == 2 && ragged >= 0) {
+            // ------------------------ rows of Q and dO past the sequence's end read as 0
+            for (int g = 0; g < p.s.group; ++g) {
+                const bool ok = mbar_wait(smem_u32(&bar->zero_req), g & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                const int s = (g * n_blk + ragged) & 1;
+                zero_rows<D>(smem_u32(sQ + s * C::kTile), nq % kT, lane);
+                zero_rows<D>(smem_u32(sO + s * C::kTile), nq % kT, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar->zero_done));
+            }
+        }
+    } else {
+        // ------------------------------------------------------ softmax warpgroups
+        setmaxnreg_inc<kRegsHigh>();
+        const int wg = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t tS = tmem + lane_base + kS + 64 * wg;
+        const uint32_t tDP = tmem + lane_base + kDP + 64 * wg;
+        const int key = k0 + row;
+        int ra = 0, re = 0;  // the queries that keep this lane's key
+        if (key < nk) mask_rows(p.s.mask, key, nq, off, ra, re);
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+        bool ok = true;
+        int blk = 0;
+        for (int i = 0; i < steps; ++i) {
+            const int r0 = (qb0 + blk) * kT;
+            if (++blk == n_blk) blk = 0;
+            const MaskRange m0 = mask_range(p.s.mask, r0 + off, nk);
+            const MaskRange m1 = mask_range(p.s.mask, min(r0 + kT, nq) - 1 + off, nk);
+            const bool full = ((m1.lo <= k0 || m1.lo <= m0.sk) && k1 <= m0.hi) || k1 <= m0.sk;
+            // kept columns of this thread's half: [c0, c1)
+            const int c0 = ra - r0 - 64 * wg, c1 = re - r0 - 64 * wg;
+            uint32_t keep[2] = {bits_below(c1) & ~bits_below(c0),
+                                bits_below(c1 - 32) & ~bits_below(c0 - 32)};
+            const float4 *nl = reinterpret_cast<const float4 *>(sStats + (i & 1) * C::kStats) +
+                               16 * wg;
+            uint32_t x[64];
+            float pr[64];
+            // the statistics are read here: this thread waits for their copy itself (it has
+            // landed, the issuer waited for it before S)
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(smem_u32(&bar->s_full), i & 1, abort_flag) &&
+                                mbar_wait(smem_u32(&bar->q_full[i & 1]), (i >> 1) & 1, abort_flag));
+            tc_fence_after();
+            if (!ok) break;
+            tmem_ld64(tS, x);
+            tmem_wait_ld();
+            if (!full) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (!((keep[c >> 5] >> (c & 31)) & 1u)) x[c] = kNegInfBits;
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+                const float4 n = nl[c >> 2];
+                const float2 u = ffma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                                       sc2, make_float2(n.x, n.y));
+                const float2 v =
+                    ffma2(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc2,
+                          make_float2(n.z, n.w));
+                pr[c] = fast_exp2(u.x);
+                pr[c + 1] = fast_exp2(u.y);
+                pr[c + 2] = fast_exp2(v.x);
+                pr[c + 3] = fast_exp2(v.y);
+            }
+            {
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) pk[c] = pack_16x2<F16>(pr[2 * c], pr[2 * c + 1]);
+                tmem_st32(tS, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar->p_ready));
+
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->dp_full), i & 1, abort_flag));
+            tc_fence_after();
+            if (!ok) break;
+            tmem_ld64(tDP, x);
+            tmem_wait_ld();
+            {
+                const float4 *nd = nl + kT / 4;
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 64; c += 4) {
+                    const float4 n = nd[c >> 2];
+                    float2 u = fadd2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                                     make_float2(n.x, n.y));
+                    float2 v = fadd2(
+                        make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
+                        make_float2(n.z, n.w));
+                    u = ffma2(u, make_float2(pr[c], pr[c + 1]), make_float2(0.f, 0.f));
+                    v = ffma2(v, make_float2(pr[c + 2], pr[c + 3]), make_float2(0.f, 0.f));
+                    pk[c / 2] = pack_16x2<F16>(u.x, u.y);
+                    pk[c / 2 + 1] = pack_16x2<F16>(v.x, v.y);
+                }
+                if (!full) {  // 0 also where a dropped pair's product is not finite
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const uint32_t k2 = keep[c >> 4] >> (2 * (c & 15));
+                        pk[c] &= ((k2 & 1u) ? 0xffffu : 0u) | ((k2 & 2u) ? 0xffff0000u : 0u);
+                    }
+                }
+                tmem_st32(tDP, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar->ds_ready));
+        }
+        // ------------------------------- epilogue: group 0 stores dV, group 1 dK
+        if (ok && steps > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->acc_done), 0, abort_flag));
+            tc_fence_after();
+        }
+        if (ok) {
+            const View &w = wg ? p.dk : p.dv;
+            char *dst = key < nk ? w.p + 2 * (b * w.sb + hk * w.sh + key * w.st) : nullptr;
+            store_row<D, F16>(tmem + lane_base + (wg ? kDK : kDV), dst, wg ? p.scale : 1.f,
+                              steps > 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && bar->abort && p.s.status)
+        atomicExch(p.s.status, (int32_t)SVGA_ERR_TIMEOUT);
+}
+
+// ------------------------------------------------------------------------------- dq
+struct DqBars {
+    uint64_t q_full;
+    uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+    uint64_t s_full[2], dp_full;  // S of a step (two tiles), dP
+    uint64_t ds_ready;            // dS (8 warps); implies S and dP were read
+    uint64_t acc_done, drain;
+    uint64_t zero_req, zero_done;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(DqBars) <= 512, "barrier space");
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const BwdParams p)
+{
+    using C = Cfg<D>;
+    constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    uint8_t *sQ = smem, *sO = smem + C::kTile;
+    uint8_t *sK = smem + 2 * C::kTile;               // [stage]
+    uint8_t *sV = sK + C::kKStages * C::kTile;       // [stage]
+    DqBars *bar = reinterpret_cast<DqBars *>(smem + C::kDqData);
+    volatile int *abort_flag = &bar->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // this CTA's queries (last blocks first: the longest under a causal mask) and their keys
+    const int bhq = p.s.batch * p.s.hq;
+    const int slot = blockIdx.x / bhq, r = blockIdx.x - slot * bhq;
+    const int b = r / p.s.hq, h = r - b * p.s.hq, hk = h / p.s.group;
+    const int blk = p.n_qblk - 1 - slot, r0 = blk * kT;
+    const int nq = clamped_len(p.s.q_lens, b, p.s.tq), nk = clamped_len(p.s.k_lens, b, p.s.tk);
+    const int off = nk - nq;
+    if (r0 >= nq) return;
+    const ChunkList cl =
+        chunk_list<kT>(p.s.mask, r0 + off, min(r0 + kT, nq) - 1 + off, nk);
+    const int skip = max(cl.a, cl.w0);
+    const int E = cl.a + max(cl.w1 - skip, 0);
+    auto chunk_of = [&](int e) { return e < cl.a ? e : skip + e - cl.a; };
+    const int ragged = (p.s.k_lens && nk < p.s.tk && nk % kT) ? nk / kT : -1;
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar->q_full), 1);
+        for (int i = 0; i < C::kKStages; ++i) {
+            mbar_init(smem_u32(&bar->k_full[i]), 1);
+            mbar_init(smem_u32(&bar->k_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar->v_full[i]), 1);
+            mbar_init(smem_u32(&bar->v_empty[i]), 1);
+            mbar_init(smem_u32(&bar->s_full[i]), 1);
+        }
+        mbar_init(smem_u32(&bar->dp_full), 1);
+        mbar_init(smem_u32(&bar->ds_ready), 8);
+        mbar_init(smem_u32(&bar->acc_done), 1);
+        mbar_init(smem_u32(&bar->drain), 1);
+        mbar_init(smem_u32(&bar->zero_req), 1);
+        mbar_init(smem_u32(&bar->zero_done), 1);
+        bar->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bar->tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem_base;
+
+    if (warp < 4) {
+        setmaxnreg_dec<kRegsLow>();
+        if (warp == 0 && lane == 0 && E > 0) {
+            // -------------------------------------------------------- TMA producer
+            const uint32_t qf = smem_u32(&bar->q_full);
+            mbar_arrive_expect_tx(qf, 2 * C::kTile);
+            for (int c = 0; c < D / 64; ++c) {
+                tma_load_4d(smem_u32(sQ + c * C::kChunk), &tmQ, qf, 64 * c, r0, h * p.q_mh,
+                            b * p.q_mb);
+                tma_load_4d(smem_u32(sO + c * C::kChunk), &tmO, qf, 64 * c, r0, h * p.o_mh,
+                            b * p.o_mb);
+            }
+            int k_issued = 0, v_issued = 0;
+            for (int i = 0; i < E; ++i) {
+                const int row = chunk_of(i) * kT, ks = i % C::kKStages, vs = i % C::kVStages;
+                const int kr = i / C::kKStages, vr = i / C::kVStages;
+                if (kr > 0 && !mbar_wait(smem_u32(&bar->k_empty[ks]), (kr - 1) & 1, abort_flag))
+                    break;
+                uint32_t fb = smem_u32(&bar->k_full[ks]);
+                mbar_arrive_expect_tx(fb, C::kTile);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem_u32(sK + ks * C::kTile + c * C::kChunk), &tmK, fb, 64 * c, row,
+                                hk * p.k_mh, b * p.k_mb);
+                k_issued = i + 1;
+                if (vr > 0 && !mbar_wait(smem_u32(&bar->v_empty[vs]), (vr - 1) & 1, abort_flag))
+                    break;
+                fb = smem_u32(&bar->v_full[vs]);
+                mbar_arrive_expect_tx(fb, C::kTile);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem_u32(sV + vs * C::kTile + c * C::kChunk), &tmV, fb, 64 * c, row,
+                                hk * p.v_mh, b * p.v_mb);
+                v_issued = i + 1;
+            }
+            // every copy lands before the CTA can exit, whichever role aborts
+            mbar_wait_bounded(qf, 0);
+            for (int i = max(k_issued - C::kKStages, 0); i < k_issued; ++i)
+                mbar_wait_bounded(smem_u32(&bar->k_full[i % C::kKStages]), (i / C::kKStages) & 1);
+            for (int i = max(v_issued - C::kVStages, 0); i < v_issued; ++i)
+                mbar_wait_bounded(smem_u32(&bar->v_full[i % C::kVStages]), (i / C::kVStages) & 1);
+        } else if (warp == 1 && lane == 0 && E > 0) {
+            // ---------------------------------------------------------- MMA issuer
+            constexpr uint32_t idS = idesc_16_f32(F16, kT, kT, 0, 0);
+            constexpr uint32_t idA = idesc_16_f32(F16, kT, D, 0, 1);
+            const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);
+            const uint64_t nmaj = smem_desc_sw128(0, C::kChunk, 1024);
+            const uint32_t aQ = smem_u32(sQ) >> 4, aO = smem_u32(sO) >> 4;
+            const uint32_t aK = smem_u32(sK) >> 4, aV = smem_u32(sV) >> 4;
+            auto issue_s = [&](int i) {
+                const int ks = i % C::kKStages;
+                if (!mbar_wait(smem_u32(&bar->k_full[ks]), (i / C::kKStages) & 1, abort_flag))
+                    return false;
+                if (chunk_of(i) == ragged) {  // warp 2 clears the keys past the end
+                    mbar_arrive(smem_u32(&bar->zero_req));
+                    if (!mbar_wait(smem_u32(&bar->zero_done), 0, abort_flag)) return false;
+                }
+                product_ss<D>(tmem + kS + 128 * (i & 1), kmaj + aQ,
+                              kmaj + aK + ks * (C::kTile >> 4), idS);
+                mma_commit(smem_u32(&bar->s_full[i & 1]));
+                return true;
+            };
+            auto issue_dp = [&](int i) {
+                const int vs = i % C::kVStages;
+                if (!mbar_wait(smem_u32(&bar->v_full[vs]), (i / C::kVStages) & 1, abort_flag))
+                    return false;
+                product_ss<D>(tmem + kDP, kmaj + aO, kmaj + aV + vs * (C::kTile >> 4), idS);
+                mma_commit(smem_u32(&bar->dp_full));
+                mma_commit(smem_u32(&bar->v_empty[vs]));
+                return true;
+            };
+            bool ok = mbar_wait(smem_u32(&bar->q_full), 0, abort_flag) && issue_s(0) &&
+                      issue_dp(0) && (E < 2 || issue_s(1));
+            for (int i = 0; ok && i < E; ++i) {
+                if (!(ok = mbar_wait(smem_u32(&bar->ds_ready), i & 1, abort_flag))) break;
+                tc_fence_after();
+                const int ks = i % C::kKStages;
+                product_ts(tmem + kDQ, tmem + kDP, nmaj + aK + ks * (C::kTile >> 4), idA, i > 0);
+                mma_commit(smem_u32(&bar->k_empty[ks]));
+                if (i + 1 < E && !(ok = issue_dp(i + 1))) break;
+                if (i + 2 < E && !(ok = issue_s(i + 2))) break;
+            }
+            if (ok) {
+                mma_commit(smem_u32(&bar->acc_done));
+            } else {
+                mma_commit(smem_u32(&bar->drain));
+                mbar_wait_bounded(smem_u32(&bar->drain), 0);
+            }
+        } else if (warp == 2 && ragged >= 0) {
+            // ------------------------------- keys past the sequence's end read as 0
+            int n = E - 1;  // the ragged chunk is a sequence's last: its entry, if any
+            while (n >= 0 && chunk_of(n) > ragged) --n;
+            if (n >= 0 && chunk_of(n) == ragged) {
+                const bool ok = mbar_wait(smem_u32(&bar->zero_req), 0, abort_flag);
+                if (__all_sync(0xffffffffu, ok)) {
+                    zero_rows<D>(smem_u32(sK + (n % C::kKStages) * C::kTile), nk % kT, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar->zero_done));
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------ softmax warpgroups
+        setmaxnreg_inc<kRegsHigh>();
+        const int wg = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t tS = tmem + lane_base + kS + 64 * wg;
+        const uint32_t tDP = tmem + lane_base + kDP + 64 * wg;
+        const int qrow = r0 + row;
+        MaskRange mr = {0, 0, 0};
+        if (qrow < nq) mr = mask_range(p.s.mask, qrow + off, nk);
+        const float *st = p.stats + (((long long)b * p.s.hq + h) * p.n_qblk + blk) * 2 * kT + row;
+        const float nl = __ldg(st), nd = __ldg(st + kT);
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl),
+                     nd2 = make_float2(nd, nd);
+        bool ok = true;
+        for (int i = 0; i < E; ++i) {
+            const int c = chunk_of(i), base = c * kT + 64 * wg;
+            const bool full = cl.full(c);
+            uint32_t keep[2];
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                keep[w] = (bits_below(mr.hi - base - 32 * w) & ~bits_below(mr.lo - base - 32 * w)) |
+                          bits_below(mr.sk - base - 32 * w);
+            uint32_t x[64];
+            float pr[64];
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(smem_u32(&bar->s_full[i & 1]), (i >> 1) & 1, abort_flag));
+            tc_fence_after();
+            if (!ok) break;
+            tmem_ld64(tS + 128 * (i & 1), x);
+            tmem_wait_ld();
+            if (!full) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    if (!((keep[j >> 5] >> (j & 31)) & 1u)) x[j] = kNegInfBits;
+            }
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+                const float2 u = ffma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                                       sc2, nl2);
+                pr[j] = fast_exp2(u.x);
+                pr[j + 1] = fast_exp2(u.y);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->dp_full), i & 1, abort_flag));
+            tc_fence_after();
+            if (!ok) break;
+            tmem_ld64(tDP, x);
+            tmem_wait_ld();
+            {
+                uint32_t pk[32];
+#pragma unroll
+                for (int j = 0; j < 64; j += 2) {
+                    float2 u = fadd2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                                     nd2);
+                    u = ffma2(u, make_float2(pr[j], pr[j + 1]), make_float2(0.f, 0.f));
+                    pk[j / 2] = pack_16x2<F16>(u.x, u.y);
+                }
+                if (!full) {  // 0 also where a dropped pair's product is not finite
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const uint32_t k2 = keep[j >> 4] >> (2 * (j & 15));
+                        pk[j] &= ((k2 & 1u) ? 0xffffu : 0u) | ((k2 & 2u) ? 0xffff0000u : 0u);
+                    }
+                }
+                tmem_st32(tDP, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar->ds_ready));
+        }
+        // ------------------------------------ epilogue: each group half the columns
+        if (ok && E > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->acc_done), 0, abort_flag));
+            tc_fence_after();
+        }
+        if (ok) {
+            char *dst = qrow < nq ? p.dq.p + 2 * (b * p.dq.sb + h * p.dq.sh + qrow * p.dq.st +
+                                                  wg * (D / 2))
+                                  : nullptr;
+            store_row<D / 2, F16>(tmem + lane_base + kDQ + wg * (D / 2), dst, p.scale, E > 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && bar->abort && p.s.status)
+        atomicExch(p.s.status, (int32_t)SVGA_ERR_TIMEOUT);
+}
+
+template <typename K>
+svga_status prepare(K kfn, int smem, const char *what)
+{
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kfn) != cudaSuccess) {
+        set_error("cudaFuncGetAttributes failed: %s", cudaGetErrorString(cudaGetLastError()));
+        return SVGA_ERR_CUDA;
+    }
+    if (fa.numRegs < kRegsLaunch) {
+        // the setmaxnreg split draws on the registers the CTA is launched with
+        set_error("%s kernel built with %d registers/thread, the register split needs %d", what,
+                  fa.numRegs, kRegsLaunch);
+        return SVGA_ERR_UNSUPPORTED;
+    }
+    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess) {
+        set_error("cudaFuncSetAttribute(max dynamic shared memory) failed");
+        return SVGA_ERR_CUDA;
+    }
+    return SVGA_OK;
+}
+
+template <int D, bool F16>
+svga_status launch(const svga_view &d_o, const svga_view &q, const svga_view &k,
+                   const svga_view &v, BwdParams &kp, const svga_window_problem *p,
+                   cudaStream_t st)
+{
+    using C = Cfg<D>;
+    svga_status rc;
+    if ((rc = prepare(bwd_dkdv_kernel<D, F16>, C::kKvAlloc, "window dK/dV")) != SVGA_OK ||
+        (rc = prepare(bwd_dq_kernel<D, F16>, C::kDqAlloc, "window dQ")) != SVGA_OK)
+        return rc;
+    alignas(64) CUtensorMap tq, to, tk, tv;
+    // an empty side is never loaded: its maps only have to be valid
+    const bool hq = p->q_tokens > 0, hk = p->k_tokens > 0;
+    const svga_view &qs = hq ? q : k, &os = hq ? d_o : k, &ks = hk ? k : q, &vs = hk ? v : q;
+    const int qb = hq ? p->batch : 1, qh = hq ? p->q_heads : 1, qt = std::max(p->q_tokens, 1);
+    const int kb = hk ? p->batch : 1, kh = hk ? p->kv_heads : 1, kt = std::max(p->k_tokens, 1);
+    if (!make_view_map(&tq, qs, qb, qh, qt, D, p->dtype, kT, &kp.q_mh, &kp.q_mb) ||
+        !make_view_map(&to, os, qb, qh, qt, D, p->dtype, kT, &kp.o_mh, &kp.o_mb) ||
+        !make_view_map(&tk, ks, kb, kh, kt, D, p->dtype, kT, &kp.k_mh, &kp.k_mb) ||
+        !make_view_map(&tv, vs, kb, kh, kt, D, p->dtype, kT, &kp.v_mh, &kp.v_mb)) {
+        set_error("cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+        return SVGA_ERR_CUDA;
+    }
+    if (hq) {
+        const long long n = (long long)p->batch * p->q_heads * kp.n_qblk * kT * (D / 8);
+        bwd_rows_kernel<D, F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp);
+        if ((rc = check_launch_of("window backward rows")) != SVGA_OK) return rc;
+    }
+    if (hk) {
+        const unsigned grid = (unsigned)((long long)p->batch * p->kv_heads * kp.n_kblk);
+        bwd_dkdv_kernel<D, F16><<<grid, kThreads, C::kKvAlloc, st>>>(tq, to, tk, tv, kp);
+        if ((rc = check_launch_of("window dK/dV")) != SVGA_OK) return rc;
+    }
+    if (hq) {
+        const unsigned grid = (unsigned)((long long)p->batch * p->q_heads * kp.n_qblk);
+        bwd_dq_kernel<D, F16><<<grid, kThreads, C::kDqAlloc, st>>>(tq, to, tk, tv, kp);
+        rc = check_launch_of("window dQ");
+    }
+    return rc;
+}
+
+View to_view(const svga_view &v)
+{
+    return {static_cast<char *>(v.data), v.stride_batch, v.stride_head, v.stride_token};
+}
+
+}  // namespace
+
+size_t window_bwd_workspace(const svga_window_problem *p)
+{
+    const size_t blocks = (size_t)(p->q_tokens + kT - 1) / kT;
+    return (size_t)p->batch * p->q_heads * blocks * 2 * kT * sizeof(float);
+}
+
+svga_status launch_window_bwd(const svga_view &d_o, const svga_view &q, const svga_view &k,
+                              const svga_view &v, const svga_view &o, const float *lse,
+                              const svga_view &dq, const svga_view &dk, const svga_view &dv,
+                              const svga_window_problem *p, float scale, void *ws, void *stream)
+{
+    BwdParams kp{};
+    kp.s = to_shape(p);
+    kp.d_o = to_view(d_o);
+    kp.o = to_view(o);
+    kp.dq = to_view(dq);
+    kp.dk = to_view(dk);
+    kp.dv = to_view(dv);
+    kp.lse = lse;
+    kp.stats = static_cast<float *>(ws);
+    kp.scale = scale;
+    kp.scale_log2 = scale * kLog2e;
+    kp.n_qblk = (p->q_tokens + kT - 1) / kT;
+    kp.n_kblk = (p->k_tokens + kT - 1) / kT;
+    kp.d = p->head_dim;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p->head_dim == 128)
+        return p->dtype == SVGA_F16 ? launch<128, true>(d_o, q, k, v, kp, p, st)
+                                    : launch<128, false>(d_o, q, k, v, kp, p, st);
+    return p->dtype == SVGA_F16 ? launch<64, true>(d_o, q, k, v, kp, p, st)
+                                : launch<64, false>(d_o, q, k, v, kp, p, st);
+}
+
+}  // namespace svga

@@ -1,0 +1,681 @@
+// window_fwd.cu -- attention under a causal window with sinks, forward (sm_100a).
+//
+//   O_i = sum_j P_ij V_j / sum_j P_ij,  P_ij = exp(scale q_i . k_j - m_i),  j kept by the mask,
+//   lse_i = m_i + ln sum_j P_ij.
+//
+// The design is the block-sparse kernel's (attention.cu: two 128-row query blocks a CTA,
+// TMA ring, two tcgen05.mma issuers, S | P0 | P1 | O0 | O1 in TMEM, one row per softmax
+// thread, the reference maximum of the first tile kept until a tile's sum would pass a
+// limit).  What differs:
+//   * the visited key chunks need no map: the keys a run of queries keeps are [0, sk) and
+//     [lo, hi), all monotone in the position (stream.h), so every role computes its list;
+//   * rows are masked by those two intervals, two shifts a 32-key word;
+//   * tensors are strided and batched (4-D tensor maps), query heads share key heads, every
+//     sequence may have its own lengths; rows of V past a sequence's end are set to 0 in
+//     shared memory before they meet P (0 times a NaN left there is not 0);
+//   * bf16 or fp16.  P reaches at most the tile-sum limit: 2^16 in bf16, 2^15 in fp16 (65504
+//     is its largest value); what underflows in fp16 (below 2^-24 of a sum >= 1) is lost
+//     below the rounding of O;
+//   * with few query rows the key list is split over `ksplit` CTAs that leave fp32 partial
+//     rows in the workspace, joined in a fixed order by a second kernel.
+// Query blocks are launched last first: under a causal mask those are the longest, and the
+// hardware hands CTAs out in index order.  Neighbouring CTAs are heads of one group, so
+// the K and V chunks they share meet in L2.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "stream.h"
+#include "svga_device.cuh"
+
+namespace svga {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kKN = 128;  // keys per chunk
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kNegInfBits = 0xff800000u;
+// registers: the producer / MMA warpgroup drops to kRegsLow, the softmax warpgroups rise to
+// kRegsHigh (checked against the launch's on the host)
+constexpr int kRegsLaunch = 168, kRegsLow = 120, kRegsHigh = 192;
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "register split");
+// TMEM columns: the S tile shared by the two groups, a P tile per group, an O per group
+constexpr uint32_t kTmS = 0, kTmP = 128, kTmO = 256;
+constexpr int kMinChunksPerSplit = 4;
+
+struct FwdParams {
+    WindowShape s;
+    View o;
+    float *lse;
+    float scale_log2;
+    int n_pairs, ksplit;
+    int q_mb, q_mh, k_mb, k_mh, v_mb, v_mh;  // coordinate multipliers (0: broadcast)
+    float *part_o;    // [ksplit][batch * hq * tq][d], unnormalised
+    float2 *part_ml;  // [ksplit][batch * hq * tq] (reference maximum, sum)
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int kQBytes = kBlockM * D * 2;
+    static constexpr int kQChunk = kBlockM * 128;  // 64 columns x 128 rows
+    static constexpr int kKVBytes = kKN * D * 2;
+    static constexpr int kKVChunk = kKN * 128;
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kSmemData = 2 * kQBytes + kStages * kKVBytes;
+    static constexpr int kSmemAlloc = kSmemData + 1024 + 1024;  // barriers, alignment slack
+    // one CTA per SM: the TMEM of a CTA is the whole SM's
+    static constexpr int kSmemLaunch = kSmemAlloc < 120 * 1024 ? 120 * 1024 : kSmemAlloc;
+    static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
+};
+
+struct Barriers {
+    uint64_t q_full;
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t s_full[2];    // [group]: that group's S is in the shared S columns
+    uint64_t s_free;       // the S columns were read into registers by their owner (4 warps)
+    uint64_t s_issued[4];  // [visit % 4]: the S issuer has issued the S of that visit
+    uint64_t p_full[2];    // [group]: P of the group's tile is in its P columns (4 warps)
+    uint64_t o_done[2];    // [group]: the group's last P V product is done
+    uint64_t drain[2];     // abort: [issuer]: the MMAs that issuer started are done
+    uint64_t zero_req, zero_done;  // the ragged V chunk landed / its rows past the end are 0
+    uint32_t tmem_base;
+    int abort;
+};
+
+constexpr uint32_t kV0 = 1, kF0 = 2, kV1 = 4, kF1 = 8;
+
+// One CTA's work: two query blocks of one head and its share of their merged chunk list.
+struct Item {
+    int b, h, b0, nq, nk;
+    bool valid1;
+    ChunkList l0, l1;
+    int a, skip;  // merged list: chunks 0 .. a - 1, then skip, skip + 1, ...
+    int e0, E;    // this CTA's entries
+    __device__ __forceinline__ int chunk(int n) const
+    {
+        const int e = e0 + n;
+        return e < a ? e : skip + e - a;
+    }
+    __device__ __forceinline__ uint32_t flags(int c) const
+    {
+        uint32_t f = l0.visits(c) ? kV0 | (l0.full(c) ? kF0 : 0u) : 0u;
+        if (valid1 && l1.visits(c)) f |= kV1 | (l1.full(c) ? kF1 : 0u);
+        return f;
+    }
+};
+
+// The merged chunk list of two consecutive runs of queries.  The windows of consecutive
+// positions touch or overlap, so every chunk of the list is visited by one of the runs.
+__host__ __device__ __forceinline__ void merge_lists(const ChunkList &l0, const ChunkList &l1,
+                                                     bool valid1, int &a, int &skip, int &end)
+{
+    a = l0.a;
+    int w0 = l0.w0, w1 = l0.w1;
+    if (valid1) {
+        a = l1.a > a ? l1.a : a;
+        if (l1.w1 > l1.w0) {
+            if (w1 <= w0 || l1.w0 < w0) w0 = l1.w0;
+            if (l1.w1 > w1) w1 = l1.w1;
+        }
+    }
+    skip = w0 > a ? w0 : a;
+    end = w1 > skip ? w1 : skip;
+}
+
+__device__ __forceinline__ int clamped_len(const int32_t *lens, int b, int most)
+{
+    return lens ? min(max(__ldg(lens + b), 0), most) : most;
+}
+
+__device__ __forceinline__ bool make_item(const FwdParams &p, Item &it)
+{
+    const int bh = p.s.batch * p.s.hq;
+    const int slot = blockIdx.x / p.ksplit, part = blockIdx.x - slot * p.ksplit;
+    const int pair = p.n_pairs - 1 - slot / bh, r = slot % bh;
+    it.b = r / p.s.hq;
+    it.h = r - it.b * p.s.hq;
+    it.b0 = 2 * pair;
+    it.nq = clamped_len(p.s.q_lens, it.b, p.s.tq);
+    it.nk = clamped_len(p.s.k_lens, it.b, p.s.tk);
+    const int off = it.nk - it.nq, r0 = it.b0 * kBlockM;
+    if (r0 >= it.nq) return false;
+    it.valid1 = r0 + kBlockM < it.nq;
+    it.l0 = chunk_list<kKN>(p.s.mask, r0 + off, min(r0 + kBlockM, it.nq) - 1 + off, it.nk);
+    if (it.valid1)
+        it.l1 = chunk_list<kKN>(p.s.mask, r0 + kBlockM + off,
+                                min(r0 + 2 * kBlockM, it.nq) - 1 + off, it.nk);
+    else
+        it.l1 = it.l0;
+    int end;
+    merge_lists(it.l0, it.l1, it.valid1, it.a, it.skip, end);
+    const long long all = it.a + end - it.skip;
+    it.e0 = (int)(part * all / p.ksplit);
+    it.E = (int)((part + 1) * all / p.ksplit) - it.e0;
+    return true;
+}
+
+// bits [0, n) of a 32-bit word
+__device__ __forceinline__ uint32_t bits_below(int n)
+{
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const FwdParams p)
+{
+    using C = Cfg<D>;
+    constexpr float kSumLimit = F16 ? 32768.f : 65536.f;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    uint8_t *sQ = smem;
+    uint8_t *sKV = smem + 2 * C::kQBytes;
+    Barriers *bar = reinterpret_cast<Barriers *>(smem + C::kSmemData);
+    volatile int *abort_flag = &bar->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    Item it;
+    if (!make_item(p, it)) return;  // past the sequence's queries (uniform over the CTA)
+    // the chunk whose last rows lie past the sequence's end but inside the tensor
+    const int ragged = (p.s.k_lens && it.nk < p.s.tk && it.nk % kKN) ? it.nk / kKN : -1;
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar->q_full), 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(smem_u32(&bar->kv_full[s]), 1);
+            mbar_init(smem_u32(&bar->kv_empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar->s_full[i]), 1);
+            mbar_init(smem_u32(&bar->p_full[i]), 4);
+            mbar_init(smem_u32(&bar->o_done[i]), 1);
+            mbar_init(smem_u32(&bar->drain[i]), 1);
+        }
+        mbar_init(smem_u32(&bar->s_free), 4);
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bar->s_issued[i]), 1);
+        mbar_init(smem_u32(&bar->zero_req), 1);
+        mbar_init(smem_u32(&bar->zero_done), 1);
+        bar->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bar->tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem_base;
+
+    if (warp < 4) {
+        setmaxnreg_dec<kRegsLow>();
+        if (warp == 0 && lane == 0 && it.E > 0) {
+            // -------------------------------------------------------- TMA producer
+            const uint32_t qf = smem_u32(&bar->q_full);
+            const int nq_tiles = it.valid1 ? 2 : 1, hk = it.h / p.s.group;
+            mbar_arrive_expect_tx(qf, nq_tiles * C::kQBytes);
+            for (int i = 0; i < nq_tiles; ++i)
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem_u32(sQ + i * C::kQBytes + c * C::kQChunk), &tmQ, qf, 64 * c,
+                                (it.b0 + i) * kBlockM, it.h * p.q_mh, it.b * p.q_mb);
+            int issued = 0;
+            bool ok = true;
+            for (int n = 0; n < it.E && ok; ++n) {
+                const int row = it.chunk(n) * kKN;
+                for (int t = 0; t < 2; ++t) {
+                    const int idx = 2 * n + t, s = idx % C::kStages, round = idx / C::kStages;
+                    if (round > 0 &&
+                        !mbar_wait(smem_u32(&bar->kv_empty[s]), (round - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&bar->kv_full[s]);
+                    mbar_arrive_expect_tx(fb, C::kKVBytes);
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d(smem_u32(sKV + s * C::kKVBytes + c * C::kKVChunk),
+                                    t ? &tmV : &tmK, fb, 64 * c, row,
+                                    hk * (t ? p.v_mh : p.k_mh), it.b * (t ? p.v_mb : p.k_mb));
+                    issued = idx + 1;
+                }
+            }
+            // every copy lands before the CTA can exit, whichever role aborts
+            mbar_wait_bounded(qf, 0);
+            for (int idx = max(issued - C::kStages, 0); idx < issued; ++idx)
+                mbar_wait_bounded(smem_u32(&bar->kv_full[idx % C::kStages]),
+                                  (idx / C::kStages) & 1);
+        } else if ((warp == 1 || warp == 3) && lane == 0) {
+            // ------------------------------------------------------- MMA issuers
+            // warp 1: S = Q K^T, warp 3: O += P V; each waits on its own barriers only, the
+            // hazards between them go through the softmax groups' barriers (attention.cu)
+            const bool s_role = warp == 1;
+            constexpr uint32_t idS = idesc_16_f32(F16, kBlockM, kKN, 0, 0);
+            constexpr uint32_t idO = idesc_16_f32(F16, kBlockM, D, 0, 1);
+            const uint64_t dK = smem_desc_sw128(0, 16, 1024);
+            const uint64_t dV = smem_desc_sw128(0, C::kKVChunk, 1024);
+            const uint32_t q_addr = smem_u32(sQ) >> 4, kv_addr = smem_u32(sKV) >> 4;
+            const int total = 2 * it.E;
+            bool ok = it.E == 0 || !s_role || mbar_wait(smem_u32(&bar->q_full), 0, abort_flag);
+            auto wait_full = [&](int idx) {
+                return mbar_wait(smem_u32(&bar->kv_full[idx % C::kStages]),
+                                 (idx / C::kStages) & 1, abort_flag);
+            };
+            auto release = [&](int idx) {
+                if (idx + C::kStages < total)
+                    mma_commit(smem_u32(&bar->kv_empty[idx % C::kStages]));
+            };
+            // the visits: (entry n, group g), entries ascending, group 0 before group 1
+            int n = 0, k = 0, pvn0 = 0, pvn1 = 0;
+            auto run = [&](auto role_tag) {
+                constexpr bool kSRole = decltype(role_tag)::value;
+                for (; ok && n < it.E; ++n) {
+                    const int chunk = it.chunk(n);
+                    const uint32_t f = it.flags(chunk);
+                    bool waited = false;
+#pragma unroll 1
+                    for (int g = (f & kV0) ? 0 : 1; g < 2; ++g) {
+                        if (g == 1 && !(f & kV1)) break;
+                        const bool last = g == 1 || !(f & kV1);
+                        if constexpr (kSRole) {
+                            // once the owner of the previous visit has read its S
+                            if (k > 0 && !(ok = mbar_wait(smem_u32(&bar->s_free), (k - 1) & 1,
+                                                          abort_flag)))
+                                break;
+                            tc_fence_after();
+                            if (!waited && !(ok = wait_full(2 * n))) break;
+                            waited = true;
+                            const uint64_t a0 = dK + (q_addr + g * (C::kQBytes >> 4));
+                            const uint64_t b0 =
+                                dK + (kv_addr + ((2 * n) % C::kStages) * (C::kKVBytes >> 4));
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                mma_ss(tmem + kTmS,
+                                       a0 + (uint32_t)(((kk >> 2) * C::kQChunk + (kk & 3) * 32) >> 4),
+                                       b0 + (uint32_t)(((kk >> 2) * C::kKVChunk + (kk & 3) * 32) >> 4),
+                                       idS, kk > 0 ? 1u : 0u);
+                            mma_commit(smem_u32(&bar->s_full[g]));
+                            if (last) release(2 * n);
+                            mbar_arrive(smem_u32(&bar->s_issued[k & 3]));
+                        } else {
+                            if (!waited) {
+                                if (!(ok = wait_full(2 * n + 1))) break;
+                                if (chunk == ragged) {  // warp 2 clears the rows past the end
+                                    mbar_arrive(smem_u32(&bar->zero_req));
+                                    if (!(ok = mbar_wait(smem_u32(&bar->zero_done), 0, abort_flag)))
+                                        break;
+                                }
+                                waited = true;
+                            }
+                            int &pvn = g ? pvn1 : pvn0;
+                            ok = mbar_wait(smem_u32(&bar->p_full[g]), pvn & 1, abort_flag);
+                            // right behind the S two visits ahead, where it runs while that S
+                            // is being read (attention.cu has the argument that the barrier
+                            // is never two phases off)
+                            ok = ok && mbar_wait(smem_u32(&bar->s_issued[(k + 2) & 3]),
+                                                 ((k + 2) >> 2) & 1, abort_flag);
+                            tc_fence_after();
+                            if (!ok) break;
+                            const uint64_t b0 =
+                                dV + (kv_addr + ((2 * n + 1) % C::kStages) * (C::kKVBytes >> 4));
+#pragma unroll
+                            for (int kk = 0; kk < kKN / 16; ++kk)
+                                mma_ts(tmem + kTmO + g * 128, tmem + kTmP + g * 64 + kk * 8,
+                                       b0 + (uint32_t)(kk * (2048 >> 4)), idO,
+                                       (pvn != 0 || kk > 0) ? 1u : 0u);
+                            mma_commit(smem_u32(&bar->o_done[g]));
+                            if (last) release(2 * n + 1);
+                            ++pvn;
+                        }
+                        ++k;
+                    }
+                }
+            };
+            if (s_role)
+                run(std::true_type{});
+            else
+                run(std::false_type{});
+            if (ok && s_role) {  // the last two P V products wait for no later S
+                mbar_arrive(smem_u32(&bar->s_issued[k & 3]));
+                mbar_arrive(smem_u32(&bar->s_issued[(k + 1) & 3]));
+            }
+            if (!ok) {
+                // abort: wait for every MMA this thread issued before TMEM is freed
+                const uint32_t drain = smem_u32(&bar->drain[s_role ? 0 : 1]);
+                mma_commit(drain);
+                mbar_wait_bounded(drain, 0);
+            }
+        } else if (warp == 2 && ragged >= 0) {
+            // --------------------------------- rows of V past the sequence's end read as 0
+            int n = it.E - 1;  // the ragged chunk is a sequence's last: its entry, if any
+            while (n >= 0 && it.chunk(n) > ragged) --n;
+            if (n >= 0 && it.chunk(n) == ragged) {
+                const bool ok = mbar_wait(smem_u32(&bar->zero_req), 0, abort_flag);
+                if (__all_sync(0xffffffffu, ok)) {
+                    const uint32_t base =
+                        smem_u32(sKV + ((2 * n + 1) % C::kStages) * C::kKVBytes);
+                    for (int u = (it.nk % kKN) * 8 + lane; u < kKN * 8; u += 32)
+                        for (int c = 0; c < D / 64; ++c)
+                            st_shared_v4(base + c * C::kKVChunk + u * 16, 0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar->zero_done));
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------ softmax warpgroups
+        setmaxnreg_inc<kRegsHigh>();
+        const int wg = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t tS = tmem + lane_base + kTmS;
+        const uint32_t tP = tmem + lane_base + kTmP + wg * 64;
+        const uint32_t tO = tmem + lane_base + kTmO + wg * 128;
+        const int qrow = (it.b0 + wg) * kBlockM + row;
+        const bool row_valid = qrow < it.nq;
+        MaskRange mr = {0, 0, 0};
+        if (row_valid) mr = mask_range(p.s.mask, qrow + it.nk - it.nq, it.nk);
+        const uint32_t vbit = wg ? kV1 : kV0, fbit = wg ? kF1 : kF0;
+        const float sl2 = p.scale_log2;
+        float m_used = -INFINITY, l = 0.f;
+        int visit = 0;
+        bool ok = true;
+        for (int n = 0; n < it.E; ++n) {
+            const int chunk = it.chunk(n);
+            const uint32_t f = it.flags(chunk);
+            if (!(f & vbit)) continue;
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(smem_u32(&bar->s_full[wg]), visit & 1, abort_flag));
+            tc_fence_after();
+            if (!ok) break;
+            uint32_t r[kKN];
+#pragma unroll
+            for (int j = 0; j < kKN / 32; ++j)
+                tmem_ld32(tS + j * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[j * 32]));
+            tmem_wait_ld();
+            tc_fence_before();  // S is in registers: its columns may take the next visit's
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar->s_free));
+            if (!(f & fbit)) {
+                const int k0 = chunk * kKN;
+#pragma unroll
+                for (int w = 0; w < kKN / 32; ++w) {
+                    const int x = k0 + 32 * w;
+                    const uint32_t keep = (bits_below(mr.hi - x) & ~bits_below(mr.lo - x)) |
+                                          bits_below(mr.sk - x);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!((keep >> c) & 1u)) r[32 * w + c] = kNegInfBits;
+                }
+            }
+            auto tile_max = [&]() {
+                float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kKN; c += 8) {
+                    a0 = fmax3(a0, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+                    a1 = fmax3(a1, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+                    a2 = fmax3(a2, __uint_as_float(r[c + 4]), __uint_as_float(r[c + 5]));
+                    a3 = fmax3(a3, __uint_as_float(r[c + 6]), __uint_as_float(r[c + 7]));
+                }
+                return fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sl2;
+            };
+            if (m_used == -INFINITY) m_used = tile_max();
+            if (visit > 0) {  // the previous P V reads the P columns this tile writes
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->o_done[wg]),
+                                                       (visit - 1) & 1, abort_flag));
+                tc_fence_after();
+                if (!ok) break;
+            }
+            float lt;
+#pragma unroll 1
+            for (int attempt = 0;; ++attempt) {
+                const float ms = (m_used == -INFINITY) ? 0.f : m_used;
+                const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-ms, -ms);
+                float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < kKN / 32; ++j) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c2 = 0; c2 < 16; ++c2) {
+                        const int c = j * 32 + 2 * c2;
+                        const float2 x = ffma2(
+                            make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nm2);
+                        const float2 ev = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        if (c2 & 1)
+                            s1 = fadd2(s1, ev);
+                        else
+                            s0 = fadd2(s0, ev);
+                        pk[c2] = F16 ? pack_f16x2(ev.x, ev.y) : pack_bf16x2_int(ev.x, ev.y);
+                    }
+                    tmem_st16(tP + j * 16, pk);
+                }
+                lt = (s0.x + s0.y) + (s1.x + s1.y);
+                const bool need = !(lt <= kSumLimit);
+                if (attempt > 0 || !__any_sync(0xffffffffu, need)) break;
+                // rare: O is rescaled to the tile's exact maximum and the tile is done again
+                const float m_new = need ? fmaxf(m_used, tile_max()) : m_used;
+                const float fac = need ? fast_exp2(m_used - m_new) : 1.f;
+                l *= fac;
+                m_used = m_new;
+                if (visit > 0) {
+#pragma unroll 1
+                    for (int j = 0; j < D / 32; ++j) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + j * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            o[c] = __float_as_uint(__uint_as_float(o[c]) * fac);
+                        tmem_st32(tO + j * 32, o);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            l += lt;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar->p_full[wg]));
+            ++visit;
+        }
+        // ----------------------------------------------------------------- epilogue
+        if (ok && visit > 0) {
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(smem_u32(&bar->o_done[wg]), (visit - 1) & 1, abort_flag));
+            tc_fence_after();
+        }
+        const bool split = p.ksplit > 1;
+        if (ok && (wg == 0 || it.valid1)) {
+            const float inv = split ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+            const long long flat = ((long long)it.b * p.s.hq + it.h) * p.s.tq + qrow;
+            const long long part =
+                (long long)(blockIdx.x % p.ksplit) * p.s.batch * p.s.hq * p.s.tq + flat;
+            char *orow = p.o.p + 2 * (it.b * p.o.sb + it.h * p.o.sh + qrow * p.o.st);
+#pragma unroll 1
+            for (int j = 0; j < D / 32; ++j) {
+                uint32_t o[32];
+                if (visit > 0) {
+                    tmem_ld32(tO + j * 32, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] = 0u;
+                }
+                if (!row_valid) continue;
+                if (split) {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + part * D + j * 32);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                             __uint_as_float(o[4 * c + 2]),
+                                             __uint_as_float(o[4 * c + 3]));
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(orow + 64 * j);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = pack_16x2<F16>(__uint_as_float(o[8 * c + 2 * i]) * inv,
+                                                  __uint_as_float(o[8 * c + 2 * i + 1]) * inv);
+                        dst[c] = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+            }
+            if (row_valid && split)
+                p.part_ml[part] = make_float2(m_used, l);
+            else if (row_valid && p.lse)
+                p.lse[flat] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.6931471805599453f;
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && bar->abort && p.s.status)
+        atomicExch(p.s.status, (int32_t)SVGA_ERR_TIMEOUT);
+}
+
+// Join of a split launch: one thread per 8 values of a row; the parts' maxima give the
+// common scale, sums run in part order.  A part that saw no key of the row has l = 0.
+template <bool F16>
+__global__ void __launch_bounds__(256) join_kernel(const FwdParams p, int d)
+{
+    const int per = d / 8;
+    const long long rows = (long long)p.s.batch * p.s.hq * p.s.tq;
+    const long long i = blockIdx.x * 256ll + threadIdx.x;
+    if (i >= rows * per) return;
+    const long long row = i / per, bh = row / p.s.tq;
+    const int c = 8 * (int)(i - row * per), t = (int)(row - bh * p.s.tq);
+    const int b = (int)(bh / p.s.hq), h = (int)(bh - (long long)b * p.s.hq);
+    if (t >= clamped_len(p.s.q_lens, b, p.s.tq)) return;
+    float m = -INFINITY;
+    for (int r = 0; r < p.ksplit; ++r) m = fmaxf(m, __ldg(&p.part_ml[r * rows + row].x));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int r = 0; r < p.ksplit; ++r) {
+        const float2 ml = __ldg(&p.part_ml[r * rows + row]);
+        const float4 *src =
+            reinterpret_cast<const float4 *>(p.part_o + (r * rows + row) * d + c);
+        const float4 u = __ldg(src), v = __ldg(src + 1);
+        const float w = exp2f(ml.x - ref);
+        l += w * ml.y;
+        x[0] += w * u.x;
+        x[1] += w * u.y;
+        x[2] += w * u.z;
+        x[3] += w * u.w;
+        x[4] += w * v.x;
+        x[5] += w * v.y;
+        x[6] += w * v.z;
+        x[7] += w * v.w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = pack_16x2<F16>(x[2 * k] * inv, x[2 * k + 1] * inv);
+    *reinterpret_cast<uint4 *>(p.o.p + 2 * (b * p.o.sb + h * p.o.sh + t * p.o.st + c)) =
+        make_uint4(y[0], y[1], y[2], y[3]);
+    if (c == 0 && p.lse)
+        p.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+}
+
+// CTAs a key list is split over: one unless the launch has fewer than half as many items as
+// the GPU has SMs, then as many as fill the SMs once while every part keeps
+// kMinChunksPerSplit chunks of the longest list the shapes allow.
+int choose_split(const svga_window_problem *p)
+{
+    const long long items = (long long)p->batch * p->q_heads * ((p->q_tokens + 255) / 256);
+    if (items == 0 || 2 * items > 148) return 1;
+    const Mask m = to_mask(p->mask);
+    const int last = p->k_tokens - 1, first = std::max(last - std::min(p->q_tokens, 256) + 1, 0);
+    const ChunkList c = chunk_list<kKN>(m, first, last, p->k_tokens);
+    const int chunks = c.a + std::max(c.w1 - std::max(c.a, c.w0), 0);
+    return (int)std::max(1ll, std::min(148 / items, (long long)chunks / kMinChunksPerSplit));
+}
+
+template <int D, bool F16>
+svga_status launch(const svga_view &q, const svga_view &k, const svga_view &v, FwdParams &kp,
+                   const svga_window_problem *p, cudaStream_t st)
+{
+    using C = Cfg<D>;
+    auto kfn = window_fwd_kernel<D, F16>;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kfn) != cudaSuccess) {
+        set_error("cudaFuncGetAttributes failed: %s", cudaGetErrorString(cudaGetLastError()));
+        return SVGA_ERR_CUDA;
+    }
+    if (fa.numRegs < kRegsLaunch) {
+        // the setmaxnreg split draws on the registers the CTA is launched with
+        set_error("window kernel built with %d registers/thread, the register split needs %d",
+                  fa.numRegs, kRegsLaunch);
+        return SVGA_ERR_UNSUPPORTED;
+    }
+    alignas(64) CUtensorMap tq, tk, tv;
+    // without keys nothing is loaded: the maps of K and V then only have to be valid
+    const svga_view &ks = p->k_tokens ? k : q, &vs = p->k_tokens ? v : q;
+    const int kt = std::max(p->k_tokens, 1), kh = p->k_tokens ? p->kv_heads : 1;
+    const int kb = p->k_tokens ? p->batch : 1;
+    if (!make_view_map(&tq, q, p->batch, p->q_heads, p->q_tokens, D, p->dtype, kBlockM, &kp.q_mh,
+                       &kp.q_mb) ||
+        !make_view_map(&tk, ks, kb, kh, kt, D, p->dtype, kKN, &kp.k_mh, &kp.k_mb) ||
+        !make_view_map(&tv, vs, kb, kh, kt, D, p->dtype, kKN, &kp.v_mh, &kp.v_mb)) {
+        set_error("cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+        return SVGA_ERR_CUDA;
+    }
+    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemLaunch) !=
+        cudaSuccess) {
+        set_error("cudaFuncSetAttribute(max dynamic shared memory) failed");
+        return SVGA_ERR_CUDA;
+    }
+    const long long grid = (long long)p->batch * p->q_heads * kp.n_pairs * kp.ksplit;
+    kfn<<<(unsigned)grid, kThreads, C::kSmemLaunch, st>>>(tq, tk, tv, kp);
+    svga_status rc = check_launch_of("window attention");
+    if (rc != SVGA_OK || kp.ksplit == 1) return rc;
+    const long long n = (long long)p->batch * p->q_heads * p->q_tokens * (D / 8);
+    join_kernel<F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp, D);
+    return check_launch_of("window attention join");
+}
+
+}  // namespace
+
+size_t window_fwd_workspace(const svga_window_problem *p)
+{
+    const int split = choose_split(p);
+    if (split == 1) return 0;
+    const size_t rows = (size_t)p->batch * p->q_heads * p->q_tokens;
+    return (size_t)split * rows * (p->head_dim * 4 + 8);
+}
+
+svga_status launch_window_fwd(const svga_view &q, const svga_view &k, const svga_view &v,
+                              const svga_view &o, float *lse, const svga_window_problem *p,
+                              float scale, void *ws, void *stream)
+{
+    FwdParams kp{};
+    kp.s = to_shape(p);
+    kp.o = {static_cast<char *>(o.data), o.stride_batch, o.stride_head, o.stride_token};
+    kp.lse = lse;
+    kp.scale_log2 = scale * kLog2e;
+    kp.n_pairs = (p->q_tokens + 2 * kBlockM - 1) / (2 * kBlockM);
+    kp.ksplit = choose_split(p);
+    if (kp.ksplit > 1) {
+        const size_t rows = (size_t)p->batch * p->q_heads * p->q_tokens;
+        kp.part_o = static_cast<float *>(ws);
+        kp.part_ml = reinterpret_cast<float2 *>(kp.part_o + kp.ksplit * rows * p->head_dim);
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p->head_dim == 128)
+        return p->dtype == SVGA_F16 ? launch<128, true>(q, k, v, kp, p, st)
+                                    : launch<128, false>(q, k, v, kp, p, st);
+    return p->dtype == SVGA_F16 ? launch<64, true>(q, k, v, kp, p, st)
+                                : launch<64, false>(q, k, v, kp, p, st);
+}
+
+}  // namespace svga

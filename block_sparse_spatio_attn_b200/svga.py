@@ -39,6 +39,8 @@ EXPORTED = ["svga_problem_rows", "svga_block_map_size", "svga_build_block_map",
             "svga_classify_size", "svga_classify_heads", "svga_kept_fraction",
             "svga_autotune_size", "svga_autotune_heads",
             "svga_rotary_table_size", "svga_rotary_table", "svga_rotary",
+            "svga_window_attention_size", "svga_window_attention_fwd",
+            "svga_window_attention_bwd",
             "svga_cache_append", "svga_cache_decode", "svga_last_error",
             "svga_status_string", "svga_version"]
 
@@ -82,6 +84,14 @@ class RotarySpecC(ctypes.Structure):
 class WindowMaskC(ctypes.Structure):
     _fields_ = [("causal", ctypes.c_int), ("window", ctypes.c_int), ("sinks", ctypes.c_int),
                 ("block", ctypes.c_int)]
+
+
+class WindowProblemC(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("q_tokens", ctypes.c_int), ("k_tokens", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("mask", WindowMaskC),
+                ("q_lens", ctypes.c_void_p), ("k_lens", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
 
 
 class PagedCacheC(ctypes.Structure):
@@ -137,6 +147,11 @@ def load() -> ctypes.CDLL:
         lib.svga_rotary_table_size.argtypes = [PR, ctypes.POINTER(SZ)]
         lib.svga_rotary_table.argtypes = [PR, ctypes.c_double, P, P]
         lib.svga_rotary.argtypes = [PV, PV, I, I, I, I, I, PR, P, P, ctypes.c_int64, I, P, P]
+        PW = ctypes.POINTER(WindowProblemC)
+        lib.svga_window_attention_size.argtypes = [PW, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
+        lib.svga_window_attention_fwd.argtypes = [PV, PV, PV, PV, P, PW, F, P, SZ, P]
+        lib.svga_window_attention_bwd.argtypes = [PV, PV, PV, PV, PV, P, PV, PV, PV, PW, F, P,
+                                                  SZ, P]
         lib.svga_cache_append.argtypes = [PV, PV, I, P, PC, PR, P, P]
         lib.svga_cache_decode.argtypes = [PV, PV, P, I, PC, PM, F, P]
         lib.svga_last_error.restype = ctypes.c_char_p
@@ -663,6 +678,86 @@ class WindowMask:
 
     def __post_init__(self):
         self.c = WindowMaskC(int(self.causal), self.window, self.sinks, self.block)
+
+
+def _window_problem(a: _Strided, q, k, mask, q_lens, k_lens, status) -> WindowProblemC:
+    dt = _dtype_of(q, "q", 4)
+    _dtype_of(k, "k", 4)
+    B, H, Tq, d = q.shape
+    pql = a.flat(q_lens, "q_lens", torch.int32, (B,), optional=True)
+    pkl = a.flat(k_lens, "k_lens", torch.int32, (B,), optional=True)
+    ps = a.flat(status, "status", torch.int32, (1,), optional=True)
+    return WindowProblemC(B, H, k.shape[1], Tq, k.shape[2], d, dt, mask.c, pql, pkl, ps)
+
+
+def _window_workspace(a: _Strided, workspace, need: int, stream):
+    """The caller's workspace, or one from the allocator that belongs to the call's stream."""
+    if workspace is not None:
+        a._add(workspace, "workspace", torch.uint8, workspace.shape)
+        if not workspace.is_contiguous():
+            raise SvgaError(1, "workspace must be contiguous")
+        a.done()
+        return workspace, workspace.numel()
+    if need == 0:
+        return None, 0
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=a.device), need
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=a.device), need
+
+
+def svga_window_attention_size(q, k, mask: WindowMask) -> dict:
+    """Bytes of workspace of the forward and the backward call on tensors shaped like q and k."""
+    c = _window_problem(_Strided(), q, k, mask, None, None, None)
+    n = [ctypes.c_size_t() for _ in range(2)]
+    _check(load().svga_window_attention_size(ctypes.byref(c), ctypes.byref(n[0]),
+                                             ctypes.byref(n[1])))
+    return {"fwd_bytes": n[0].value, "bwd_bytes": n[1].value}
+
+
+def svga_window_attention_fwd(q, k, v, o, lse, mask: WindowMask, scale: float, q_lens=None,
+                              k_lens=None, status=None, workspace=None,
+                              stream=None) -> torch.Tensor:
+    """o = softmax(scale q k^T) v under the mask, strided [batch, heads, tokens, head_dim];
+    lse: fp32 [batch, q_heads, q_tokens] or None; q_lens, k_lens: int32 [batch] or None."""
+    a = _Strided()
+    c = _window_problem(a, q, k, mask, q_lens, k_lens, status)
+    ks = (c.batch, c.kv_heads, c.k_tokens, c.head_dim)
+    vq, vk = a.view(q, "q", q.dtype, q.shape), a.view(k, "k", q.dtype, ks)
+    vv, vo = a.view(v, "v", q.dtype, ks), a.view(o, "o", q.dtype, q.shape)
+    pl = a.flat(lse, "lse", torch.float32, q.shape[:3], optional=True)
+    lib, need, rc = load(), ctypes.c_size_t(), ctypes.byref(c)
+    with a.done():
+        _check(lib.svga_window_attention_size(rc, ctypes.byref(need), None))
+        st = a.stream(stream)
+        ws, n = _window_workspace(a, workspace, need.value, stream)
+        _check(lib.svga_window_attention_fwd(ctypes.byref(vq), ctypes.byref(vk), ctypes.byref(vv),
+                                             ctypes.byref(vo), pl, rc, float(scale), _ptr(ws), n,
+                                             st))
+    return o
+
+
+def svga_window_attention_bwd(d_o, q, k, v, o, lse, dq, dk, dv, mask: WindowMask, scale: float,
+                              q_lens=None, k_lens=None, status=None, workspace=None,
+                              stream=None):
+    """Gradients dq, dk, dv of svga_window_attention_fwd from that of o; o and lse are the
+    forward call's.  Returns (dq, dk, dv)."""
+    a = _Strided()
+    c = _window_problem(a, q, k, mask, q_lens, k_lens, status)
+    ks = (c.batch, c.kv_heads, c.k_tokens, c.head_dim)
+    views = [a.view(t, n, q.dtype, q.shape if i in "q" else ks)
+             for t, n, i in ((d_o, "d_o", "q"), (q, "q", "q"), (k, "k", "k"), (v, "v", "k"),
+                             (o, "o", "q"), (dq, "dq", "q"), (dk, "dk", "k"), (dv, "dv", "k"))]
+    pl = a.flat(lse, "lse", torch.float32, q.shape[:3])
+    lib, need, rc = load(), ctypes.c_size_t(), ctypes.byref(c)
+    with a.done():
+        _check(lib.svga_window_attention_size(rc, None, ctypes.byref(need)))
+        st = a.stream(stream)
+        ws, n = _window_workspace(a, workspace, need.value, stream)
+        p = [ctypes.byref(x) for x in views]
+        _check(lib.svga_window_attention_bwd(*p[:5], pl, *p[5:], rc, float(scale), _ptr(ws), n,
+                                             st))
+    return dq, dk, dv
 
 
 def _paged_cache(a: _Strided, k_pages, v_pages, page_table, lens, batch, status):

@@ -527,6 +527,60 @@ typedef struct {
     int block;  /* 1 .. 2^24 tokens */
 } svga_window_mask;
 
+/* Shapes of a window call.  q_heads is a multiple of kv_heads; query head h reads key head
+ * h / (q_heads / kv_heads).  0 <= q_tokens, k_tokens <= 2^24, head_dim 64 or 128, dtype
+ * bf16 or fp16.
+ *   q_lens, k_lens : DEVICE int32 [batch] or NULL (every sequence full): each sequence's
+ *                    own queries and keys, clamped to 0 .. q_tokens / k_tokens.  Rows at
+ *                    and past them are never written, and what they hold (NaN included)
+ *                    changes nothing.
+ * A non-finite value in a key or value row a sequence does own can reach every query of
+ * the 128 x 128 tiles that visit the key, also those whose mask drops it. */
+typedef struct {
+    int batch;
+    int q_heads;
+    int kv_heads;
+    int q_tokens;
+    int k_tokens;
+    int head_dim;
+    svga_dtype dtype;
+    svga_window_mask mask;
+    const int32_t *q_lens;
+    const int32_t *k_lens;
+    int32_t *status;
+} svga_window_problem;
+
+/* Workspace of the forward call (0 unless the keys are split over several CTAs because
+ * the launch has few query rows) and of the backward call.  Host-only. */
+SVGA_API svga_status svga_window_attention_size(const svga_window_problem *problem,
+                                                size_t *fwd_bytes, size_t *bwd_bytes);
+
+/* O = softmax(scale Q K^T) V over the kept keys and lse = ln sum exp (fp32, contiguous
+ * [batch, q_heads, q_tokens], or NULL).  P is rounded to the tensors' type for the P V
+ * product, everything else is fp32.  workspace: DEVICE scratch of at least fwd_bytes,
+ * 256-byte aligned (NULL when fwd_bytes is 0); calls that may overlap need one each. */
+SVGA_API svga_status svga_window_attention_fwd(const svga_view *q, const svga_view *k,
+                                               const svga_view *v, const svga_view *o, float *lse,
+                                               const svga_window_problem *problem, float scale,
+                                               void *workspace, size_t workspace_bytes,
+                                               svga_stream_t stream);
+
+/* Gradients of svga_window_attention_fwd: with P = exp(scale Q K^T - lse) on the kept
+ * pairs, D = rowsum(dO o O) and dS = P o (dO V^T - D),
+ *   dV = P^T dO,   dQ = scale dS K,   dK = scale dS^T Q,
+ * dK and dV summed over the query heads that share a key head.  o and lse are the forward
+ * call's.  P and dS are rounded to the tensors' type for the products, sums are fp32, and
+ * the order of every sum is fixed: the same inputs give the same bits.  dq, dk, dv have
+ * the shapes of q, k, v; rows past a sequence's lengths are left as they were. */
+SVGA_API svga_status svga_window_attention_bwd(const svga_view *d_o, const svga_view *q,
+                                               const svga_view *k, const svga_view *v,
+                                               const svga_view *o, const float *lse,
+                                               const svga_view *dq, const svga_view *dk,
+                                               const svga_view *dv,
+                                               const svga_window_problem *problem, float scale,
+                                               void *workspace, size_t workspace_bytes,
+                                               svga_stream_t stream);
+
 /* A paged key-value cache: k_pages and v_pages are contiguous
  * [pages, kv_heads, page_size, head_dim] of bf16 or fp16; position x of sequence b lives in
  * page page_table[b][x / page_size], row x % page_size.

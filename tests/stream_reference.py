@@ -8,7 +8,9 @@ Error bounds (u = half a step of the tensors' type, relative: bf16 2^-8, fp16 2^
   * probabilities are rounded to the tensors' type before they meet V: u relative, or in
     fp16 half its smallest step (2^-25) where that is more, with the row's sum >= 1;
   * sums in fp32 and the exponential add less than 2^-17 relative;
-  * the result is rounded once: u relative to it.
+  * the result is rounded once: u relative to it, or in fp16 half its smallest step where that
+    is more: below 2^-14 fp16 values are 2^-24 apart, so rounding moves one by up to 2^-25,
+    which u times a value below 2^-14 does not cover.
 """
 import math
 
@@ -75,9 +77,9 @@ def gradients(q, k, v, do, mask, scale):
                          zero)
     p_err = torch.where(keep, p * (u + p_rel) + tiny, zero)
     return (dq, dk, dv,
-            scale * ds_err @ k64.abs() + (u + ARITH) * dq.abs() + ARITH * scale * ds.abs() @ k64.abs(),
-            scale * ds_err.T @ q64.abs() + (u + ARITH) * dk.abs() + ARITH * scale * ds.abs().T @ q64.abs(),
-            p_err.T @ g64.abs() + (u + ARITH) * dv.abs() + ARITH * p.T @ g64.abs())
+            tiny + scale * ds_err @ k64.abs() + (u + ARITH) * dq.abs() + ARITH * scale * ds.abs() @ k64.abs(),
+            tiny + scale * ds_err.T @ q64.abs() + (u + ARITH) * dk.abs() + ARITH * scale * ds.abs().T @ q64.abs(),
+            tiny + p_err.T @ g64.abs() + (u + ARITH) * dv.abs() + ARITH * p.T @ g64.abs())
 
 
 def angles(spec, theta, place):

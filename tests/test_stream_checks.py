@@ -161,3 +161,98 @@ def test_binding_checks():
     rejected(lambda: svga.svga_cache_append(x[:, :, :3], x, pages, pages, table, lens), 2, "v has shape")
     rejected(lambda: svga.svga_cache_append(x[:, :1], x, pages, pages, table, lens), 2, "k has shape")
     rejected(lambda: svga.svga_cache_append(x, x, pages, pages, table, lens, table=t), 1, "without a RotarySpec")
+
+
+def problem(**kw):
+    d = dict(batch=2, q_heads=4, kv_heads=2, q_tokens=300, k_tokens=300, head_dim=64, dtype=0,
+             mask=svga.WindowMask().c, q_lens=None, k_lens=None, status=None)
+    d.update(kw)
+    return svga.WindowProblemC(*d.values())
+
+
+def window_calls(lib, p, scale=0.1, ws=A, n=1 << 40, lse=A, **views):
+    """Both passes with each view good unless given."""
+    def v(name, heads, tokens):
+        return ctypes.byref(views.get(name) or view(A, heads * tokens * 64, tokens * 64, 64))
+    q = {x: v(x, 4, 300) for x in ("d_o", "q", "o", "dq")}
+    k = {x: v(x, 2, 300) for x in ("k", "v", "dk", "dv")}
+    fwd = lambda: lib.svga_window_attention_fwd(q["q"], k["k"], k["v"], q["o"], lse, ctypes.byref(p), scale, ws, n, None)  # noqa: E731
+    bwd = lambda: lib.svga_window_attention_bwd(q["d_o"], q["q"], k["k"], k["v"], q["o"], lse, q["dq"], k["dk"], k["dv"],  # noqa: E731
+                                                ctypes.byref(p), scale, ws, n, None)
+    return fwd, bwd
+
+
+@pytest.mark.parametrize("kw,status,words", [
+    (dict(batch=-1), SHAPE, "batch -1"), (dict(batch=65536), SHAPE, "batch"), (dict(q_heads=5), SHAPE, "kv_heads 2"),
+    (dict(kv_heads=0), SHAPE, "kv_heads 0"), (dict(q_tokens=-1), SHAPE, "q_tokens -1"),
+    (dict(k_tokens=(1 << 24) + 1), SHAPE, "k_tokens"), (dict(head_dim=256), UNSUP, "head_dim"),
+    (dict(dtype=2), UNSUP, "dtype"), (dict(q_lens=A + 2), ALIGN, "q_lens"), (dict(k_lens=A + 1), ALIGN, "k_lens"),
+    (dict(status=A + 2), ALIGN, "status"), (dict(mask=svga.WindowMask(window=-2).c), ARG, "window -2"),
+    (dict(batch=60000, q_heads=4096, kv_heads=1), SHAPE, "do not fit one launch")])
+def test_window_problem_refusals(lib, kw, status, words):
+    p = problem(**kw)
+    for call in window_calls(lib, p):
+        refused(call(), status, words, lib)
+    refused(lib.svga_window_attention_size(ctypes.byref(p), None, None), status, words, lib)
+
+
+@pytest.mark.parametrize("name", ["d_o", "q", "k", "v", "o", "dq", "dk", "dv"])
+def test_window_view_refusals(lib, name):
+    fwd_too = name in ("q", "k", "v", "o")
+    for bad, status, words in ((view(0), ARG, "has no data"), (view(A + 8), ALIGN, "16-byte"),
+                               (view(A, 38400, 19200, 68), ALIGN, "stride of 68"),
+                               (view(A, 38400, 19200, 56), SHAPE, "below the 64 values"),
+                               (view(A, 38400, 19200, 0), SHAPE, "below the 64 values"),
+                               (view(A, -64, 19200, 64), SHAPE, "stride -64")):
+        fwd, bwd = window_calls(lib, problem(), **{name: bad})
+        refused(bwd(), status, f"{name}", lib)
+        refused(bwd(), status, words, lib)
+        if fwd_too:
+            refused(fwd(), status, words, lib)
+    fwd, bwd = window_calls(lib, problem(), **{name: view(A, 38400, 0, 64)})  # one head for all
+    if name in ("dq", "dk", "dv"):
+        refused(bwd(), ARG, "rows overlap", lib)
+    if name == "o":
+        refused(fwd(), ARG, "rows overlap", lib)
+
+
+def test_window_scale_lse_and_workspace_refusals(lib):
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        for call in window_calls(lib, problem(), scale=scale):
+            refused(call(), ARG, "scale", lib)
+    for call in window_calls(lib, problem(), lse=A + 2):
+        refused(call(), ALIGN, "lse", lib)
+    refused(window_calls(lib, problem(), lse=None)[1](), ARG, "lse is NULL", lib)
+    n = [ctypes.c_size_t() for _ in range(2)]
+    p = problem(k_tokens=100_000, batch=1, q_tokens=300)
+    assert lib.svga_window_attention_size(ctypes.byref(p), *map(ctypes.byref, n)) == OK
+    fwd, bwd = n[0].value, n[1].value
+    assert fwd > 0 and bwd > 0
+    long = {x: view(A, 1 << 30, 100_000 * 64, 64) for x in ("k", "v", "dk", "dv")}
+    for have, ws in ((fwd - 1, A), (fwd, None), (fwd, A + 128)):
+        refused(window_calls(lib, p, ws=ws, n=have, **long)[0](), WORK, "workspace", lib)
+    for have, ws in ((bwd - 1, A), (bwd, None), (bwd, A + 128)):
+        refused(window_calls(lib, p, ws=ws, n=have, **long)[1](), WORK, "workspace", lib)
+    # nothing to do: accepted without a launch, pointers not looked at
+    empty = problem(batch=0)
+    for call in window_calls(lib, empty, ws=None, n=0, lse=None):
+        assert call() == OK, lib.svga_last_error()
+
+
+def test_window_binding_checks():
+    q, k = torch.zeros(1, 4, 10, 64, dtype=torch.bfloat16), torch.zeros(1, 2, 10, 64, dtype=torch.bfloat16)
+    lse, m = torch.zeros(1, 4, 10), svga.WindowMask()
+    fwd, bwd = svga.svga_window_attention_fwd, svga.svga_window_attention_bwd
+    rejected(lambda: fwd(q[0], k, k, q, lse, m, 0.1), 2, "q must be a tensor of 4")
+    rejected(lambda: fwd(q.float(), k, k, q, lse, m, 0.1), 1, "q must be bf16 or fp16")
+    rejected(lambda: fwd(q, k.half(), k, q, lse, m, 0.1), 1, "k must be torch.bfloat16")
+    rejected(lambda: fwd(q, k, k[:, :1], q, lse, m, 0.1), 2, "v has shape")
+    rejected(lambda: fwd(q, k, k, q[:, :2], lse, m, 0.1), 2, "o has shape")
+    rejected(lambda: fwd(q, k, k, q, lse[:, :2], m, 0.1), 2, "lse has shape")
+    rejected(lambda: fwd(q, k, k, q, lse, m, 0.1, torch.zeros(2, dtype=torch.int32)), 2, "q_lens has shape")
+    rejected(lambda: fwd(q, k, k, q, lse, m, 0.1, None, torch.zeros(1)), 1, "k_lens must be")
+    rejected(lambda: fwd(q, k, k, q, None, m, 0.1), 1, "CUDA device")
+    rejected(lambda: bwd(q, q, k, k, q, None, q, k, k, m, 0.1), 1, "lse must be a torch.Tensor")
+    rejected(lambda: bwd(q, q, k, k, q, lse, q, k, k[:, :1], m, 0.1), 2, "dv has shape")
+    rejected(lambda: bwd(q, q, k, k, q, lse, k, k, k, m, 0.1), 2, "dq has shape")
+    rejected(lambda: bwd(q, q, k, k, q, lse, q, k, k, m, 0.1), 1, "CUDA device")
