@@ -531,79 +531,22 @@ def svga_unpermute_tokens_mapped(src: torch.Tensor, dst: torch.Tensor, problem: 
 
 # ---- streaming (causal) video attention: strided tensors, bf16 or fp16 ----------------
 
-DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
+_native = None
 
 
-class _Strided:
-    """The tensor arguments of one streaming call, checked for what the C ABI cannot see:
-    type, shape, values of a row contiguous, and one CUDA device for all.  Strides and
-    alignment are the library's to check.  Used as a context around the launch it makes
-    that device current, whichever was before."""
-
-    def __init__(self):
-        self.device = None
-        self.seen = []
-
-    def _add(self, t, name, dtype, shape):
-        if not isinstance(t, torch.Tensor):
-            raise SvgaError(1, f"{name} must be a torch.Tensor, got {type(t).__name__}")
-        if t.dtype != dtype:
-            raise SvgaError(1, f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise SvgaError(2, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        self.seen.append((name, t.device))
-
-    def view(self, t, name, dtype, shape) -> View:
-        """[batch, heads, tokens, head_dim]"""
-        self._add(t, name, dtype, shape)
-        sb, sh, st, sd = t.stride()
-        if sd != 1 and t.numel() > 0:
-            raise SvgaError(1, f"{name}: the values of a row must be contiguous")
-        return View(t.data_ptr(), sb, sh, st)
-
-    def flat(self, t, name, dtype, shape, optional=False):
-        """A contiguous array, or NULL where it may be left out."""
-        if t is None and optional:
-            return None
-        self._add(t, name, dtype, shape)
-        if not t.is_contiguous():
-            raise SvgaError(1, f"{name} must be contiguous")
-        return t.data_ptr()
-
-    def done(self):
-        for name, dev in self.seen:
-            if dev.type != "cuda":
-                raise SvgaError(1, f"{name} must be on a CUDA device")
-            if self.device is None:
-                self.device = dev
-            elif dev != self.device:
-                raise SvgaError(1, f"{name} is on {dev}, {self.seen[0][0]} on {self.device}")
-        return self
-
-    def stream(self, stream):
-        if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        if stream.device != self.device:
-            raise SvgaError(1, f"the stream is on {stream.device}, the tensors on {self.device}")
-        return stream.cuda_stream
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.device)
-        return self
-
-    def __exit__(self, *exc):
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.before)
-
-
-def _dtype_of(t, name, dims, f32=False):
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
-        raise SvgaError(2, f"{name} must be a tensor of {dims} dimensions")
-    if t.dtype not in DTYPES or (t.dtype == torch.float32 and not f32):
-        raise SvgaError(1, f"{name} must be bf16 or fp16{' or fp32' if f32 else ''}, got {t.dtype}")
-    return DTYPES[t.dtype]
+def _binding():
+    """The compiled marshalling of these calls (csrc/binding.cpp)."""
+    global _native
+    if _native is None:
+        if not os.path.exists(BINDING_PATH):
+            raise SvgaError(6, f"{BINDING_PATH} not built; run python -m "
+                               "block_sparse_spatio_attn_b200.build")
+        load()
+        from . import _binding as native
+        native.set_error_class(SvgaError)
+        _native = native
+    return _native
 
 
 @dataclass
@@ -624,11 +567,14 @@ class RotarySpec:
         self.c = RotarySpecC(self.num_frames, self.grid_h, self.grid_w,
                              (ctypes.c_int * 3)(*self.pairs), int(self.interleaved), self._od)
 
+        self.rows = (self.num_frames * self.pairs[0] + self.grid_h * self.pairs[1] +
+                     self.grid_w * self.pairs[2])
+        self.ordered_heads = -1 if self.order is None else len(self.order)
+
     @property
     def table_shape(self):
         """(cos, sin) rows of the table: the frame axis, then rows, then columns."""
-        return (self.num_frames * self.pairs[0] + self.grid_h * self.pairs[1] +
-                self.grid_w * self.pairs[2], 2)
+        return (self.rows, 2)
 
 
 def svga_rotary_table_size(spec: RotarySpec) -> int:
@@ -640,10 +586,7 @@ def svga_rotary_table_size(spec: RotarySpec) -> int:
 def svga_rotary_table(spec: RotarySpec, theta: float, table: torch.Tensor,
                       stream=None) -> torch.Tensor:
     """Fill table (fp32 [rows, 2], rows = spec.table_shape[0]) with the axes' cos and sin."""
-    a = _Strided()
-    pt = a.flat(table, "table", torch.float32, spec.table_shape)
-    with a.done():
-        _check(load().svga_rotary_table(ctypes.byref(spec.c), float(theta), pt, a.stream(stream)))
+    _binding().rotary_table(ctypes.addressof(spec.c), spec.rows, theta, table, stream)
     return table
 
 
@@ -651,19 +594,8 @@ def svga_rotary(src, dst, spec: RotarySpec, table, positions=None, first_token: 
                 inverse: bool = False, status=None, stream=None) -> torch.Tensor:
     """Rotate src into dst, [batch, heads, tokens, head_dim] each, strided; inverse turns
     back (the backward pass).  positions: int32 [batch, tokens], or first_token."""
-    dt = _dtype_of(src, "src", 4, f32=True)
-    B, H, T, d = src.shape
-    a = _Strided()
-    vs, vd = a.view(src, "src", src.dtype, src.shape), a.view(dst, "dst", src.dtype, src.shape)
-    pt = a.flat(table, "table", torch.float32, spec.table_shape)
-    pp = a.flat(positions, "positions", torch.int32, (B, T), optional=True)
-    ps = a.flat(status, "status", torch.int32, (1,), optional=True)
-    if spec.order is not None and len(spec.order) != H:
-        raise SvgaError(2, f"order names {len(spec.order)} heads, src has {H}")
-    with a.done():
-        _check(load().svga_rotary(ctypes.byref(vs), ctypes.byref(vd), B, H, T, d, dt,
-                                  ctypes.byref(spec.c), pt, pp, int(first_token), int(inverse),
-                                  ps, a.stream(stream)))
+    _binding().rotary(src, dst, ctypes.addressof(spec.c), spec.rows, spec.ordered_heads, table,
+                      positions, first_token, inverse, status, stream)
     return dst
 
 
@@ -680,35 +612,10 @@ class WindowMask:
         self.c = WindowMaskC(int(self.causal), self.window, self.sinks, self.block)
 
 
-def _window_problem(a: _Strided, q, k, mask, q_lens, k_lens, status) -> WindowProblemC:
-    dt = _dtype_of(q, "q", 4)
-    _dtype_of(k, "k", 4)
-    B, H, Tq, d = q.shape
-    pql = a.flat(q_lens, "q_lens", torch.int32, (B,), optional=True)
-    pkl = a.flat(k_lens, "k_lens", torch.int32, (B,), optional=True)
-    ps = a.flat(status, "status", torch.int32, (1,), optional=True)
-    return WindowProblemC(B, H, k.shape[1], Tq, k.shape[2], d, dt, mask.c, pql, pkl, ps)
-
-
-def _window_workspace(a: _Strided, workspace, need: int, stream):
-    """The caller's workspace, or one from the allocator that belongs to the call's stream."""
-    if workspace is not None:
-        a._add(workspace, "workspace", torch.uint8, workspace.shape)
-        if not workspace.is_contiguous():
-            raise SvgaError(1, "workspace must be contiguous")
-        a.done()
-        return workspace, workspace.numel()
-    if need == 0:
-        return None, 0
-    if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=a.device), need
-    with torch.cuda.stream(stream):
-        return torch.empty(need, dtype=torch.uint8, device=a.device), need
-
-
 def svga_window_attention_size(q, k, mask: WindowMask) -> dict:
     """Bytes of workspace of the forward and the backward call on tensors shaped like q and k."""
-    c = _window_problem(_Strided(), q, k, mask, None, None, None)
+    (B, H, Tq, d), (_, G, Tk, _) = q.shape, k.shape
+    c = WindowProblemC(B, H, G, Tq, Tk, d, 1 if q.dtype == torch.float16 else 0, mask.c)
     n = [ctypes.c_size_t() for _ in range(2)]
     _check(load().svga_window_attention_size(ctypes.byref(c), ctypes.byref(n[0]),
                                              ctypes.byref(n[1])))
@@ -719,21 +626,10 @@ def svga_window_attention_fwd(q, k, v, o, lse, mask: WindowMask, scale: float, q
                               k_lens=None, status=None, workspace=None,
                               stream=None) -> torch.Tensor:
     """o = softmax(scale q k^T) v under the mask, strided [batch, heads, tokens, head_dim];
-    lse: fp32 [batch, q_heads, q_tokens] or None; q_lens, k_lens: int32 [batch] or None."""
-    a = _Strided()
-    c = _window_problem(a, q, k, mask, q_lens, k_lens, status)
-    ks = (c.batch, c.kv_heads, c.k_tokens, c.head_dim)
-    vq, vk = a.view(q, "q", q.dtype, q.shape), a.view(k, "k", q.dtype, ks)
-    vv, vo = a.view(v, "v", q.dtype, ks), a.view(o, "o", q.dtype, q.shape)
-    pl = a.flat(lse, "lse", torch.float32, q.shape[:3], optional=True)
-    lib, need, rc = load(), ctypes.c_size_t(), ctypes.byref(c)
-    with a.done():
-        _check(lib.svga_window_attention_size(rc, ctypes.byref(need), None))
-        st = a.stream(stream)
-        ws, n = _window_workspace(a, workspace, need.value, stream)
-        _check(lib.svga_window_attention_fwd(ctypes.byref(vq), ctypes.byref(vk), ctypes.byref(vv),
-                                             ctypes.byref(vo), pl, rc, float(scale), _ptr(ws), n,
-                                             st))
+    lse: fp32 [batch, q_heads, q_tokens] or None; q_lens, k_lens: int32 [batch] or None;
+    workspace: uint8 of svga_window_attention_size bytes, allocated when None."""
+    _binding().window_fwd(q, k, v, o, lse, ctypes.addressof(mask.c), scale, q_lens, k_lens,
+                          status, workspace, stream)
     return o
 
 
@@ -742,36 +638,9 @@ def svga_window_attention_bwd(d_o, q, k, v, o, lse, dq, dk, dv, mask: WindowMask
                               stream=None):
     """Gradients dq, dk, dv of svga_window_attention_fwd from that of o; o and lse are the
     forward call's.  Returns (dq, dk, dv)."""
-    a = _Strided()
-    c = _window_problem(a, q, k, mask, q_lens, k_lens, status)
-    ks = (c.batch, c.kv_heads, c.k_tokens, c.head_dim)
-    views = [a.view(t, n, q.dtype, q.shape if i in "q" else ks)
-             for t, n, i in ((d_o, "d_o", "q"), (q, "q", "q"), (k, "k", "k"), (v, "v", "k"),
-                             (o, "o", "q"), (dq, "dq", "q"), (dk, "dk", "k"), (dv, "dv", "k"))]
-    pl = a.flat(lse, "lse", torch.float32, q.shape[:3])
-    lib, need, rc = load(), ctypes.c_size_t(), ctypes.byref(c)
-    with a.done():
-        _check(lib.svga_window_attention_size(rc, None, ctypes.byref(need)))
-        st = a.stream(stream)
-        ws, n = _window_workspace(a, workspace, need.value, stream)
-        p = [ctypes.byref(x) for x in views]
-        _check(lib.svga_window_attention_bwd(*p[:5], pl, *p[5:], rc, float(scale), _ptr(ws), n,
-                                             st))
+    _binding().window_bwd(d_o, q, k, v, o, lse, dq, dk, dv, ctypes.addressof(mask.c), scale,
+                          q_lens, k_lens, status, workspace, stream)
     return dq, dk, dv
-
-
-def _paged_cache(a: _Strided, k_pages, v_pages, page_table, lens, batch, status):
-    dt = _dtype_of(k_pages, "k_pages", 4)
-    n, heads, page, d = k_pages.shape
-    pk = a.flat(k_pages, "k_pages", k_pages.dtype, k_pages.shape)
-    pv = a.flat(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise SvgaError(2, "page_table must be an int32 tensor [batch, pages a sequence]")
-    most = page_table.shape[1]
-    pt = a.flat(page_table, "page_table", torch.int32, (batch, most))
-    pl = a.flat(lens, "lens", torch.int32, (batch,))
-    ps = a.flat(status, "status", torch.int32, (1,), optional=True)
-    return PagedCacheC(pk, pv, n, heads, page, d, dt, batch, most, pt, pl, ps)
 
 
 def svga_cache_append(k, v, k_pages, v_pages, page_table, lens, new_lens=None,
@@ -779,43 +648,17 @@ def svga_cache_append(k, v, k_pages, v_pages, page_table, lens, new_lens=None,
                       stream=None) -> None:
     """Write k and v ([batch, kv_heads, tokens, head_dim], strided) behind each sequence's
     end; lens counts the new rows already.  With rotary and its table, keys turn on the way."""
-    _dtype_of(k, "k", 4)
-    B, H, T, d = k.shape
-    a = _Strided()
-    c = _paged_cache(a, k_pages, v_pages, page_table, lens, B, status)
-    shape = (B, k_pages.shape[1], T, k_pages.shape[3])
-    vk, vv = a.view(k, "k", k_pages.dtype, shape), a.view(v, "v", k_pages.dtype, shape)
-    pn = a.flat(new_lens, "new_lens", torch.int32, (B,), optional=True)
-    pt = None
-    if rotary is not None:
-        pt = a.flat(table, "table", torch.float32, rotary.table_shape)
-    elif table is not None:
-        raise SvgaError(1, "a table without a RotarySpec")
-    with a.done():
-        _check(load().svga_cache_append(ctypes.byref(vk), ctypes.byref(vv), T, pn,
-                                        ctypes.byref(c),
-                                        None if rotary is None else ctypes.byref(rotary.c), pt,
-                                        a.stream(stream)))
+    _binding().cache_append(k, v, k_pages, v_pages, page_table, lens, new_lens,
+                            0 if rotary is None else ctypes.addressof(rotary.c),
+                            0 if rotary is None else rotary.rows, table, status, stream)
 
 
 def svga_cache_decode(q, k_pages, v_pages, page_table, lens, o, lse, mask: WindowMask,
                       scale: float, status=None, stream=None) -> torch.Tensor:
     """Attention of one new token per sequence over its pages.  q, o: [batch, q_heads,
     head_dim], strided; lse: fp32 [batch, q_heads] or None."""
-    _dtype_of(q, "q", 3)
-    B, H, d = q.shape
-    a = _Strided()
-    c = _paged_cache(a, k_pages, v_pages, page_table, lens, B, status)
-    shape = (B, H, 1, k_pages.shape[3])
-    if not isinstance(o, torch.Tensor) or o.dim() != 3:
-        raise SvgaError(2, "o must be a tensor of 3 dimensions")
-    vq = a.view(q.unsqueeze(2), "q", k_pages.dtype, shape)
-    vo = a.view(o.unsqueeze(2), "o", k_pages.dtype, shape)
-    pl = a.flat(lse, "lse", torch.float32, (B, H), optional=True)
-    with a.done():
-        _check(load().svga_cache_decode(ctypes.byref(vq), ctypes.byref(vo), pl, H,
-                                        ctypes.byref(c), ctypes.byref(mask.c), float(scale),
-                                        a.stream(stream)))
+    _binding().cache_decode(q, k_pages, v_pages, page_table, lens, o, lse,
+                            ctypes.addressof(mask.c), scale, status, stream)
     return o
 
 
