@@ -128,7 +128,7 @@ struct Barriers {
     uint64_t kv_empty[8];
     uint64_t s_full[2];  // [group]: that group's S is in the shared S columns
     uint64_t s_free;     // the S columns were read into registers by their owner (4 warps)
-    uint64_t s_issued[4];  // [visit % 4]: the S issuer has issued the S of that visit
+    uint64_t s_issued[8];  // [visit % 8]: the S issuer has issued the S of that visit
     uint64_t p_full[2];  // [group]: P of the group's tile is in its P columns (4 warps)
     uint64_t o_done[2];  // [group]: the group's last P V product is done
     uint64_t drain[2];   // abort: [issuer]: the MMAs that issuer started are done
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bar->o_done[i]), 1);
         }
         mbar_init(smem_u32(&bar->s_free), 4);  // one arrival per softmax warp of the owner
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bar->s_issued[i]), 1);
+        for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&bar->s_issued[i]), 1);
         mbar_init(smem_u32(&bar->drain[0]), 1);
         mbar_init(smem_u32(&bar->drain[1]), 1);
         bar->abort = 0;
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                idS, kk > 0 ? 1u : 0u);
                     mma_commit(smem_u32(&bar->s_full[c.g]));
                     if (last_of_chunk(c)) release(2 * c.n);
-                    mbar_arrive(smem_u32(&bar->s_issued[k & 3]));
+                    mbar_arrive(smem_u32(&bar->s_issued[k & 7]));
                 } else {
                     // O_g += P_g V of visit k, once the group has written P
                     if (c.n != need_chunk) {
@@ -658,16 +658,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Behind the S of visit k + 2 in the pipe: the S stream is the chain
                     // (each S waits until the previous one was read), and a P V product
                     // issued right after an S runs while that S is being read.
-                    // The S of visit m completes phase m / 4 of s_issued[m % 4].  While
+                    // The S of visit m completes phase m / 8 of s_issued[m % 8].  While
                     // this P V is not issued, the S of visit k + 5 cannot be: an S waits
                     // for the previous S to be read, which waits for its group's P
-                    // columns, which wait for that group's previous P V; so at most S of
-                    // visits up to k + 4 are issued, and the barrier of visit k + 2 is at
-                    // most one phase past the one waited for (a parity wait would take a
-                    // barrier two phases ahead for one behind).  (After its last S the S
-                    // issuer arrives for two more visits.)
-                    ok = ok && mbar_wait(smem_u32(&bar->s_issued[(k + 2) & 3]),
-                                         ((k + 2) >> 2) & 1, abort_flag);
+                    // columns, which wait for that group's previous P V.  So S of visits
+                    // up to k + 4 are issued, and behind an item's last S the issuer
+                    // arrives for two more visits: up to k + 6, less than a whole round of
+                    // the barriers past k + 2, so that a parity wait never takes a barrier
+                    // two phases ahead for one behind (with four barriers k + 6 would be
+                    // visit k + 2's next round).
+                    ok = ok && mbar_wait(smem_u32(&bar->s_issued[(k + 2) & 7]),
+                                         ((k + 2) >> 3) & 1, abort_flag);
                     tc_fence_after();
                     if (!ok) break;
                     const uint64_t b0 =
@@ -690,8 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
                 run(std::false_type{});
             if (ok && s_role) {  // the last two P V products wait for no later S
-                mbar_arrive(smem_u32(&bar->s_issued[k & 3]));
-                mbar_arrive(smem_u32(&bar->s_issued[(k + 1) & 3]));
+                mbar_arrive(smem_u32(&bar->s_issued[k & 7]));
+                mbar_arrive(smem_u32(&bar->s_issued[(k + 1) & 7]));
             }
             if (!ok) {
                 // Abort: wait for every MMA this thread issued before TMEM is freed.
