@@ -104,6 +104,42 @@ __host__ __device__ __forceinline__ ChunkList chunk_list(const Mask &m, int p0, 
     return c;
 }
 
+// --------------------------------------------------------------------------- splitting
+// Work items in launch order, the first n1 of them split k1 ways and the others k2 ways over
+// as many CTAs.  Parts of a split item leave partial sums in the workspace, in slots
+// numbered over the split items' parts in launch order.
+struct Split {
+    int items, n1, k1, k2;
+    __host__ __device__ __forceinline__ int k(int item) const { return item < n1 ? k1 : k2; }
+    __host__ __device__ __forceinline__ long long ctas() const
+    {
+        return (long long)n1 * k1 + (long long)(items - n1) * k2;
+    }
+    __device__ __forceinline__ void of_block(int blk, int &item, int &part) const
+    {
+        if (blk < n1 * k1) {
+            item = blk / k1;
+            part = blk - item * k1;
+        } else {
+            const int r = blk - n1 * k1;
+            item = n1 + r / k2;
+            part = r % k2;
+        }
+    }
+    __host__ __device__ __forceinline__ long long slot(int item, int part) const
+    {
+        if (item < n1) return (long long)item * k1 + part;
+        return (k1 > 1 ? (long long)n1 * k1 : 0) + (long long)(item - n1) * k2 + part;
+    }
+    __host__ __device__ __forceinline__ long long slots() const
+    {
+        return (k1 > 1 ? (long long)n1 * k1 : 0) + (k2 > 1 ? (long long)(items - n1) * k2 : 0);
+    }
+    // the items a join kernel has to visit: [from, to)
+    __host__ __device__ __forceinline__ int split_from() const { return k1 > 1 ? 0 : n1; }
+    __host__ __device__ __forceinline__ int split_to() const { return k2 > 1 ? items : n1; }
+};
+
 // ------------------------------------------------------------------- kernel parameters
 // A strided tensor in kernel parameters (strides in elements).
 struct View {

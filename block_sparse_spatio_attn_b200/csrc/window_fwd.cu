@@ -16,8 +16,11 @@
 //   * bf16 or fp16.  P reaches at most the tile-sum limit: 2^16 in bf16, 2^15 in fp16 (65504
 //     is its largest value); what underflows in fp16 (below 2^-24 of a sum >= 1) is lost
 //     below the rounding of O;
-//   * with few query rows the key list is split over `ksplit` CTAs that leave fp32 partial
-//     rows in the workspace, joined in a fixed order by a second kernel.
+//   * with few items for the GPU's SMs some or all key lists are split over CTAs that leave
+//     fp32 partial rows in the workspace, joined in a fixed order by a second kernel;
+//   * one query block's worth of rows (up to 128) and an even number of query heads to a key
+//     head: the two blocks of a CTA are two heads over one stream of keys;
+//   * head_dim 64 leaves TMEM for an S tile per group, so that S runs two visits ahead.
 // Query blocks are launched last first: under a causal mask those are the longest, and the
 // hardware hands CTAs out in index order.  Neighbouring CTAs are heads of one group, so
 // the K and V chunks they share meet in L2.
@@ -41,19 +44,28 @@ constexpr uint32_t kNegInfBits = 0xff800000u;
 // kRegsHigh (checked against the launch's on the host)
 constexpr int kRegsLaunch = 168, kRegsLow = 120, kRegsHigh = 192;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "register split");
-// TMEM columns: the S tile shared by the two groups, a P tile per group, an O per group
-constexpr uint32_t kTmS = 0, kTmP = 128, kTmO = 256;
+// TMEM columns: S at 0, then a P tile (64 columns) and an O per group
+// (head_dim 128: one S tile for both, head_dim 64: one each)
+template <int D>
+struct Tm {
+    static constexpr bool kTwoS = D == 64;
+    static constexpr uint32_t kS1 = kTwoS ? 128 : 0, kP = kTwoS ? 256 : 128, kO = kP + 128;
+    static constexpr uint32_t kOStep = kTwoS ? 64 : 128;
+};
 constexpr int kMinChunksPerSplit = 4;
+constexpr int kSms = 148;
 
 struct FwdParams {
     WindowShape s;
     View o;
     float *lse;
     float scale_log2;
-    int n_pairs, ksplit;
+    int n_pairs;    // items per (sequence, head or pair of heads)
+    int by_heads;   // 1: an item's two blocks are block 0 of two heads
+    Split split;    // over items, last query blocks first
     int q_mb, q_mh, k_mb, k_mh, v_mb, v_mh;  // coordinate multipliers (0: broadcast)
-    float *part_o;    // [ksplit][batch * hq * tq][d], unnormalised
-    float2 *part_ml;  // [ksplit][batch * hq * tq] (reference maximum, sum)
+    float *part_o;    // [slot][256][d], unnormalised
+    float2 *part_ml;  // [slot][256] (reference maximum, sum)
 };
 
 template <int D>
@@ -73,9 +85,10 @@ struct Cfg {
 struct Barriers {
     uint64_t q_full;
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t s_full[2];    // [group]: that group's S is in the shared S columns
-    uint64_t s_free;       // the S columns were read into registers by their owner (4 warps)
-    uint64_t s_issued[4];  // [visit % 4]: the S issuer has issued the S of that visit
+    uint64_t s_full[2];    // [group]: that group's S is in the S columns
+    uint64_t s_free[2];    // S columns were read into registers (4 warps); [group] with an S
+                           // tile each, [0] when they share one
+    uint64_t s_issued[8];  // [visit % 8]: the S issuer has issued the S of that visit
     uint64_t p_full[2];    // [group]: P of the group's tile is in its P columns (4 warps)
     uint64_t o_done[2];    // [group]: the group's last P V product is done
     uint64_t drain[2];     // abort: [issuer]: the MMAs that issuer started are done
@@ -90,6 +103,8 @@ constexpr uint32_t kV0 = 1, kF0 = 2, kV1 = 4, kF1 = 8;
 struct Item {
     int b, h, b0, nq, nk;
     bool valid1;
+    int ksplit;
+    long long slot;
     ChunkList l0, l1;
     int a, skip;  // merged list: chunks 0 .. a - 1, then skip, skip + 1, ...
     int e0, E;    // this CTA's entries
@@ -129,30 +144,37 @@ __device__ __forceinline__ int clamped_len(const int32_t *lens, int b, int most)
     return lens ? min(max(__ldg(lens + b), 0), most) : most;
 }
 
+// Item `i` in launch order: its sequence, first head and first 128-row block.
+__device__ __forceinline__ void place_item(const FwdParams &p, int i, int &b, int &h, int &b0)
+{
+    const int heads = p.by_heads ? p.s.hq / 2 : p.s.hq, bh = p.s.batch * heads;
+    const int pair = i / bh, r = i - pair * bh;
+    b = r / heads;
+    h = (r - b * heads) << p.by_heads;
+    b0 = 2 * (p.n_pairs - 1 - pair);
+}
+
 __device__ __forceinline__ bool make_item(const FwdParams &p, Item &it)
 {
-    const int bh = p.s.batch * p.s.hq;
-    const int slot = blockIdx.x / p.ksplit, part = blockIdx.x - slot * p.ksplit;
-    const int pair = p.n_pairs - 1 - slot / bh, r = slot % bh;
-    it.b = r / p.s.hq;
-    it.h = r - it.b * p.s.hq;
-    it.b0 = 2 * pair;
+    int item, part;
+    p.split.of_block(blockIdx.x, item, part);
+    place_item(p, item, it.b, it.h, it.b0);
+    it.ksplit = p.split.k(item);
+    it.slot = it.ksplit > 1 ? p.split.slot(item, part) : 0;
     it.nq = clamped_len(p.s.q_lens, it.b, p.s.tq);
     it.nk = clamped_len(p.s.k_lens, it.b, p.s.tk);
     const int off = it.nk - it.nq, r0 = it.b0 * kBlockM;
     if (r0 >= it.nq) return false;
-    it.valid1 = r0 + kBlockM < it.nq;
-    it.l0 = chunk_list<kKN>(p.s.mask, r0 + off, min(r0 + kBlockM, it.nq) - 1 + off, it.nk);
-    if (it.valid1)
+    it.l0 = it.l1 = chunk_list<kKN>(p.s.mask, r0 + off, min(r0 + kBlockM, it.nq) - 1 + off, it.nk);
+    it.valid1 = p.by_heads || r0 + kBlockM < it.nq;
+    if (!p.by_heads && it.valid1)
         it.l1 = chunk_list<kKN>(p.s.mask, r0 + kBlockM + off,
                                 min(r0 + 2 * kBlockM, it.nq) - 1 + off, it.nk);
-    else
-        it.l1 = it.l0;
     int end;
     merge_lists(it.l0, it.l1, it.valid1, it.a, it.skip, end);
     const long long all = it.a + end - it.skip;
-    it.e0 = (int)(part * all / p.ksplit);
-    it.E = (int)((part + 1) * all / p.ksplit) - it.e0;
+    it.e0 = (int)(part * all / it.ksplit);
+    it.E = (int)((part + 1) * all / it.ksplit) - it.e0;
     return true;
 }
 
@@ -169,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tmV, const FwdParams p)
 {
     using C = Cfg<D>;
+    using T = Tm<D>;
     constexpr float kSumLimit = F16 ? 32768.f : 65536.f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -192,12 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bar->s_full[i]), 1);
+            mbar_init(smem_u32(&bar->s_free[i]), 4);
             mbar_init(smem_u32(&bar->p_full[i]), 4);
             mbar_init(smem_u32(&bar->o_done[i]), 1);
             mbar_init(smem_u32(&bar->drain[i]), 1);
         }
-        mbar_init(smem_u32(&bar->s_free), 4);
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bar->s_issued[i]), 1);
+        for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&bar->s_issued[i]), 1);
         mbar_init(smem_u32(&bar->zero_req), 1);
         mbar_init(smem_u32(&bar->zero_done), 1);
         bar->abort = 0;
@@ -222,7 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < nq_tiles; ++i)
                 for (int c = 0; c < D / 64; ++c)
                     tma_load_4d(smem_u32(sQ + i * C::kQBytes + c * C::kQChunk), &tmQ, qf, 64 * c,
-                                (it.b0 + i) * kBlockM, it.h * p.q_mh, it.b * p.q_mb);
+                                (it.b0 + (p.by_heads ? 0 : i)) * kBlockM,
+                                (it.h + (p.by_heads ? i : 0)) * p.q_mh, it.b * p.q_mb);
             int issued = 0;
             bool ok = true;
             for (int n = 0; n < it.E && ok; ++n) {
@@ -269,7 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(smem_u32(&bar->kv_empty[idx % C::kStages]));
             };
             // the visits: (entry n, group g), entries ascending, group 0 before group 1
-            int n = 0, k = 0, pvn0 = 0, pvn1 = 0;
+            // k: visits done, gn: of each group
+            int n = 0, k = 0, gn0 = 0, gn1 = 0;
             auto run = [&](auto role_tag) {
                 constexpr bool kSRole = decltype(role_tag)::value;
                 for (; ok && n < it.E; ++n) {
@@ -282,8 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool last = g == 1 || !(f & kV1);
                         if constexpr (kSRole) {
                             // once the owner of the previous visit has read its S
-                            if (k > 0 && !(ok = mbar_wait(smem_u32(&bar->s_free), (k - 1) & 1,
-                                                          abort_flag)))
+                            const int before = T::kTwoS ? (g ? gn1 : gn0) : k;
+                            if (before > 0 &&
+                                !(ok = mbar_wait(smem_u32(&bar->s_free[T::kTwoS ? g : 0]),
+                                                 (before - 1) & 1, abort_flag)))
                                 break;
                             tc_fence_after();
                             if (!waited && !(ok = wait_full(2 * n))) break;
@@ -293,13 +320,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 dK + (kv_addr + ((2 * n) % C::kStages) * (C::kKVBytes >> 4));
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk)
-                                mma_ss(tmem + kTmS,
+                                mma_ss(tmem + g * T::kS1,
                                        a0 + (uint32_t)(((kk >> 2) * C::kQChunk + (kk & 3) * 32) >> 4),
                                        b0 + (uint32_t)(((kk >> 2) * C::kKVChunk + (kk & 3) * 32) >> 4),
                                        idS, kk > 0 ? 1u : 0u);
                             mma_commit(smem_u32(&bar->s_full[g]));
                             if (last) release(2 * n);
-                            mbar_arrive(smem_u32(&bar->s_issued[k & 3]));
+                            mbar_arrive(smem_u32(&bar->s_issued[k & 7]));
+                            (g ? gn1 : gn0)++;
                         } else {
                             if (!waited) {
                                 if (!(ok = wait_full(2 * n + 1))) break;
@@ -310,20 +338,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                                 waited = true;
                             }
-                            int &pvn = g ? pvn1 : pvn0;
+                            int &pvn = g ? gn1 : gn0;
                             ok = mbar_wait(smem_u32(&bar->p_full[g]), pvn & 1, abort_flag);
-                            // right behind the S two visits ahead, where it runs while that S
-                            // is being read (attention.cu has the argument that the barrier
-                            // is never two phases off)
-                            ok = ok && mbar_wait(smem_u32(&bar->s_issued[(k + 2) & 3]),
-                                                 ((k + 2) >> 2) & 1, abort_flag);
+                            // Right behind the S two visits ahead, where it runs while that S
+                            // is being read.  The S of visit m completes phase m / 8 of
+                            // s_issued[m % 8].  While this P V (visit k) is not issued, a
+                            // group can have read the S of at most one visit past the one
+                            // whose P it wrote last, and with an S tile of its own have one
+                            // more issued: S runs to visit k + 4 at most (k + 2, k + 3 and
+                            // k + 4 when the other group has the last two), and the two
+                            // arrivals behind the last S reach k + 6, below k + 2 + 8: a
+                            // parity wait is never a whole round behind.
+                            ok = ok && mbar_wait(smem_u32(&bar->s_issued[(k + 2) & 7]),
+                                                 ((k + 2) >> 3) & 1, abort_flag);
                             tc_fence_after();
                             if (!ok) break;
                             const uint64_t b0 =
                                 dV + (kv_addr + ((2 * n + 1) % C::kStages) * (C::kKVBytes >> 4));
 #pragma unroll
                             for (int kk = 0; kk < kKN / 16; ++kk)
-                                mma_ts(tmem + kTmO + g * 128, tmem + kTmP + g * 64 + kk * 8,
+                                mma_ts(tmem + T::kO + g * T::kOStep, tmem + T::kP + g * 64 + kk * 8,
                                        b0 + (uint32_t)(kk * (2048 >> 4)), idO,
                                        (pvn != 0 || kk > 0) ? 1u : 0u);
                             mma_commit(smem_u32(&bar->o_done[g]));
@@ -339,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
                 run(std::false_type{});
             if (ok && s_role) {  // the last two P V products wait for no later S
-                mbar_arrive(smem_u32(&bar->s_issued[k & 3]));
-                mbar_arrive(smem_u32(&bar->s_issued[(k + 1) & 3]));
+                mbar_arrive(smem_u32(&bar->s_issued[k & 7]));
+                mbar_arrive(smem_u32(&bar->s_issued[(k + 1) & 7]));
             }
             if (!ok) {
                 // abort: wait for every MMA this thread issued before TMEM is freed
@@ -371,10 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         setmaxnreg_inc<kRegsHigh>();
         const int wg = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-        const uint32_t tS = tmem + lane_base + kTmS;
-        const uint32_t tP = tmem + lane_base + kTmP + wg * 64;
-        const uint32_t tO = tmem + lane_base + kTmO + wg * 128;
-        const int qrow = (it.b0 + wg) * kBlockM + row;
+        const uint32_t tS = tmem + lane_base + wg * T::kS1;
+        const uint32_t tP = tmem + lane_base + T::kP + wg * 64;
+        const uint32_t tO = tmem + lane_base + T::kO + wg * T::kOStep;
+        const int qrow = (it.b0 + (p.by_heads ? 0 : wg)) * kBlockM + row;
         const bool row_valid = qrow < it.nq;
         MaskRange mr = {0, 0, 0};
         if (row_valid) mr = mask_range(p.s.mask, qrow + it.nk - it.nq, it.nk);
@@ -396,9 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < kKN / 32; ++j)
                 tmem_ld32(tS + j * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[j * 32]));
             tmem_wait_ld();
-            tc_fence_before();  // S is in registers: its columns may take the next visit's
+            tc_fence_before();  // S is in registers: its columns may take another visit's
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar->s_free));
+            if (lane == 0) mbar_arrive(smem_u32(&bar->s_free[T::kTwoS ? wg : 0]));
             if (!(f & fbit)) {
                 const int k0 = chunk * kKN;
 #pragma unroll
@@ -487,13 +521,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_wait(smem_u32(&bar->o_done[wg]), (visit - 1) & 1, abort_flag));
             tc_fence_after();
         }
-        const bool split = p.ksplit > 1;
+        const bool split = it.ksplit > 1;
         if (ok && (wg == 0 || it.valid1)) {
             const float inv = split ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-            const long long flat = ((long long)it.b * p.s.hq + it.h) * p.s.tq + qrow;
-            const long long part =
-                (long long)(blockIdx.x % p.ksplit) * p.s.batch * p.s.hq * p.s.tq + flat;
-            char *orow = p.o.p + 2 * (it.b * p.o.sb + it.h * p.o.sh + qrow * p.o.st);
+            const int h = it.h + (p.by_heads ? wg : 0);
+            const long long flat = ((long long)it.b * p.s.hq + h) * p.s.tq + qrow;
+            const long long part = it.slot * 2 * kBlockM + wg * kBlockM + row;
+            char *orow = p.o.p + 2 * (it.b * p.o.sb + h * p.o.sh + qrow * p.o.st);
 #pragma unroll 1
             for (int j = 0; j < D / 32; ++j) {
                 uint32_t o[32];
@@ -543,28 +577,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicExch(p.s.status, (int32_t)SVGA_ERR_TIMEOUT);
 }
 
-// Join of a split launch: one thread per 8 values of a row; the parts' maxima give the
+// Join of the split items: one thread per 8 values of a row; the parts' maxima give the
 // common scale, sums run in part order.  A part that saw no key of the row has l = 0.
 template <bool F16>
 __global__ void __launch_bounds__(256) join_kernel(const FwdParams p, int d)
 {
     const int per = d / 8;
-    const long long rows = (long long)p.s.batch * p.s.hq * p.s.tq;
     const long long i = blockIdx.x * 256ll + threadIdx.x;
-    if (i >= rows * per) return;
-    const long long row = i / per, bh = row / p.s.tq;
-    const int c = 8 * (int)(i - row * per), t = (int)(row - bh * p.s.tq);
-    const int b = (int)(bh / p.s.hq), h = (int)(bh - (long long)b * p.s.hq);
+    const long long all = i / per;
+    const int c = 8 * (int)(i - all * per), row = (int)(all % (2 * kBlockM));
+    const long long it = p.split.split_from() + all / (2 * kBlockM);
+    if (it >= p.split.split_to()) return;
+    const int item = (int)it, k = p.split.k(item);
+    int b, h, b0;
+    place_item(p, item, b, h, b0);
+    const int g = row / kBlockM;
+    h += p.by_heads ? g : 0;
+    const int t = (b0 + (p.by_heads ? 0 : g)) * kBlockM + row % kBlockM;
     if (t >= clamped_len(p.s.q_lens, b, p.s.tq)) return;
+    const long long at = p.split.slot(item, 0) * 2 * kBlockM + row;
+    constexpr int kStep = 2 * kBlockM;  // rows from one part's slot to the next
     float m = -INFINITY;
-    for (int r = 0; r < p.ksplit; ++r) m = fmaxf(m, __ldg(&p.part_ml[r * rows + row].x));
+#pragma unroll 4
+    for (int r = 0; r < k; ++r) m = fmaxf(m, __ldg(&p.part_ml[at + r * kStep].x));
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int r = 0; r < p.ksplit; ++r) {
-        const float2 ml = __ldg(&p.part_ml[r * rows + row]);
+    for (int r = 0; r < k; ++r) {
+        const float2 ml = __ldg(&p.part_ml[at + r * kStep]);
         const float4 *src =
-            reinterpret_cast<const float4 *>(p.part_o + (r * rows + row) * d + c);
+            reinterpret_cast<const float4 *>(p.part_o + (at + r * kStep) * d + c);
         const float4 u = __ldg(src), v = __ldg(src + 1);
         const float w = exp2f(ml.x - ref);
         l += w * ml.y;
@@ -580,25 +622,65 @@ __global__ void __launch_bounds__(256) join_kernel(const FwdParams p, int d)
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint32_t y[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = pack_16x2<F16>(x[2 * k] * inv, x[2 * k + 1] * inv);
+    for (int j = 0; j < 4; ++j) y[j] = pack_16x2<F16>(x[2 * j] * inv, x[2 * j + 1] * inv);
     *reinterpret_cast<uint4 *>(p.o.p + 2 * (b * p.o.sb + h * p.o.sh + t * p.o.st + c)) =
         make_uint4(y[0], y[1], y[2], y[3]);
     if (c == 0 && p.lse)
-        p.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+        p.lse[((long long)b * p.s.hq + h) * p.s.tq + t] =
+            l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
 }
 
-// CTAs a key list is split over: one unless the launch has fewer than half as many items as
-// the GPU has SMs, then as many as fill the SMs once while every part keeps
-// kMinChunksPerSplit chunks of the longest list the shapes allow.
-int choose_split(const svga_window_problem *p)
+// Two heads a CTA: one query block of rows would leave the second group idle (and its S
+// product's latency uncovered).
+bool pair_heads(const svga_window_problem *p)
 {
-    const long long items = (long long)p->batch * p->q_heads * ((p->q_tokens + 255) / 256);
-    if (items == 0 || 2 * items > 148) return 1;
+    return p->q_tokens <= kBlockM && (p->q_heads / p->kv_heads) % 2 == 0;
+}
+
+// Which items are split, from the shapes alone.  An item is `len` chunks long (the longest
+// and the mean over its query blocks); the GPU runs kSms items at a time.
+//   * less than one round of items: all split, to fill it once;
+//   * items of about one length: those behind the last whole round are split to fill one
+//     (12,480 tokens of 4 heads, 196 equal items: TAIL_FIGURES);
+//   * a causal list without a window, where lengths run from 1 to the longest: the longest
+//     items, launched first, are split in two when one alone would take over half of the
+//     whole launch's time.
+// From four rounds on the last one costs less than the partial sums.  A part keeps at least
+// kMinChunksPerSplit chunks.
+Split choose_split(const svga_window_problem *p)
+{
+    const long long pairs = (p->q_tokens + 2 * kBlockM - 1) / (2 * kBlockM);
+    const long long n = (long long)p->batch * (pair_heads(p) ? p->q_heads / 2 : p->q_heads) * pairs;
+    Split s = {(int)n, (int)n, 1, 1};
+    if (n == 0 || n >= 4 * kSms || p->k_tokens == 0) return s;
     const Mask m = to_mask(p->mask);
-    const int last = p->k_tokens - 1, first = std::max(last - std::min(p->q_tokens, 256) + 1, 0);
-    const ChunkList c = chunk_list<kKN>(m, first, last, p->k_tokens);
-    const int chunks = c.a + std::max(c.w1 - std::max(c.a, c.w0), 0);
-    return (int)std::max(1ll, std::min(148 / items, (long long)chunks / kMinChunksPerSplit));
+    const int off = p->k_tokens - p->q_tokens;
+    long long longest = 0, sum = 0;
+    for (int i = 0; i < pairs; ++i) {
+        const int r0 = i * 2 * kBlockM, r1 = std::min(r0 + 2 * kBlockM, p->q_tokens) - 1;
+        const ChunkList c = chunk_list<kKN>(m, r0 + off, r1 + off, p->k_tokens);
+        const int len = c.a + std::max(c.w1 - std::max(c.a, c.w0), 0);
+        longest = std::max<long long>(longest, len);
+        sum += len;
+    }
+    const long long most = std::max(1ll, longest / kMinChunksPerSplit);
+    if (n < kSms) {
+        s.k1 = (int)std::min<long long>(kSms / n, most);
+        return s;
+    }
+    if (5 * sum >= 4 * longest * pairs) {  // mean at least 0.8 of the longest
+        const int tail = (int)(n % kSms);
+        if (tail == 0) return s;
+        s.n1 = (int)n - tail;
+        s.k2 = (int)std::min<long long>(kSms / tail, most);
+        return s;
+    }
+    const double per_sm = (double)sum / pairs * n / kSms;  // chunks
+    if (2 * longest > per_sm && most > 1) {
+        s.n1 = (int)(n / 2);
+        s.k1 = 2;
+    }
+    return s;
 }
 
 template <int D, bool F16>
@@ -635,11 +717,11 @@ svga_status launch(const svga_view &q, const svga_view &k, const svga_view &v, F
         set_error("cudaFuncSetAttribute(max dynamic shared memory) failed");
         return SVGA_ERR_CUDA;
     }
-    const long long grid = (long long)p->batch * p->q_heads * kp.n_pairs * kp.ksplit;
-    kfn<<<(unsigned)grid, kThreads, C::kSmemLaunch, st>>>(tq, tk, tv, kp);
+    kfn<<<(unsigned)kp.split.ctas(), kThreads, C::kSmemLaunch, st>>>(tq, tk, tv, kp);
     svga_status rc = check_launch_of("window attention");
-    if (rc != SVGA_OK || kp.ksplit == 1) return rc;
-    const long long n = (long long)p->batch * p->q_heads * p->q_tokens * (D / 8);
+    if (rc != SVGA_OK || kp.split.slots() == 0) return rc;
+    const long long n = (long long)(kp.split.split_to() - kp.split.split_from()) * 2 * kBlockM *
+                        (D / 8);
     join_kernel<F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp, D);
     return check_launch_of("window attention join");
 }
@@ -648,10 +730,7 @@ svga_status launch(const svga_view &q, const svga_view &k, const svga_view &v, F
 
 size_t window_fwd_workspace(const svga_window_problem *p)
 {
-    const int split = choose_split(p);
-    if (split == 1) return 0;
-    const size_t rows = (size_t)p->batch * p->q_heads * p->q_tokens;
-    return (size_t)split * rows * (p->head_dim * 4 + 8);
+    return (size_t)choose_split(p).slots() * 2 * kBlockM * (p->head_dim * 4 + 8);
 }
 
 svga_status launch_window_fwd(const svga_view &q, const svga_view &k, const svga_view &v,
@@ -664,12 +743,11 @@ svga_status launch_window_fwd(const svga_view &q, const svga_view &k, const svga
     kp.lse = lse;
     kp.scale_log2 = scale * kLog2e;
     kp.n_pairs = (p->q_tokens + 2 * kBlockM - 1) / (2 * kBlockM);
-    kp.ksplit = choose_split(p);
-    if (kp.ksplit > 1) {
-        const size_t rows = (size_t)p->batch * p->q_heads * p->q_tokens;
-        kp.part_o = static_cast<float *>(ws);
-        kp.part_ml = reinterpret_cast<float2 *>(kp.part_o + kp.ksplit * rows * p->head_dim);
-    }
+    kp.by_heads = pair_heads(p);
+    kp.split = choose_split(p);
+    kp.part_o = static_cast<float *>(ws);
+    kp.part_ml = reinterpret_cast<float2 *>(kp.part_o + (size_t)kp.split.slots() * 2 * kBlockM *
+                                                            p->head_dim);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (p->head_dim == 128)
         return p->dtype == SVGA_F16 ? launch<128, true>(q, k, v, kp, p, st)

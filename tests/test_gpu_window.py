@@ -149,12 +149,25 @@ def test_split_key_lists(B, H, G, nq, nk):
         k_lens = [nk - 700 * b for b in range(B)]
         o, lse = forward(q, k, v, mask, 0.125, q_lens, k_lens)
         check(q, k, v, mask, 0.125, o, lse, q_lens, k_lens)
-        assert (size > 0) == (2 * B * H * -(-nq // 256) <= 148)
+        assert size > 0
     need = svga.svga_window_attention_size(q, k, M())["fwd_bytes"]
     small = torch.empty(max(need - 1, 0), dtype=torch.uint8, device="cuda")
     with pytest.raises(svga.SvgaError) as e:
         forward(q, k, v, M(), 0.125, workspace=small)
     assert e.value.status == 5
+
+
+@pytest.mark.parametrize("mask,dtype", [(M(window=700, sinks=100), BF), (M(), FP)], ids=str)
+def test_launches_split_in_part(mask, dtype):
+    """160 items for 148 SMs: the last ones split (lists of one length), the first ones split
+    (a causal list without a window).  Three heads are compared."""
+    q = values(1, 10, 4000, 64, dtype=dtype)
+    k, v = (values(1, 5, 4000, 64, dtype=dtype, seed=s) for s in (1, 2))
+    assert svga.svga_window_attention_size(q, k, mask)["fwd_bytes"] > 0
+    o, lse = forward(q, k, v, mask, 0.125)
+    for h in (0, 5, 9):
+        g = h // 2
+        check(q[:, h:h + 1], k[:, g:g + 1], v[:, g:g + 1], mask, 0.125, o[:, h:h + 1], lse[:, h:h + 1])
 
 
 def test_scores_far_apart():

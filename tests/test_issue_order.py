@@ -83,7 +83,8 @@ def ring_of(source):
     return int(re.search(r"uint64_t s_issued\[(\d+)\]", text).group(1))
 
 
-@pytest.mark.parametrize("source,own_s_tiles", [("attention.cu", False)])
+@pytest.mark.parametrize("source,own_s_tiles", [("attention.cu", False), ("window_fwd.cu", False),
+                                                ("window_fwd.cu", True)])
 def test_no_order_leaves_a_role_waiting(source, own_s_tiles):
     rng = random.Random(1)
     ring = ring_of(source)
