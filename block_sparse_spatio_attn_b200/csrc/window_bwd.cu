@@ -16,14 +16,27 @@
 // dkdv works on transposed tiles, S^T = K Q^T and dP^T = V dO^T (TMEM lane = key), so that P^T
 // and dS^T are in place as the A operands of dV += P^T dO and dK += dS^T Q: nothing is
 // transposed through shared memory.  TMEM: S^T | dP^T | dV | dK, 128 columns each; P^T and
-// dS^T are written over the first half of what each softmax group read of S^T and dP^T.  All
-// four products are issued by one thread in the order
-//   ... dV(i), S(i+1), dK(i), dP(i+1), ...
-// so while the softmax threads turn S(i+1) into P(i+1) the tensor pipe runs dK(i) and
-// dP(i+1), and while they turn dP(i+1) into dS(i+1) it runs dV(i+1) and S(i+2).
-// dq has room for two S tiles (S0 | S1 | dP | dQ): S runs a chunk ahead.
-// In both, warps 4-7 and 8-11 hold a lane's columns 0-63 and 64-127; P stays in registers
-// in fp32 between the two steps of a tile.
+// dS^T are written over the first half of what each softmax group read of S^T and dP^T.
+//
+// Warps 4-7 (group A) hold a lane's columns 0-63, warps 8-11 (B) columns 64-127, P staying in
+// registers in fp32 between the two steps of a tile.
+//
+// What bounds them.  A product of 128 x 128 tiles with both operands in shared memory reads
+// 128 bytes a cycle there, all it has, so that barrier operations and loads of the other
+// threads take some 200 cycles beside it; an issuing thread that waits before every product
+// leaves the tensor pipe idle between them (one issuer: 2,870 cycles a step of dq, 967 of
+// them in waits).  So
+//   * two threads issue, each the products of its own accumulators and tiles (dkdv: dV and S^T,
+//     dK and dP^T; dq: S, dQ and dP), and each waits for its loads before it waits for the
+//     softmax threads;
+//   * dkdv: a step's S^T cannot be computed before the last P^T is used up, and no TMEM is
+//     left for a second tile.  The groups are therefore two chains of their own (barriers,
+//     products of 64 columns or 64 terms each): while one waits, the other has the
+//     exponential unit and the tensor pipe;
+//   * dq: S | dP0 | dP1 | dQ in TMEM: S is computed again as soon as it was read, dP a step
+//     ahead, so no step waits for its products;
+//   * three stages of Q (dkdv) and of K (dq), which are needed longest, and two of the other
+//     operand fill shared memory with the resident tiles.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -59,17 +72,18 @@ struct Cfg {
     static constexpr int kTile = kT * D * 2;   // a 128-row tile of Q, K, V or dO
     static constexpr int kChunk = kT * 128;    // 64 columns of it
     static constexpr int kStats = 2 * kT * 4;  // a query block's statistics
-    // dkdv: K, V, two stages of Q and dO with their statistics
-    static constexpr int kKvStages = 2;
-    static constexpr int kKvData = 2 * kTile + kKvStages * (2 * kTile + kStats);
+    // dkdv: K, V, three stages of Q, two of dO with the block's statistics
+    static constexpr int kQStages = 3, kOStages = 2;
+    static constexpr int kKvData = (2 + kQStages + kOStages) * kTile + kOStages * kStats;
     // dq: Q, dO, three stages of K, two of V
     static constexpr int kKStages = 3, kVStages = 2;
     static constexpr int kDqData = (2 + kKStages + kVStages) * kTile;
     static constexpr int kBars = 512;
-    // one CTA per SM (each takes the whole TMEM): never less than half the shared memory
+    // one CTA per SM (each takes the whole TMEM): never less than half the shared memory.
+    // No room is left to align the base by hand: the kernels check it.
     static constexpr int alloc(int data)
     {
-        return data + kBars + 1024 < 120 * 1024 ? 120 * 1024 : data + kBars + 1024;
+        return data + kBars < 120 * 1024 ? 120 * 1024 : data + kBars;
     }
     static constexpr int kKvAlloc = alloc(kKvData), kDqAlloc = alloc(kDqData);
     static_assert(kKvAlloc <= 227 * 1024 && kDqAlloc <= 227 * 1024, "shared memory budget");
@@ -176,7 +190,30 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane)
             st_shared_v4(tile + c * Cfg<D>::kChunk + u * 16, 0u, 0u, 0u, 0u);
 }
 
-// One product of a 128 x N tile over 128 (A in TMEM) or D (A in shared memory) terms.
+// Columns 64 g .. 64 g + 63 of a 128 x 128 product over D terms, both operands in shared
+// memory: b's rows 64 g and up.
+template <int D>
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, int g, uint32_t id)
+{
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t at = ((kk >> 2) * Cfg<D>::kChunk + (kk & 3) * 32) >> 4;
+        mma_ss(d + 64 * g, a + at, b + at + g * (64 * 128 >> 4), id, kk > 0 ? 1u : 0u);
+    }
+}
+
+// A 128 x D product over terms 64 g .. 64 g + 63: a holds them as packed 16-bit pairs in
+// columns 64 g .. 64 g + 31, b's rows are the terms.
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, int g, uint32_t id,
+                                           bool accumulate)
+{
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+        mma_ts(d, a + 64 * g + 8 * kk, b + (uint32_t)((4 * g + kk) * (2048 >> 4)), id,
+               (accumulate || kk > 0) ? 1u : 0u);
+}
+
+// The same, all 128 columns and all 128 terms.
 template <int D>
 __device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id)
 {
@@ -187,25 +224,33 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, u
     }
 }
 
-// A: 128 terms as packed 16-bit pairs, terms 0-63 in columns a .. a + 31, 64-127 in a + 64 ..
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
                                            bool accumulate)
 {
-#pragma unroll
-    for (int kk = 0; kk < kT / 16; ++kk)
-        mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + (uint32_t)(kk * (2048 >> 4)), id,
-               (accumulate || kk > 0) ? 1u : 0u);
+    product_ts(d, a, b, 0, id, accumulate);
+    product_ts(d, a, b, 1, id, true);
+}
+
+// The base of the dynamic shared memory, on the 1024-byte boundary the swizzle needs.  The
+// runtime places it there; should it ever not, the kernel reports instead of computing.
+__device__ __forceinline__ bool smem_misplaced(const void *base, int32_t *status)
+{
+    if ((smem_u32(base) & 1023u) == 0) return false;
+    if (threadIdx.x == 0 && status) atomicCAS(status, 0, (int32_t)SVGA_ERR_ALIGNMENT);
+    return true;
 }
 
 // ----------------------------------------------------------------------------- dkdv
 struct KvBars {
     uint64_t kv_full;
-    uint64_t q_full[2], q_empty[2];  // stages of Q, dO and their statistics
-    uint64_t s_full, dp_full;        // S^T / dP^T of a step is in TMEM
-    uint64_t p_ready, ds_ready;      // P^T / dS^T is (8 warps)
-    uint64_t acc_done;               // every product is done
-    uint64_t drain;
-    uint64_t zero_req, zero_done;
+    uint64_t q_full[3], q_empty[3];      // stages of Q
+    uint64_t o_full[2], o_empty[2];      // stages of dO
+    uint64_t st_full[2], st_empty[2];    // of the statistics (needed longer than dO)
+    uint64_t s_full[2], dp_full[2];      // [group]: its columns of S^T / dP^T are in TMEM
+    uint64_t p_ready[2], ds_ready[2];    // [group]: its P^T / dS^T is (4 warps)
+    uint64_t acc_done;                   // every product is done (both issuers)
+    uint64_t drain[2];
+    uint64_t zero_req[2], zero_done[2];  // Q, dO
     uint32_t tmem_base;
     int abort;
 };
@@ -219,13 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using C = Cfg<D>;
     constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_misplaced(smem, p.s.status)) return;
     uint8_t *sK = smem, *sV = smem + C::kTile;
-    uint8_t *sQ = smem + 2 * C::kTile;                       // [stage]
-    uint8_t *sO = sQ + C::kKvStages * C::kTile;              // [stage]
-    uint8_t *sStats = sO + C::kKvStages * C::kTile;          // [stage]
+    uint8_t *sQ = smem + 2 * C::kTile;              // [stage]
+    uint8_t *sO = sQ + C::kQStages * C::kTile;      // [stage]
+    uint8_t *sStats = sO + C::kOStages * C::kTile;  // [stage]
     KvBars *bar = reinterpret_cast<KvBars *>(smem + C::kKvData);
     volatile int *abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -249,18 +293,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bar->kv_full), 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kQStages; ++i) {
             mbar_init(smem_u32(&bar->q_full[i]), 1);
             mbar_init(smem_u32(&bar->q_empty[i]), 1);
         }
-        mbar_init(smem_u32(&bar->s_full), 1);
-        mbar_init(smem_u32(&bar->dp_full), 1);
-        mbar_init(smem_u32(&bar->p_ready), 8);
-        mbar_init(smem_u32(&bar->ds_ready), 8);
-        mbar_init(smem_u32(&bar->acc_done), 1);
-        mbar_init(smem_u32(&bar->drain), 1);
-        mbar_init(smem_u32(&bar->zero_req), 1);
-        mbar_init(smem_u32(&bar->zero_done), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar->o_full[i]), 1);
+            mbar_init(smem_u32(&bar->o_empty[i]), 2);  // dV and dP of the step are done
+            mbar_init(smem_u32(&bar->st_full[i]), 1);
+            mbar_init(smem_u32(&bar->st_empty[i]), 1);
+            mbar_init(smem_u32(&bar->s_full[i]), 1);
+            mbar_init(smem_u32(&bar->dp_full[i]), 1);
+            mbar_init(smem_u32(&bar->p_ready[i]), 4);
+            mbar_init(smem_u32(&bar->ds_ready[i]), 4);
+            mbar_init(smem_u32(&bar->zero_req[i]), 1);
+            mbar_init(smem_u32(&bar->zero_done[i]), 1);
+            mbar_init(smem_u32(&bar->drain[i]), 1);
+        }
+        mbar_init(smem_u32(&bar->acc_done), 2);
         bar->abort = 0;
         fence_barrier_init();
     }
@@ -285,25 +335,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_4d(smem_u32(sV + c * C::kChunk), &tmV, kvf, 64 * c, k0, hk * p.v_mh,
                             b * p.v_mb);
             }
-            int issued = 0, g = 0, blk = 0;
+            int q_issued = 0, o_issued = 0, st_issued = 0, g = 0, blk = 0;
             for (int i = 0; i < steps; ++i) {
-                const int s = i & 1, round = i >> 1;
-                if (round > 0 &&
-                    !mbar_wait(smem_u32(&bar->q_empty[s]), (round - 1) & 1, abort_flag))
-                    break;
-                const uint32_t fb = smem_u32(&bar->q_full[s]);
                 const int h = hk * p.s.group + g, row = (qb0 + blk) * kT;
-                mbar_arrive_expect_tx(fb, 2 * C::kTile + C::kStats);
-                for (int c = 0; c < D / 64; ++c) {
-                    tma_load_4d(smem_u32(sQ + s * C::kTile + c * C::kChunk), &tmQ, fb, 64 * c, row,
+                const int qs = i % C::kQStages, os = i % C::kOStages;
+                const int qr = i / C::kQStages, orr = i / C::kOStages;
+                if (qr > 0 && !mbar_wait(smem_u32(&bar->q_empty[qs]), (qr - 1) & 1, abort_flag))
+                    break;
+                uint32_t fb = smem_u32(&bar->q_full[qs]);
+                mbar_arrive_expect_tx(fb, C::kTile);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem_u32(sQ + qs * C::kTile + c * C::kChunk), &tmQ, fb, 64 * c, row,
                                 h * p.q_mh, b * p.q_mb);
-                    tma_load_4d(smem_u32(sO + s * C::kTile + c * C::kChunk), &tmO, fb, 64 * c, row,
+                q_issued = i + 1;
+                if (orr > 0 && !mbar_wait(smem_u32(&bar->o_empty[os]), (orr - 1) & 1, abort_flag))
+                    break;
+                fb = smem_u32(&bar->o_full[os]);
+                mbar_arrive_expect_tx(fb, C::kTile);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem_u32(sO + os * C::kTile + c * C::kChunk), &tmO, fb, 64 * c, row,
                                 h * p.o_mh, b * p.o_mb);
-                }
-                bulk_load(smem_u32(sStats + s * C::kStats),
+                o_issued = i + 1;
+                if (orr > 0 && !mbar_wait(smem_u32(&bar->st_empty[os]), (orr - 1) & 1, abort_flag))
+                    break;
+                fb = smem_u32(&bar->st_full[os]);
+                mbar_arrive_expect_tx(fb, C::kStats);
+                bulk_load(smem_u32(sStats + os * C::kStats),
                           p.stats + (((long long)b * p.s.hq + h) * p.n_qblk + qb0 + blk) * 2 * kT,
                           C::kStats, fb);
-                issued = i + 1;
+                st_issued = i + 1;
                 if (++blk == n_blk) {
                     blk = 0;
                     ++g;
@@ -311,72 +371,118 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every copy lands before the CTA can exit, whichever role aborts
             mbar_wait_bounded(kvf, 0);
-            for (int i = max(issued - 2, 0); i < issued; ++i)
-                mbar_wait_bounded(smem_u32(&bar->q_full[i & 1]), (i >> 1) & 1);
-        } else if (warp == 1 && lane == 0 && steps > 0) {
-            // ---------------------------------------------------------- MMA issuer
-            constexpr uint32_t idS = idesc_16_f32(F16, kT, kT, 0, 0);
+            for (int i = max(q_issued - C::kQStages, 0); i < q_issued; ++i)
+                mbar_wait_bounded(smem_u32(&bar->q_full[i % C::kQStages]), (i / C::kQStages) & 1);
+            for (int i = max(o_issued - C::kOStages, 0); i < o_issued; ++i)
+                mbar_wait_bounded(smem_u32(&bar->o_full[i % C::kOStages]), (i / C::kOStages) & 1);
+            for (int i = max(st_issued - C::kOStages, 0); i < st_issued; ++i)
+                mbar_wait_bounded(smem_u32(&bar->st_full[i % C::kOStages]), (i / C::kOStages) & 1);
+        } else if ((warp == 1 || warp == 3) && lane == 0 && steps > 0) {
+            // --------------------------------------------------------- MMA issuers
+            // warp 1: S^T and dV, warp 3: dP^T and dK.  Each accumulator and tile belongs to
+            // one of them, so its products stay in order.
+            const int role = warp == 3;
+            constexpr uint32_t idS = idesc_16_f32(F16, kT, 64, 0, 0);
             constexpr uint32_t idA = idesc_16_f32(F16, kT, D, 0, 1);
             const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);         // rows of terms
             const uint64_t nmaj = smem_desc_sw128(0, C::kChunk, 1024);  // terms down the rows
-            const uint32_t aK = smem_u32(sK) >> 4, aV = smem_u32(sV) >> 4;
             const uint32_t aQ = smem_u32(sQ) >> 4, aO = smem_u32(sO) >> 4;
-            int blk = 0;  // block of the next step whose stage is taken in
-            auto take = [&](int i) {  // stage of step i has landed and is clean
-                bool ok = mbar_wait(smem_u32(&bar->q_full[i & 1]), (i >> 1) & 1, abort_flag);
-                if (ok && blk == ragged) {  // warp 2 clears the rows past the end
-                    const int time = i / n_blk;
-                    mbar_arrive(smem_u32(&bar->zero_req));
-                    ok = mbar_wait(smem_u32(&bar->zero_done), time & 1, abort_flag);
+            // the stage of step i has landed (w: 0 Q, 1 dO)
+            auto landed = [&](int i, int w) {
+                return w ? mbar_wait(smem_u32(&bar->o_full[i % C::kOStages]),
+                                     (i / C::kOStages) & 1, abort_flag)
+                         : mbar_wait(smem_u32(&bar->q_full[i % C::kQStages]),
+                                     (i / C::kQStages) & 1, abort_flag);
+            };
+            int blk[2] = {0, 0}, cleaned[2] = {0, 0};  // walks of Q's and dO's steps
+            // landed, and its rows past the sequence's end are 0 (asked of warp 2 once, by the
+            // issuer whose first product on the stage it is)
+            auto take = [&](int i, int w, bool ask) {
+                if (!landed(i, w)) return false;
+                const bool dirty = blk[w] == ragged;
+                if (++blk[w] == n_blk) blk[w] = 0;
+                if (!dirty) return true;
+                if (ask) mbar_arrive(smem_u32(&bar->zero_req[w]));
+                return mbar_wait(smem_u32(&bar->zero_done[w]), cleaned[w]++ & 1, abort_flag);
+            };
+            auto q_at = [&](int i) { return aQ + (i % C::kQStages) * (C::kTile >> 4); };
+            auto o_at = [&](int i) { return aO + (i % C::kOStages) * (C::kTile >> 4); };
+            bool ok = mbar_wait(smem_u32(&bar->kv_full), 0, abort_flag) && take(0, role, true);
+            if (role == 0) {
+                const uint64_t a = kmaj + (smem_u32(sK) >> 4);
+                auto issue = [&](int i, int g) {
+                    product_ss<D>(tmem + kS, a, kmaj + q_at(i), g, idS);
+                    mma_commit(smem_u32(&bar->s_full[g]));
+                };
+                if (ok) {
+                    issue(0, 0);
+                    issue(0, 1);
                 }
-                if (++blk == n_blk) blk = 0;
-                return ok;
-            };
-            auto issue_s = [&](int i) {
-                product_ss<D>(tmem + kS, kmaj + aK, kmaj + aQ + (i & 1) * (C::kTile >> 4), idS);
-                mma_commit(smem_u32(&bar->s_full));
-            };
-            auto issue_dp = [&](int i) {
-                product_ss<D>(tmem + kDP, kmaj + aV, kmaj + aO + (i & 1) * (C::kTile >> 4), idS);
-                mma_commit(smem_u32(&bar->dp_full));
-            };
-            bool ok = mbar_wait(smem_u32(&bar->kv_full), 0, abort_flag) && take(0);
-            if (ok) {
-                issue_s(0);
-                issue_dp(0);
-            }
-            for (int i = 0; ok && i < steps; ++i) {
-                const uint32_t st = (i & 1) * (C::kTile >> 4);
-                if (!(ok = mbar_wait(smem_u32(&bar->p_ready), i & 1, abort_flag))) break;
-                tc_fence_after();
-                product_ts(tmem + kDV, tmem + kS, nmaj + aO + st, idA, i > 0);
-                if (i + 1 < steps) {
-                    if (!(ok = take(i + 1))) break;
-                    issue_s(i + 1);
+                for (int i = 0; ok && i < steps; ++i) {
+                    const bool next = i + 1 < steps;
+                    ok = take(i, 1, false) && (!next || take(i + 1, 0, true));
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (!ok || !(ok = mbar_wait(smem_u32(&bar->p_ready[g]), i & 1, abort_flag)))
+                            break;
+                        tc_fence_after();
+                        product_ts(tmem + kDV, tmem + kS, nmaj + o_at(i), g, idA, i > 0 || g > 0);
+                        if (g == 1) mma_commit(smem_u32(&bar->o_empty[i % C::kOStages]));
+                        if (next) issue(i + 1, g);
+                    }
                 }
-                if (!(ok = mbar_wait(smem_u32(&bar->ds_ready), i & 1, abort_flag))) break;
-                tc_fence_after();
-                product_ts(tmem + kDK, tmem + kDP, nmaj + aQ + st, idA, i > 0);
-                mma_commit(smem_u32(&bar->q_empty[i & 1]));
-                if (i + 1 < steps) issue_dp(i + 1);
+            } else {
+                const uint64_t a = kmaj + (smem_u32(sV) >> 4);
+                auto issue = [&](int i, int g) {
+                    product_ss<D>(tmem + kDP, a, kmaj + o_at(i), g, idS);
+                    mma_commit(smem_u32(&bar->dp_full[g]));
+                    if (g == 1) mma_commit(smem_u32(&bar->o_empty[i % C::kOStages]));
+                };
+                if (ok) {
+                    issue(0, 0);
+                    issue(0, 1);
+                }
+                for (int i = 0; ok && i < steps; ++i) {
+                    const bool next = i + 1 < steps;
+                    ok = landed(i, 0) && (!next || take(i + 1, 1, true));
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (!ok ||
+                            !(ok = mbar_wait(smem_u32(&bar->ds_ready[g]), i & 1, abort_flag)))
+                            break;
+                        tc_fence_after();
+                        product_ts(tmem + kDK, tmem + kDP, nmaj + q_at(i), g, idA, i > 0 || g > 0);
+                        if (g == 1) {  // the last to use the step's Q; the statistics were read
+                            mma_commit(smem_u32(&bar->q_empty[i % C::kQStages]));
+                            mma_commit(smem_u32(&bar->st_empty[i % C::kOStages]));
+                        }
+                        if (next) issue(i + 1, g);
+                    }
+                }
             }
             if (ok) {
                 mma_commit(smem_u32(&bar->acc_done));
             } else {
-                mma_commit(smem_u32(&bar->drain));
-                mbar_wait_bounded(smem_u32(&bar->drain), 0);
+                mma_commit(smem_u32(&bar->drain[role]));
+                mbar_wait_bounded(smem_u32(&bar->drain[role]), 0);
             }
         } else if (warp == 2 && ragged >= 0) {
             // ------------------------ rows of Q and dO past the sequence's end read as 0
             for (int g = 0; g < p.s.group; ++g) {
-                const bool ok = mbar_wait(smem_u32(&bar->zero_req), g & 1, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                const int s = (g * n_blk + ragged) & 1;
-                zero_rows<D>(smem_u32(sQ + s * C::kTile), nq % kT, lane);
-                zero_rows<D>(smem_u32(sO + s * C::kTile), nq % kT, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar->zero_done));
+                bool ok = true;
+                for (int w = 0; w < 2 && ok; ++w) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(smem_u32(&bar->zero_req[w]), g & 1, abort_flag));
+                    if (!ok) break;
+                    const int i = g * n_blk + ragged;
+                    zero_rows<D>(smem_u32(w ? sO + (i % C::kOStages) * C::kTile
+                                            : sQ + (i % C::kQStages) * C::kTile),
+                                 nq % kT, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar->zero_done[w]));
+                }
+                if (!ok) break;
             }
         }
     } else {
@@ -402,15 +508,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c0 = ra - r0 - 64 * wg, c1 = re - r0 - 64 * wg;
             uint32_t keep[2] = {bits_below(c1) & ~bits_below(c0),
                                 bits_below(c1 - 32) & ~bits_below(c0 - 32)};
-            const float4 *nl = reinterpret_cast<const float4 *>(sStats + (i & 1) * C::kStats) +
+            const float4 *nl = reinterpret_cast<const float4 *>(
+                                   sStats + (i % C::kOStages) * C::kStats) +
                                16 * wg;
             uint32_t x[64];
             float pr[64];
-            // the statistics are read here: this thread waits for their copy itself (it has
-            // landed, the issuer waited for it before S)
             ok = __all_sync(0xffffffffu,
-                            mbar_wait(smem_u32(&bar->s_full), i & 1, abort_flag) &&
-                                mbar_wait(smem_u32(&bar->q_full[i & 1]), (i >> 1) & 1, abort_flag));
+                            mbar_wait(smem_u32(&bar->s_full[wg]), i & 1, abort_flag) &&
+                                mbar_wait(smem_u32(&bar->st_full[i % C::kOStages]),
+                                          (i / C::kOStages) & 1, abort_flag));
             tc_fence_after();
             if (!ok) break;
             tmem_ld64(tS, x);
@@ -442,9 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar->p_ready));
+            if (lane == 0) mbar_arrive(smem_u32(&bar->p_ready[wg]));
 
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->dp_full), i & 1, abort_flag));
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(smem_u32(&bar->dp_full[wg]), i & 1, abort_flag));
             tc_fence_after();
             if (!ok) break;
             tmem_ld64(tDP, x);
@@ -477,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar->ds_ready));
+            if (lane == 0) mbar_arrive(smem_u32(&bar->ds_ready[wg]));
         }
         // ------------------------------- epilogue: group 0 stores dV, group 1 dK
         if (ok && steps > 0) {
@@ -505,9 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct DqBars {
     uint64_t q_full;
     uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
-    uint64_t s_full[2], dp_full;  // S of a step (two tiles), dP
-    uint64_t ds_ready;            // dS (8 warps); implies S and dP were read
-    uint64_t acc_done, drain;
+    uint64_t s_full, s_free;   // S of a step is in TMEM, was read into registers (8 warps)
+    uint64_t dp_full[2];       // dP of an even / odd step
+    // dS (8 warps) of an even / odd step, over the dP it came from.  Two barriers: a warp can
+    // be done with step i + 1, whose S and dP do not wait for dS(i), before another with i;
+    // i + 2 needs dS(i) of all.
+    uint64_t ds_ready[2];
+    uint64_t acc_done, drain[2];
     uint64_t zero_req, zero_done;
     uint32_t tmem_base;
     int abort;
@@ -521,10 +632,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const BwdParams p)
 {
     using C = Cfg<D>;
-    constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                ~uintptr_t(1023));
+    constexpr uint32_t kS = 0, kDP = 128, kDQ = 384;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_misplaced(smem, p.s.status)) return;
     uint8_t *sQ = smem, *sO = smem + C::kTile;
     uint8_t *sK = smem + 2 * C::kTile;               // [stage]
     uint8_t *sV = sK + C::kKStages * C::kTile;       // [stage]
@@ -556,12 +666,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bar->v_full[i]), 1);
             mbar_init(smem_u32(&bar->v_empty[i]), 1);
-            mbar_init(smem_u32(&bar->s_full[i]), 1);
+            mbar_init(smem_u32(&bar->dp_full[i]), 1);
+            mbar_init(smem_u32(&bar->ds_ready[i]), 8);
+            mbar_init(smem_u32(&bar->drain[i]), 1);
         }
-        mbar_init(smem_u32(&bar->dp_full), 1);
-        mbar_init(smem_u32(&bar->ds_ready), 8);
+        mbar_init(smem_u32(&bar->s_full), 1);
+        mbar_init(smem_u32(&bar->s_free), 8);
         mbar_init(smem_u32(&bar->acc_done), 1);
-        mbar_init(smem_u32(&bar->drain), 1);
         mbar_init(smem_u32(&bar->zero_req), 1);
         mbar_init(smem_u32(&bar->zero_done), 1);
         bar->abort = 0;
@@ -615,52 +726,67 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait_bounded(smem_u32(&bar->k_full[i % C::kKStages]), (i / C::kKStages) & 1);
             for (int i = max(v_issued - C::kVStages, 0); i < v_issued; ++i)
                 mbar_wait_bounded(smem_u32(&bar->v_full[i % C::kVStages]), (i / C::kVStages) & 1);
-        } else if (warp == 1 && lane == 0 && E > 0) {
-            // ---------------------------------------------------------- MMA issuer
+        } else if ((warp == 1 || warp == 3) && lane == 0 && E > 0) {
+            // --------------------------------------------------------- MMA issuers
+            // warp 1: S, warp 3: dP and dQ
+            const int role = warp == 3;
             constexpr uint32_t idS = idesc_16_f32(F16, kT, kT, 0, 0);
             constexpr uint32_t idA = idesc_16_f32(F16, kT, D, 0, 1);
             const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);
             const uint64_t nmaj = smem_desc_sw128(0, C::kChunk, 1024);
-            const uint32_t aQ = smem_u32(sQ) >> 4, aO = smem_u32(sO) >> 4;
             const uint32_t aK = smem_u32(sK) >> 4, aV = smem_u32(sV) >> 4;
-            auto issue_s = [&](int i) {
-                const int ks = i % C::kKStages;
-                if (!mbar_wait(smem_u32(&bar->k_full[ks]), (i / C::kKStages) & 1, abort_flag))
-                    return false;
-                if (chunk_of(i) == ragged) {  // warp 2 clears the keys past the end
-                    mbar_arrive(smem_u32(&bar->zero_req));
-                    if (!mbar_wait(smem_u32(&bar->zero_done), 0, abort_flag)) return false;
+            auto k_landed = [&](int i) {
+                return mbar_wait(smem_u32(&bar->k_full[i % C::kKStages]), (i / C::kKStages) & 1,
+                                 abort_flag);
+            };
+            auto k_at = [&](int i) { return aK + (i % C::kKStages) * (C::kTile >> 4); };
+            bool ok = mbar_wait(smem_u32(&bar->q_full), 0, abort_flag);
+            if (role == 0) {
+                const uint64_t a = kmaj + (smem_u32(sQ) >> 4);
+                for (int i = 0; ok && i < E; ++i) {
+                    if (!(ok = k_landed(i))) break;
+                    if (chunk_of(i) == ragged) {  // warp 2 clears the keys past the end
+                        mbar_arrive(smem_u32(&bar->zero_req));
+                        if (!(ok = mbar_wait(smem_u32(&bar->zero_done), 0, abort_flag))) break;
+                    }
+                    if (i > 0) {
+                        if (!(ok = mbar_wait(smem_u32(&bar->s_free), (i - 1) & 1, abort_flag)))
+                            break;
+                        tc_fence_after();
+                    }
+                    product_ss<D>(tmem + kS, a, kmaj + k_at(i), idS);
+                    mma_commit(smem_u32(&bar->s_full));
                 }
-                product_ss<D>(tmem + kS + 128 * (i & 1), kmaj + aQ,
-                              kmaj + aK + ks * (C::kTile >> 4), idS);
-                mma_commit(smem_u32(&bar->s_full[i & 1]));
-                return true;
-            };
-            auto issue_dp = [&](int i) {
-                const int vs = i % C::kVStages;
-                if (!mbar_wait(smem_u32(&bar->v_full[vs]), (i / C::kVStages) & 1, abort_flag))
-                    return false;
-                product_ss<D>(tmem + kDP, kmaj + aO, kmaj + aV + vs * (C::kTile >> 4), idS);
-                mma_commit(smem_u32(&bar->dp_full));
-                mma_commit(smem_u32(&bar->v_empty[vs]));
-                return true;
-            };
-            bool ok = mbar_wait(smem_u32(&bar->q_full), 0, abort_flag) && issue_s(0) &&
-                      issue_dp(0) && (E < 2 || issue_s(1));
-            for (int i = 0; ok && i < E; ++i) {
-                if (!(ok = mbar_wait(smem_u32(&bar->ds_ready), i & 1, abort_flag))) break;
-                tc_fence_after();
-                const int ks = i % C::kKStages;
-                product_ts(tmem + kDQ, tmem + kDP, nmaj + aK + ks * (C::kTile >> 4), idA, i > 0);
-                mma_commit(smem_u32(&bar->k_empty[ks]));
-                if (i + 1 < E && !(ok = issue_dp(i + 1))) break;
-                if (i + 2 < E && !(ok = issue_s(i + 2))) break;
-            }
-            if (ok) {
-                mma_commit(smem_u32(&bar->acc_done));
             } else {
-                mma_commit(smem_u32(&bar->drain));
-                mbar_wait_bounded(smem_u32(&bar->drain), 0);
+                const uint64_t a = kmaj + (smem_u32(sO) >> 4);
+                auto v_landed = [&](int i) {
+                    return mbar_wait(smem_u32(&bar->v_full[i % C::kVStages]),
+                                     (i / C::kVStages) & 1, abort_flag);
+                };
+                auto issue = [&](int i) {
+                    const int vs = i % C::kVStages;
+                    product_ss<D>(tmem + kDP + 128 * (i & 1), a, kmaj + aV + vs * (C::kTile >> 4),
+                                  idS);
+                    mma_commit(smem_u32(&bar->dp_full[i & 1]));
+                    mma_commit(smem_u32(&bar->v_empty[vs]));
+                };
+                for (int i = 0; ok && i < min(E, 2); ++i)
+                    if ((ok = v_landed(i))) issue(i);
+                for (int i = 0; ok && i < E; ++i) {
+                    const bool next = i + 2 < E;
+                    ok = k_landed(i) && (!next || v_landed(i + 2)) &&
+                         mbar_wait(smem_u32(&bar->ds_ready[i & 1]), (i >> 1) & 1, abort_flag);
+                    tc_fence_after();
+                    if (!ok) break;
+                    product_ts(tmem + kDQ, tmem + kDP + 128 * (i & 1), nmaj + k_at(i), idA, i > 0);
+                    mma_commit(smem_u32(&bar->k_empty[i % C::kKStages]));
+                    if (next) issue(i + 2);
+                }
+                if (ok) mma_commit(smem_u32(&bar->acc_done));
+            }
+            if (!ok) {
+                mma_commit(smem_u32(&bar->drain[role]));
+                mbar_wait_bounded(smem_u32(&bar->drain[role]), 0);
             }
         } else if (warp == 2 && ragged >= 0) {
             // ------------------------------- keys past the sequence's end read as 0
@@ -702,11 +828,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t x[64];
             float pr[64];
             ok = __all_sync(0xffffffffu,
-                            mbar_wait(smem_u32(&bar->s_full[i & 1]), (i >> 1) & 1, abort_flag));
+                            mbar_wait(smem_u32(&bar->s_full), i & 1, abort_flag));
             tc_fence_after();
             if (!ok) break;
-            tmem_ld64(tS + 128 * (i & 1), x);
+            tmem_ld64(tS, x);
             tmem_wait_ld();
+            tc_fence_before();  // S is in registers: its columns may take the next step's
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar->s_free));
             if (!full) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
@@ -719,10 +848,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pr[j] = fast_exp2(u.x);
                 pr[j + 1] = fast_exp2(u.y);
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->dp_full), i & 1, abort_flag));
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(smem_u32(&bar->dp_full[i & 1]), (i >> 1) & 1, abort_flag));
             tc_fence_after();
             if (!ok) break;
-            tmem_ld64(tDP, x);
+            tmem_ld64(tDP + 128 * (i & 1), x);
             tmem_wait_ld();
             {
                 uint32_t pk[32];
@@ -740,12 +870,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[j] &= ((k2 & 1u) ? 0xffffu : 0u) | ((k2 & 2u) ? 0xffff0000u : 0u);
                     }
                 }
-                tmem_st32(tDP, pk);
+                tmem_st32(tDP + 128 * (i & 1), pk);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar->ds_ready));
+            if (lane == 0) mbar_arrive(smem_u32(&bar->ds_ready[i & 1]));
         }
         // ------------------------------------ epilogue: each group half the columns
         if (ok && E > 0) {
