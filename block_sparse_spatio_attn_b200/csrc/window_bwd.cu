@@ -7,7 +7,9 @@
 //   rows    D and lse of every query row in the exp2 domain, negated, 1 KB per 128 rows;
 //   dkdv    one CTA per 128 keys of a key head; walks the query blocks that keep any of
 //           them, over all query heads of the group, with dK and dV in TMEM throughout, so
-//           shared heads are summed without atomics and the order is fixed;
+//           shared heads are summed without atomics and the order is fixed.  Sinks, which
+//           every later query keeps, and launches of few key blocks are split over CTAs
+//           that leave fp32 sums in the workspace, added in order by a join kernel;
 //   dq      one CTA per 128 queries; walks their key chunks with dQ in TMEM.
 // S and dO V^T are computed in both: 7 products instead of the 5 a single pass needs.  The
 // single pass would add each dQ tile into memory from every CTA: 64 KB of fp32 atomics a
@@ -43,6 +45,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "stream.h"
 #include "svga_device.cuh"
@@ -52,6 +55,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kT = 128;  // rows and keys of a tile
+constexpr int kSms = 148;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kNegInfBits = 0xff800000u;
 constexpr int kRegsLaunch = 168, kRegsLow = 96, kRegsHigh = 200;
@@ -63,7 +67,9 @@ struct BwdParams {
     const float *lse;
     float *stats;  // [batch * hq][query block][2][128]: -lse log2(e), -D
     float scale, scale_log2;
-    int n_qblk, n_kblk, d;
+    int n_qblk, n_kblk;
+    Split split;   // over dkdv's items, key blocks ascending
+    float *parts;  // [slot][dV, dK][128][d]
     int q_mb, q_mh, o_mb, o_mh, k_mb, k_mh, v_mb, v_mh;  // coordinate multipliers (o: dO)
 };
 
@@ -180,6 +186,27 @@ __device__ __forceinline__ void store_row(uint32_t taddr, char *dst, float f, bo
     }
 }
 
+template <int NCOL>
+__device__ __forceinline__ void store_part(uint32_t taddr, float *dst, bool any)
+{
+#pragma unroll 1
+    for (int j = 0; j < NCOL / 32; ++j) {
+        uint32_t o[32];
+        if (any) {
+            tmem_ld32(taddr + j * 32, o);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = 0u;
+        }
+        if (!dst) continue;
+        uint4 *to = reinterpret_cast<uint4 *>(dst + 32 * j);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            to[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+    }
+}
+
 // Rows [first, 128) of a swizzled 128-row tile read as 0 (whole rows: the swizzle permutes
 // inside a row's 128 bytes).
 template <int D>
@@ -275,8 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // this CTA's keys, and the query blocks that keep any of them
+    int item, part;
+    p.split.of_block(blockIdx.x, item, part);
+    const int ksplit = p.split.k(item);
     const int bh = p.s.batch * p.s.hk;
-    const int kblk = blockIdx.x / bh, r = blockIdx.x - kblk * bh;
+    const int kblk = item / bh, r = item - kblk * bh;
     const int b = r / p.s.hk, hk = r - b * p.s.hk;
     const int nq = clamped_len(p.s.q_lens, b, p.s.tq), nk = clamped_len(p.s.k_lens, b, p.s.tk);
     const int k0 = kblk * kT, k1 = min(k0 + kT, nk), off = nk - nq;
@@ -286,7 +316,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mask_rows(p.s.mask, k1 - 1, nq, off, x, end1);
     end = max(end, end1);
     const int qb0 = first / kT, n_blk = end > first ? (end + kT - 1) / kT - qb0 : 0;
-    const int steps = n_blk * p.s.group;
+    // steps run over the group's heads and their blocks; this CTA takes its part of them
+    const long long all = (long long)n_blk * p.s.group;
+    const int first_step = (int)(part * all / ksplit);
+    const int steps = (int)((part + 1) * all / ksplit) - first_step;
+    const int g0 = n_blk > 0 ? first_step / n_blk : 0, blk0 = first_step - g0 * n_blk;
     // the query block whose last rows lie past the sequence's end but inside the tensor
     const int ragged =
         (p.s.q_lens && nq < p.s.tq && nq % kT && nq / kT == qb0 + n_blk - 1) ? n_blk - 1 : -1;
@@ -335,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_4d(smem_u32(sV + c * C::kChunk), &tmV, kvf, 64 * c, k0, hk * p.v_mh,
                             b * p.v_mb);
             }
-            int q_issued = 0, o_issued = 0, st_issued = 0, g = 0, blk = 0;
+            int q_issued = 0, o_issued = 0, st_issued = 0, g = g0, blk = blk0;
             for (int i = 0; i < steps; ++i) {
                 const int h = hk * p.s.group + g, row = (qb0 + blk) * kT;
                 const int qs = i % C::kQStages, os = i % C::kOStages;
@@ -394,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : mbar_wait(smem_u32(&bar->q_full[i % C::kQStages]),
                                      (i / C::kQStages) & 1, abort_flag);
             };
-            int blk[2] = {0, 0}, cleaned[2] = {0, 0};  // walks of Q's and dO's steps
+            int blk[2] = {blk0, blk0}, cleaned[2] = {0, 0};  // walks of Q's and dO's steps
             // landed, and its rows past the sequence's end are 0 (asked of warp 2 once, by the
             // issuer whose first product on the stage it is)
             auto take = [&](int i, int w, bool ask) {
@@ -468,13 +502,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 2 && ragged >= 0) {
             // ------------------------ rows of Q and dO past the sequence's end read as 0
-            for (int g = 0; g < p.s.group; ++g) {
+            int time = 0;
+            for (int i = ragged - blk0 + (ragged < blk0 ? n_blk : 0); i < steps;
+                 i += n_blk, ++time) {
                 bool ok = true;
                 for (int w = 0; w < 2 && ok; ++w) {
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(smem_u32(&bar->zero_req[w]), g & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->zero_req[w]), time & 1,
+                                                           abort_flag));
                     if (!ok) break;
-                    const int i = g * n_blk + ragged;
                     zero_rows<D>(smem_u32(w ? sO + (i % C::kOStages) * C::kTile
                                             : sQ + (i % C::kQStages) * C::kTile),
                                  nq % kT, lane);
@@ -497,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (key < nk) mask_rows(p.s.mask, key, nq, off, ra, re);
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
-        int blk = 0;
+        int blk = blk0;
         for (int i = 0; i < steps; ++i) {
             const int r0 = (qb0 + blk) * kT;
             if (++blk == n_blk) blk = 0;
@@ -591,7 +626,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->acc_done), 0, abort_flag));
             tc_fence_after();
         }
-        if (ok) {
+        if (ok && ksplit > 1) {
+            float *dst = key < nk ? p.parts + ((p.split.slot(item, part) * 2 + wg) * kT + row) * D
+                                  : nullptr;
+            store_part<D>(tmem + lane_base + (wg ? kDK : kDV), dst, steps > 0);
+        } else if (ok) {
             const View &w = wg ? p.dk : p.dv;
             char *dst = key < nk ? w.p + 2 * (b * w.sb + hk * w.sh + key * w.st) : nullptr;
             store_row<D, F16>(tmem + lane_base + (wg ? kDK : kDV), dst, wg ? p.scale : 1.f,
@@ -606,6 +645,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 0 && bar->abort && p.s.status)
         atomicExch(p.s.status, (int32_t)SVGA_ERR_TIMEOUT);
+}
+
+// Adds the parts of dkdv's split items in part order: one thread per 8 values of a row.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) bwd_join_kernel(const BwdParams p)
+{
+    constexpr int kPer = D / 8;
+    const long long i = blockIdx.x * 256ll + threadIdx.x;
+    const int c = 8 * (int)(i % kPer);
+    const long long row_all = i / kPer;
+    const int row = (int)(row_all % kT), w = (int)(row_all / kT % 2);
+    const long long it = p.split.split_from() + row_all / (2 * kT);
+    if (it >= p.split.split_to()) return;
+    const int item = (int)it, k = p.split.k(item);
+    const int bh = p.s.batch * p.s.hk;
+    const int kblk = item / bh, r = item - kblk * bh;
+    const int b = r / p.s.hk, hk = r - b * p.s.hk, key = kblk * kT + row;
+    if (key >= clamped_len(p.s.k_lens, b, p.s.tk)) return;
+    const float *src = p.parts + ((p.split.slot(item, 0) * 2 + w) * kT + row) * D + c;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) {
+        const float4 u = __ldg(reinterpret_cast<const float4 *>(src + (long long)j * 2 * kT * D));
+        const float4 v =
+            __ldg(reinterpret_cast<const float4 *>(src + (long long)j * 2 * kT * D) + 1);
+        x[0] += u.x;
+        x[1] += u.y;
+        x[2] += u.z;
+        x[3] += u.w;
+        x[4] += v.x;
+        x[5] += v.y;
+        x[6] += v.z;
+        x[7] += v.w;
+    }
+    const float f = w ? p.scale : 1.f;
+    uint32_t y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = pack_16x2<F16>(x[2 * j] * f, x[2 * j + 1] * f);
+    const View &to = w ? p.dk : p.dv;
+    *reinterpret_cast<uint4 *>(to.p + 2 * (b * to.sb + hk * to.sh + key * to.st + c)) =
+        make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 // ------------------------------------------------------------------------------- dq
@@ -950,9 +1030,15 @@ svga_status launch(const svga_view &d_o, const svga_view &q, const svga_view &k,
         if ((rc = check_launch_of("window backward rows")) != SVGA_OK) return rc;
     }
     if (hk) {
-        const unsigned grid = (unsigned)((long long)p->batch * p->kv_heads * kp.n_kblk);
+        const unsigned grid = (unsigned)kp.split.ctas();
         bwd_dkdv_kernel<D, F16><<<grid, kThreads, C::kKvAlloc, st>>>(tq, to, tk, tv, kp);
         if ((rc = check_launch_of("window dK/dV")) != SVGA_OK) return rc;
+        if (kp.split.slots() > 0) {
+            const long long n =
+                (long long)(kp.split.split_to() - kp.split.split_from()) * 2 * kT * (D / 8);
+            bwd_join_kernel<D, F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp);
+            if ((rc = check_launch_of("window dK/dV join")) != SVGA_OK) return rc;
+        }
     }
     if (hq) {
         const unsigned grid = (unsigned)((long long)p->batch * p->q_heads * kp.n_qblk);
@@ -969,10 +1055,71 @@ View to_view(const svga_view &v)
 
 }  // namespace
 
-size_t window_bwd_workspace(const svga_window_problem *p)
+static size_t stats_bytes(const svga_window_problem *p)
 {
     const size_t blocks = (size_t)(p->q_tokens + kT - 1) / kT;
     return (size_t)p->batch * p->q_heads * blocks * 2 * kT * sizeof(float);
+}
+
+// How dkdv's items are split.  Items are key blocks; the ones that hold sinks, first in launch
+// order, are kept by every later query of a causal mask, the others by a window of them.
+// `per_sm` is the launch's steps divided by the SMs: an item longer than that holds up the
+// whole launch.  With fewer items than SMs parts are as short as still fit in one round of
+// CTAs; otherwise an item is split when it is longer than per_sm (sinks: 3/4 of it, they are
+// launched first and the rest fills in behind them).  Measured: FIGURES_DKDV.
+static Split choose_bwd_split(const svga_window_problem *p)
+{
+    const long long heads = (long long)p->batch * p->kv_heads;
+    const int blocks = (p->k_tokens + kT - 1) / kT, group = p->q_heads / p->kv_heads;
+    const long long n = heads * blocks;
+    Split s = {(int)n, 0, 1, 1};
+    if (n == 0 || p->q_tokens == 0) return s;
+    const Mask m = to_mask(p->mask);
+    const int sinks = m.window >= 0 ? std::min((std::min(m.sinks, p->k_tokens) + kT - 1) / kT, blocks) : 0;
+    const int off = p->k_tokens - p->q_tokens;
+    auto steps_of = [&](int kb) {
+        const int k0 = kb * kT, k1 = std::min(k0 + kT, p->k_tokens);
+        int first, end, x, end1;
+        mask_rows(m, k0, p->q_tokens, off, first, end);
+        mask_rows(m, k1 - 1, p->q_tokens, off, x, end1);
+        end = std::max(end, end1);
+        return end > first ? (long long)group * ((end + kT - 1) / kT - first / kT) : 0ll;
+    };
+    // the longest and the mean of either kind, over at most 256 blocks of each
+    long long top[2] = {0, 0};
+    double mean[2] = {0, 0};
+    for (int w = 0; w < 2; ++w) {
+        const int from = w ? sinks : 0, to = w ? blocks : sinks, stride = (to - from) / 256 + 1;
+        int count = 0;
+        for (int kb = from; kb < to; kb += stride, ++count) {
+            const long long x = steps_of(kb);
+            top[w] = std::max(top[w], x);
+            mean[w] += x;
+        }
+        mean[w] /= std::max(count, 1);
+    }
+    const double per_sm = heads * (sinks * mean[0] + (blocks - sinks) * mean[1]) / kSms;
+    auto parts = [](long long x, double most) {
+        return (int)std::max(1ll, std::min(64ll, (long long)std::ceil(x / most)));
+    };
+    s.n1 = (int)(heads * sinks);
+    if (n < kSms) {
+        for (double most = std::max(per_sm, 2.0);; most *= 1.1) {
+            s.k1 = parts(top[0], most);
+            s.k2 = parts(top[1], most);
+            if (s.ctas() <= kSms || (s.k1 == 1 && s.k2 == 1)) break;
+        }
+    } else {
+        s.k1 = parts(top[0], std::max(0.75 * per_sm, 4.0));
+        s.k2 = parts(top[1], std::max(per_sm, 4.0));
+    }
+    return s;
+}
+
+size_t window_bwd_workspace(const svga_window_problem *p)
+{
+    return stats_bytes(p) +
+           (size_t)choose_bwd_split(p).slots() * 2 * kT * p->head_dim * sizeof(float);
 }
 
 svga_status launch_window_bwd(const svga_view &d_o, const svga_view &q, const svga_view &k,
@@ -993,7 +1140,8 @@ svga_status launch_window_bwd(const svga_view &d_o, const svga_view &q, const sv
     kp.scale_log2 = scale * kLog2e;
     kp.n_qblk = (p->q_tokens + kT - 1) / kT;
     kp.n_kblk = (p->k_tokens + kT - 1) / kT;
-    kp.d = p->head_dim;
+    kp.split = choose_bwd_split(p);
+    kp.parts = kp.stats + stats_bytes(p) / sizeof(float);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (p->head_dim == 128)
         return p->dtype == SVGA_F16 ? launch<128, true>(d_o, q, k, v, kp, p, st)

@@ -637,22 +637,22 @@ bool pair_heads(const svga_window_problem *p)
     return p->q_tokens <= kBlockM && (p->q_heads / p->kv_heads) % 2 == 0;
 }
 
-// Which items are split, from the shapes alone.  An item is `len` chunks long (the longest
-// and the mean over its query blocks); the GPU runs kSms items at a time.
+// Which items are split, from the shapes alone.  An item's list is as long as the shapes allow;
+// the GPU runs kSms items at a time.
 //   * less than one round of items: all split, to fill it once;
-//   * items of about one length: those behind the last whole round are split to fill one
-//     (12,480 tokens of 4 heads, 196 equal items: TAIL_FIGURES);
-//   * a causal list without a window, where lengths run from 1 to the longest: the longest
-//     items, launched first, are split in two when one alone would take over half of the
-//     whole launch's time.
-// From four rounds on the last one costs less than the partial sums.  A part keeps at least
-// kMinChunksPerSplit chunks.
+//   * one to two rounds of lists of about one length (mean at least 0.65 of the longest): those
+//     behind the first round are split to fill the second (12,480 tokens of 4 heads, 196
+//     items: 110 us against 128 unsplit; all split in two 137, the partial sums cost more);
+//   * from two rounds on nothing (512 items of 11 chunks: 87 us against 94 with the last 68
+//     split), nor where a causal list without a window makes lengths run from 1 to the
+//     longest: those are launched longest first and pack by themselves.
+// A part keeps at least kMinChunksPerSplit chunks.
 Split choose_split(const svga_window_problem *p)
 {
     const long long pairs = (p->q_tokens + 2 * kBlockM - 1) / (2 * kBlockM);
     const long long n = (long long)p->batch * (pair_heads(p) ? p->q_heads / 2 : p->q_heads) * pairs;
     Split s = {(int)n, (int)n, 1, 1};
-    if (n == 0 || n >= 4 * kSms || p->k_tokens == 0) return s;
+    if (n == 0 || n >= 2 * kSms || n == kSms || p->k_tokens == 0) return s;
     const Mask m = to_mask(p->mask);
     const int off = p->k_tokens - p->q_tokens;
     long long longest = 0, sum = 0;
@@ -666,19 +666,9 @@ Split choose_split(const svga_window_problem *p)
     const long long most = std::max(1ll, longest / kMinChunksPerSplit);
     if (n < kSms) {
         s.k1 = (int)std::min<long long>(kSms / n, most);
-        return s;
-    }
-    if (5 * sum >= 4 * longest * pairs) {  // mean at least 0.8 of the longest
-        const int tail = (int)(n % kSms);
-        if (tail == 0) return s;
-        s.n1 = (int)n - tail;
-        s.k2 = (int)std::min<long long>(kSms / tail, most);
-        return s;
-    }
-    const double per_sm = (double)sum / pairs * n / kSms;  // chunks
-    if (2 * longest > per_sm && most > 1) {
-        s.n1 = (int)(n / 2);
-        s.k1 = 2;
+    } else if (20 * sum >= 13 * longest * pairs) {
+        s.n1 = kSms;
+        s.k2 = (int)std::min<long long>(kSms / (n - kSms), most);
     }
     return s;
 }

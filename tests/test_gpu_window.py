@@ -157,13 +157,14 @@ def test_split_key_lists(B, H, G, nq, nk):
     assert e.value.status == 5
 
 
-@pytest.mark.parametrize("mask,dtype", [(M(window=700, sinks=100), BF), (M(), FP)], ids=str)
-def test_launches_split_in_part(mask, dtype):
-    """160 items for 148 SMs: the last ones split (lists of one length), the first ones split
-    (a causal list without a window).  Three heads are compared."""
+@pytest.mark.parametrize("mask,dtype,split", [(M(window=700, sinks=100), BF, True), (M(), FP, False)],
+                         ids=str)
+def test_launches_split_in_part(mask, dtype, split):
+    """160 items for 148 SMs: the last ones split where lists are of one length, none under a
+    causal mask without a window.  Three heads are compared."""
     q = values(1, 10, 4000, 64, dtype=dtype)
     k, v = (values(1, 5, 4000, 64, dtype=dtype, seed=s) for s in (1, 2))
-    assert svga.svga_window_attention_size(q, k, mask)["fwd_bytes"] > 0
+    assert (svga.svga_window_attention_size(q, k, mask)["fwd_bytes"] > 0) == split
     o, lse = forward(q, k, v, mask, 0.125)
     for h in (0, 5, 9):
         g = h // 2
