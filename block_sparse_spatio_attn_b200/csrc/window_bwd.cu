@@ -35,10 +35,13 @@
 //     left for a second tile.  The groups are therefore two chains of their own (barriers,
 //     products of 64 columns or 64 terms each): while one waits, the other has the
 //     exponential unit and the tensor pipe;
-//   * dq: S | dP0 | dP1 | dQ in TMEM: S is computed again as soon as it was read, dP a step
-//     ahead, so no step waits for its products;
-//   * three stages of Q (dkdv) and of K (dq), which are needed longest, and two of the other
-//     operand fill shared memory with the resident tiles.
+//   * dq has three issuers and gives dS columns of its own (S | dP | dQ | dS | Q, the last two
+//     64 columns of packed pairs each): S and dP are computed again as soon as they were
+//     read, so the softmax threads wait for no product (with dS over dP the chain dS -> dQ ->
+//     dP -> dS alone took 2,440 cycles a step).  Q as an operand in TMEM spares a quarter of
+//     the shared memory's reads;
+//   * shared memory holds, beside the resident tiles, three stages of the operand that is
+//     needed longest (dkdv: Q, dq: K) and two of the other.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -81,7 +84,7 @@ struct Cfg {
     // dkdv: K, V, three stages of Q, two of dO with the block's statistics
     static constexpr int kQStages = 3, kOStages = 2;
     static constexpr int kKvData = (2 + kQStages + kOStages) * kTile + kOStages * kStats;
-    // dq: Q, dO, three stages of K, two of V
+    // dq: Q (on its way to TMEM), dO, three stages of K, two of V
     static constexpr int kKStages = 3, kVStages = 2;
     static constexpr int kDqData = (2 + kKStages + kVStages) * kTile;
     static constexpr int kBars = 512;
@@ -240,7 +243,7 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, i
                (accumulate || kk > 0) ? 1u : 0u);
 }
 
-// The same, all 128 columns and all 128 terms.
+// A 128 x 128 product over D terms, both operands in shared memory.
 template <int D>
 __device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id)
 {
@@ -251,11 +254,24 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, u
     }
 }
 
+// A 128 x D product over 128 terms: a holds them as packed pairs in 64 columns.
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
                                            bool accumulate)
 {
-    product_ts(d, a, b, 0, id, accumulate);
-    product_ts(d, a, b, 1, id, true);
+#pragma unroll
+    for (int kk = 0; kk < kT / 16; ++kk)
+        mma_ts(d, a + 8 * kk, b + (uint32_t)(kk * (2048 >> 4)), id,
+               (accumulate || kk > 0) ? 1u : 0u);
+}
+
+// A 128 x 128 product over D terms, a in TMEM as packed pairs, b's rows (K-major) the columns.
+template <int D>
+__device__ __forceinline__ void product_tk(uint32_t d, uint32_t a, uint64_t b, uint32_t id)
+{
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+        mma_ts(d, a + 8 * kk, b + (uint32_t)(((kk >> 2) * Cfg<D>::kChunk + (kk & 3) * 32) >> 4), id,
+               kk > 0 ? 1u : 0u);
 }
 
 // The base of the dynamic shared memory, on the 1024-byte boundary the swizzle needs.  The
@@ -315,6 +331,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mask_rows(p.s.mask, k0, nq, off, first, end);  // a sink among the keys is the first one
     mask_rows(p.s.mask, k1 - 1, nq, off, x, end1);
     end = max(end, end1);
+    // the queries that keep all of the keys: each key's are contiguous, a sink's run to the end
+    int all_first, all_end = nq;
+    mask_rows(p.s.mask, k1 - 1, nq, off, all_first, x);
+    all_first = max(all_first, first);
+    if (p.s.mask.window >= 0 && p.s.mask.sinks < k1) {
+        mask_rows(p.s.mask, max(k0, p.s.mask.sinks), nq, off, x, all_end);
+    } else if (p.s.mask.window < 0) {
+        mask_rows(p.s.mask, k0, nq, off, x, all_end);
+    }
     const int qb0 = first / kT, n_blk = end > first ? (end + kT - 1) / kT - qb0 : 0;
     // steps run over the group's heads and their blocks; this CTA takes its part of them
     const long long all = (long long)n_blk * p.s.group;
@@ -536,13 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < steps; ++i) {
             const int r0 = (qb0 + blk) * kT;
             if (++blk == n_blk) blk = 0;
-            const MaskRange m0 = mask_range(p.s.mask, r0 + off, nk);
-            const MaskRange m1 = mask_range(p.s.mask, min(r0 + kT, nq) - 1 + off, nk);
-            const bool full = ((m1.lo <= k0 || m1.lo <= m0.sk) && k1 <= m0.hi) || k1 <= m0.sk;
-            // kept columns of this thread's half: [c0, c1)
-            const int c0 = ra - r0 - 64 * wg, c1 = re - r0 - 64 * wg;
-            uint32_t keep[2] = {bits_below(c1) & ~bits_below(c0),
-                                bits_below(c1 - 32) & ~bits_below(c0 - 32)};
+            const bool full = r0 >= all_first && min(r0 + kT, nq) <= all_end;
+            uint32_t keep[2] = {0u, 0u};
+            if (!full) {  // kept columns of this thread's half: [c0, c1)
+                const int c0 = ra - r0 - 64 * wg, c1 = re - r0 - 64 * wg;
+                keep[0] = bits_below(c1) & ~bits_below(c0);
+                keep[1] = bits_below(c1 - 32) & ~bits_below(c0 - 32);
+            }
             const float4 *nl = reinterpret_cast<const float4 *>(
                                    sStats + (i % C::kOStages) * C::kStats) +
                                16 * wg;
@@ -690,16 +715,15 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const BwdParams p)
 
 // ------------------------------------------------------------------------------- dq
 struct DqBars {
-    uint64_t q_full;
+    uint64_t q_full;           // Q and dO are in shared memory
+    uint64_t a_ready;          // Q is in TMEM (8 warps)
     uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
     uint64_t s_full, s_free;   // S of a step is in TMEM, was read into registers (8 warps)
-    uint64_t dp_full[2];       // dP of an even / odd step
-    // dS (8 warps) of an even / odd step, over the dP it came from.  Two barriers: a warp can
-    // be done with step i + 1, whose S and dP do not wait for dS(i), before another with i;
-    // i + 2 needs dS(i) of all.
-    uint64_t ds_ready[2];
-    uint64_t acc_done, drain[2];
-    uint64_t zero_req, zero_done;
+    uint64_t dp_full, dp_free; // the same of dP
+    uint64_t ds_ready;         // dS is in its columns (8 warps)
+    uint64_t dq_done;          // the dQ product that reads them is done
+    uint64_t drain[3];
+    uint64_t zero_done;
     uint32_t tmem_base;
     int abort;
 };
@@ -712,12 +736,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const BwdParams p)
 {
     using C = Cfg<D>;
-    constexpr uint32_t kS = 0, kDP = 128, kDQ = 384;
+    constexpr uint32_t kS = 0, kDP = 128, kDQ = 256, kDS = 384, kQ = 448;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_misplaced(smem, p.s.status)) return;
     uint8_t *sQ = smem, *sO = smem + C::kTile;
-    uint8_t *sK = smem + 2 * C::kTile;               // [stage]
-    uint8_t *sV = sK + C::kKStages * C::kTile;       // [stage]
+    uint8_t *sK = smem + 2 * C::kTile;          // [stage]
+    uint8_t *sV = sK + C::kKStages * C::kTile;  // [stage]
     DqBars *bar = reinterpret_cast<DqBars *>(smem + C::kDqData);
     volatile int *abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -739,21 +763,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bar->q_full), 1);
+        mbar_init(smem_u32(&bar->a_ready), 8);
         for (int i = 0; i < C::kKStages; ++i) {
             mbar_init(smem_u32(&bar->k_full[i]), 1);
             mbar_init(smem_u32(&bar->k_empty[i]), 1);
+            mbar_init(smem_u32(&bar->drain[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kVStages; ++i) {
             mbar_init(smem_u32(&bar->v_full[i]), 1);
             mbar_init(smem_u32(&bar->v_empty[i]), 1);
-            mbar_init(smem_u32(&bar->dp_full[i]), 1);
-            mbar_init(smem_u32(&bar->ds_ready[i]), 8);
-            mbar_init(smem_u32(&bar->drain[i]), 1);
         }
         mbar_init(smem_u32(&bar->s_full), 1);
         mbar_init(smem_u32(&bar->s_free), 8);
-        mbar_init(smem_u32(&bar->acc_done), 1);
-        mbar_init(smem_u32(&bar->zero_req), 1);
+        mbar_init(smem_u32(&bar->dp_full), 1);
+        mbar_init(smem_u32(&bar->dp_free), 8);
+        mbar_init(smem_u32(&bar->ds_ready), 8);
+        mbar_init(smem_u32(&bar->dq_done), 1);
         mbar_init(smem_u32(&bar->zero_done), 1);
         bar->abort = 0;
         fence_barrier_init();
@@ -769,47 +794,67 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsLow>();
-        if (warp == 0 && lane == 0 && E > 0) {
+        // the ragged chunk, a sequence's last, is the last of the list where it is in it
+        const bool clean = E > 0 && chunk_of(E - 1) == ragged;
+        if (warp == 0 && E > 0) {
             // -------------------------------------------------------- TMA producer
-            const uint32_t qf = smem_u32(&bar->q_full);
-            mbar_arrive_expect_tx(qf, 2 * C::kTile);
-            for (int c = 0; c < D / 64; ++c) {
-                tma_load_4d(smem_u32(sQ + c * C::kChunk), &tmQ, qf, 64 * c, r0, h * p.q_mh,
-                            b * p.q_mb);
-                tma_load_4d(smem_u32(sO + c * C::kChunk), &tmO, qf, 64 * c, r0, h * p.o_mh,
-                            b * p.o_mb);
-            }
             int k_issued = 0, v_issued = 0;
-            for (int i = 0; i < E; ++i) {
-                const int row = chunk_of(i) * kT, ks = i % C::kKStages, vs = i % C::kVStages;
-                const int kr = i / C::kKStages, vr = i / C::kVStages;
-                if (kr > 0 && !mbar_wait(smem_u32(&bar->k_empty[ks]), (kr - 1) & 1, abort_flag))
-                    break;
-                uint32_t fb = smem_u32(&bar->k_full[ks]);
-                mbar_arrive_expect_tx(fb, C::kTile);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem_u32(sK + ks * C::kTile + c * C::kChunk), &tmK, fb, 64 * c, row,
-                                hk * p.k_mh, b * p.k_mb);
-                k_issued = i + 1;
-                if (vr > 0 && !mbar_wait(smem_u32(&bar->v_empty[vs]), (vr - 1) & 1, abort_flag))
-                    break;
-                fb = smem_u32(&bar->v_full[vs]);
-                mbar_arrive_expect_tx(fb, C::kTile);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem_u32(sV + vs * C::kTile + c * C::kChunk), &tmV, fb, 64 * c, row,
-                                hk * p.v_mh, b * p.v_mb);
-                v_issued = i + 1;
+            if (lane == 0) {
+                const uint32_t qf = smem_u32(&bar->q_full);
+                mbar_arrive_expect_tx(qf, 2 * C::kTile);
+                for (int c = 0; c < D / 64; ++c) {
+                    tma_load_4d(smem_u32(sQ + c * C::kChunk), &tmQ, qf, 64 * c, r0, h * p.q_mh,
+                                b * p.q_mb);
+                    tma_load_4d(smem_u32(sO + c * C::kChunk), &tmO, qf, 64 * c, r0, h * p.o_mh,
+                                b * p.o_mb);
+                }
+                for (int i = 0; i < E; ++i) {
+                    const int row = chunk_of(i) * kT, ks = i % C::kKStages, vs = i % C::kVStages;
+                    const int kr = i / C::kKStages, vr = i / C::kVStages;
+                    if (kr > 0 && !mbar_wait(smem_u32(&bar->k_empty[ks]), (kr - 1) & 1, abort_flag))
+                        break;
+                    uint32_t fb = smem_u32(&bar->k_full[ks]);
+                    mbar_arrive_expect_tx(fb, C::kTile);
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d(smem_u32(sK + ks * C::kTile + c * C::kChunk), &tmK, fb, 64 * c,
+                                    row, hk * p.k_mh, b * p.k_mb);
+                    k_issued = i + 1;
+                    if (vr > 0 && !mbar_wait(smem_u32(&bar->v_empty[vs]), (vr - 1) & 1, abort_flag))
+                        break;
+                    fb = smem_u32(&bar->v_full[vs]);
+                    mbar_arrive_expect_tx(fb, C::kTile);
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d(smem_u32(sV + vs * C::kTile + c * C::kChunk), &tmV, fb, 64 * c,
+                                    row, hk * p.v_mh, b * p.v_mb);
+                    v_issued = i + 1;
+                }
             }
-            // every copy lands before the CTA can exit, whichever role aborts
-            mbar_wait_bounded(qf, 0);
-            for (int i = max(k_issued - C::kKStages, 0); i < k_issued; ++i)
-                mbar_wait_bounded(smem_u32(&bar->k_full[i % C::kKStages]), (i / C::kKStages) & 1);
-            for (int i = max(v_issued - C::kVStages, 0); i < v_issued; ++i)
-                mbar_wait_bounded(smem_u32(&bar->v_full[i % C::kVStages]), (i / C::kVStages) & 1);
-        } else if ((warp == 1 || warp == 3) && lane == 0 && E > 0) {
+            __syncwarp();
+            if (clean && __shfl_sync(0xffffffffu, k_issued, 0) == E) {
+                // keys past the sequence's end read as 0 (this warp filled the stage, so the
+                // phase its parity names is the stage's current one)
+                const int ks = (E - 1) % C::kKStages;
+                const bool ok =
+                    mbar_wait(smem_u32(&bar->k_full[ks]), ((E - 1) / C::kKStages) & 1, abort_flag);
+                if (__all_sync(0xffffffffu, ok)) {
+                    zero_rows<D>(smem_u32(sK + ks * C::kTile), nk % kT, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar->zero_done));
+                }
+            }
+            if (lane == 0) {  // every copy lands before the CTA can exit, whichever role aborts
+                mbar_wait_bounded(smem_u32(&bar->q_full), 0);
+                for (int i = max(k_issued - C::kKStages, 0); i < k_issued; ++i)
+                    mbar_wait_bounded(smem_u32(&bar->k_full[i % C::kKStages]),
+                                      (i / C::kKStages) & 1);
+                for (int i = max(v_issued - C::kVStages, 0); i < v_issued; ++i)
+                    mbar_wait_bounded(smem_u32(&bar->v_full[i % C::kVStages]),
+                                      (i / C::kVStages) & 1);
+            }
+        } else if (warp >= 1 && lane == 0 && E > 0) {
             // --------------------------------------------------------- MMA issuers
-            // warp 1: S, warp 3: dP and dQ
-            const int role = warp == 3;
+            // warp 1: S, warp 2: dQ, warp 3: dP
             constexpr uint32_t idS = idesc_16_f32(F16, kT, kT, 0, 0);
             constexpr uint32_t idA = idesc_16_f32(F16, kT, D, 0, 1);
             const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);
@@ -820,66 +865,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  abort_flag);
             };
             auto k_at = [&](int i) { return aK + (i % C::kKStages) * (C::kTile >> 4); };
-            bool ok = mbar_wait(smem_u32(&bar->q_full), 0, abort_flag);
-            if (role == 0) {
-                const uint64_t a = kmaj + (smem_u32(sQ) >> 4);
+            bool ok = true;
+            if (warp == 1) {
+                ok = mbar_wait(smem_u32(&bar->a_ready), 0, abort_flag);
+                tc_fence_after();
                 for (int i = 0; ok && i < E; ++i) {
-                    if (!(ok = k_landed(i))) break;
-                    if (chunk_of(i) == ragged) {  // warp 2 clears the keys past the end
-                        mbar_arrive(smem_u32(&bar->zero_req));
-                        if (!(ok = mbar_wait(smem_u32(&bar->zero_done), 0, abort_flag))) break;
-                    }
-                    if (i > 0) {
-                        if (!(ok = mbar_wait(smem_u32(&bar->s_free), (i - 1) & 1, abort_flag)))
-                            break;
-                        tc_fence_after();
-                    }
-                    product_ss<D>(tmem + kS, a, kmaj + k_at(i), idS);
+                    ok = k_landed(i) &&
+                         (!(clean && i == E - 1) ||
+                          mbar_wait(smem_u32(&bar->zero_done), 0, abort_flag)) &&
+                         (i == 0 || mbar_wait(smem_u32(&bar->s_free), (i - 1) & 1, abort_flag));
+                    tc_fence_after();
+                    if (!ok) break;
+                    product_tk<D>(tmem + kS, tmem + kQ, kmaj + k_at(i), idS);
                     mma_commit(smem_u32(&bar->s_full));
+                }
+            } else if (warp == 2) {
+                for (int i = 0; ok && i < E; ++i) {
+                    ok = k_landed(i) && mbar_wait(smem_u32(&bar->ds_ready), i & 1, abort_flag);
+                    tc_fence_after();
+                    if (!ok) break;
+                    product_ts(tmem + kDQ, tmem + kDS, nmaj + k_at(i), idA, i > 0);
+                    mma_commit(smem_u32(&bar->dq_done));
+                    mma_commit(smem_u32(&bar->k_empty[i % C::kKStages]));
                 }
             } else {
                 const uint64_t a = kmaj + (smem_u32(sO) >> 4);
-                auto v_landed = [&](int i) {
-                    return mbar_wait(smem_u32(&bar->v_full[i % C::kVStages]),
-                                     (i / C::kVStages) & 1, abort_flag);
-                };
-                auto issue = [&](int i) {
-                    const int vs = i % C::kVStages;
-                    product_ss<D>(tmem + kDP + 128 * (i & 1), a, kmaj + aV + vs * (C::kTile >> 4),
-                                  idS);
-                    mma_commit(smem_u32(&bar->dp_full[i & 1]));
-                    mma_commit(smem_u32(&bar->v_empty[vs]));
-                };
-                for (int i = 0; ok && i < min(E, 2); ++i)
-                    if ((ok = v_landed(i))) issue(i);
+                ok = mbar_wait(smem_u32(&bar->q_full), 0, abort_flag);
                 for (int i = 0; ok && i < E; ++i) {
-                    const bool next = i + 2 < E;
-                    ok = k_landed(i) && (!next || v_landed(i + 2)) &&
-                         mbar_wait(smem_u32(&bar->ds_ready[i & 1]), (i >> 1) & 1, abort_flag);
+                    const int vs = i % C::kVStages;
+                    ok = mbar_wait(smem_u32(&bar->v_full[vs]), (i / C::kVStages) & 1, abort_flag) &&
+                         (i == 0 || mbar_wait(smem_u32(&bar->dp_free), (i - 1) & 1, abort_flag));
                     tc_fence_after();
                     if (!ok) break;
-                    product_ts(tmem + kDQ, tmem + kDP + 128 * (i & 1), nmaj + k_at(i), idA, i > 0);
-                    mma_commit(smem_u32(&bar->k_empty[i % C::kKStages]));
-                    if (next) issue(i + 2);
+                    product_ss<D>(tmem + kDP, a, kmaj + aV + vs * (C::kTile >> 4), idS);
+                    mma_commit(smem_u32(&bar->dp_full));
+                    mma_commit(smem_u32(&bar->v_empty[vs]));
                 }
-                if (ok) mma_commit(smem_u32(&bar->acc_done));
             }
             if (!ok) {
-                mma_commit(smem_u32(&bar->drain[role]));
-                mbar_wait_bounded(smem_u32(&bar->drain[role]), 0);
-            }
-        } else if (warp == 2 && ragged >= 0) {
-            // ------------------------------- keys past the sequence's end read as 0
-            int n = E - 1;  // the ragged chunk is a sequence's last: its entry, if any
-            while (n >= 0 && chunk_of(n) > ragged) --n;
-            if (n >= 0 && chunk_of(n) == ragged) {
-                const bool ok = mbar_wait(smem_u32(&bar->zero_req), 0, abort_flag);
-                if (__all_sync(0xffffffffu, ok)) {
-                    zero_rows<D>(smem_u32(sK + (n % C::kKStages) * C::kTile), nk % kT, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bar->zero_done));
-                }
+                mma_commit(smem_u32(&bar->drain[warp - 1]));
+                mbar_wait_bounded(smem_u32(&bar->drain[warp - 1]), 0);
             }
         }
     } else {
@@ -889,6 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const uint32_t tS = tmem + lane_base + kS + 64 * wg;
         const uint32_t tDP = tmem + lane_base + kDP + 64 * wg;
+        const uint32_t tDS = tmem + lane_base + kDS + 32 * wg;
         const int qrow = r0 + row;
         MaskRange mr = {0, 0, 0};
         if (qrow < nq) mr = mask_range(p.s.mask, qrow + off, nk);
@@ -897,14 +923,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl),
                      nd2 = make_float2(nd, nd);
         bool ok = true;
-        for (int i = 0; i < E; ++i) {
+        if (E > 0) {  // this lane's row of Q to TMEM as packed pairs, each group half of it
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->q_full), 0, abort_flag));
+            constexpr int kHalf = D / 4;  // 32-bit columns
+            const uint32_t src = smem_u32(sQ) + row * 128;
+#pragma unroll
+            for (int j = 0; j < kHalf / 16; ++j) {
+                uint32_t w[16];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    // 16-byte unit of the row: its 64-column chunk and place in the swizzle
+                    const int unit = wg * (kHalf / 4) + 4 * j + u;
+                    ld_shared_v4(src + (unit >> 3) * C::kChunk + (((unit & 7) ^ (row & 7)) << 4),
+                                 w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+                }
+                tmem_st16(tmem + lane_base + kQ + wg * kHalf + 16 * j, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(smem_u32(&bar->a_ready));
+        }
+        for (int i = 0; ok && i < E; ++i) {
             const int c = chunk_of(i), base = c * kT + 64 * wg;
             const bool full = cl.full(c);
-            uint32_t keep[2];
+            uint32_t keep[2] = {0u, 0u};
+            if (!full) {
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
-                keep[w] = (bits_below(mr.hi - base - 32 * w) & ~bits_below(mr.lo - base - 32 * w)) |
-                          bits_below(mr.sk - base - 32 * w);
+                for (int w = 0; w < 2; ++w)
+                    keep[w] =
+                        (bits_below(mr.hi - base - 32 * w) & ~bits_below(mr.lo - base - 32 * w)) |
+                        bits_below(mr.sk - base - 32 * w);
+            }
             uint32_t x[64];
             float pr[64];
             ok = __all_sync(0xffffffffu,
@@ -929,11 +979,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pr[j + 1] = fast_exp2(u.y);
             }
             ok = __all_sync(0xffffffffu,
-                            mbar_wait(smem_u32(&bar->dp_full[i & 1]), (i >> 1) & 1, abort_flag));
+                            mbar_wait(smem_u32(&bar->dp_full), i & 1, abort_flag));
             tc_fence_after();
             if (!ok) break;
-            tmem_ld64(tDP + 128 * (i & 1), x);
+            tmem_ld64(tDP, x);
             tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar->dp_free));
             {
                 uint32_t pk[32];
 #pragma unroll
@@ -950,16 +1003,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[j] &= ((k2 & 1u) ? 0xffffu : 0u) | ((k2 & 2u) ? 0xffff0000u : 0u);
                     }
                 }
-                tmem_st32(tDP + 128 * (i & 1), pk);
+                if (i > 0) {  // the last step's dQ product reads the columns
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(smem_u32(&bar->dq_done), (i - 1) & 1, abort_flag));
+                    tc_fence_after();
+                    if (!ok) break;
+                }
+                tmem_st32(tDS, pk);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar->ds_ready[i & 1]));
+            if (lane == 0) mbar_arrive(smem_u32(&bar->ds_ready));
         }
         // ------------------------------------ epilogue: each group half the columns
         if (ok && E > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->acc_done), 0, abort_flag));
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->dq_done), (E - 1) & 1, abort_flag));
             tc_fence_after();
         }
         if (ok) {
