@@ -8,14 +8,22 @@
 //     the FP32 pipe does not limit shared heads.  tcgen05 has nothing to add here: its
 //     smallest tile has 64 query rows and the operand bytes, not the products, set the time.
 //   * A cluster of CTAs splits the keys of one (sequence, key head): CTA r takes the r-th
-//     run of 64-key chunks of the mask's chunk list (sinks, then window; chunks in between
+//     run of 32-key chunks of the mask's chunk list (sinks, then window; chunks in between
 //     are never read).  The CTAs join over distributed shared memory, so the call is one
 //     launch with no workspace, and two calls can never share scratch.
-//   * Warp 4 looks up pages and streams K and V with TMA (16 rows x 64 columns a box, 128-byte
-//     swizzle) through kStages stages; warps 0-3 take 16 keys of a chunk each, with a softmax
-//     state of their own: no warp waits for another before the end.
-//   * 96 KB of stages a CTA, two CTAs an SM: 192 KB in flight, several times what the memory
-//     latency needs.
+//   * Warp 4 looks up pages and streams K and V with TMA through kStages stages of 64 keys: a
+//     copy each of K and V per box of 16, 32 or 64 rows, as many as lie whole in a page, with
+//     all their columns (64 at a time, 128-byte swizzle).  What it does per chunk bounds a CTA
+//     alone: eight times 2 KB a tensor with a page look-up each chunk took 1.34 us, one copy
+//     a tensor and look-ups a batch ahead 0.82 us (39 GB/s of K and V a CTA).
+//   * Warps 0-3 take 16 keys of a chunk each, with a softmax state of their own: no warp waits
+//     for another before the end.  Q sits in shared memory, read again for every chunk, to
+//     leave registers.
+//   * 96 KB of stages a CTA, two CTAs an SM.  One CTA an SM with eight warps and six stages
+//     streams 59 GB/s, but what 160 or 256 CTAs gain by it they lose in their second round
+//     (34 against 23 us, 80 against 70 us); chunks of 32 keys change nothing.
+// Measured: 8 sequences of 16,384 to 32,768 keys, 32 heads on 4, 385 MB: 70 us, 5.5 TB/s (84 %
+// of the measured copy); 16 sequences, 10 heads, 1,040 keys kept of up to 8,191, 85 MB: 23 us.
 // The running maximum moves only when a tile raises it (a warp vote), so O is rarely rescaled.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -30,9 +38,9 @@
 namespace svga {
 namespace {
 
-constexpr int kWarps = 4;                     // consumer warps
+constexpr int kWarps = 4;                     // consumer warps, 16 keys of a chunk each
 constexpr int kThreads = 32 * (kWarps + 1);   // + the producer
-constexpr int kChunk = 64;                    // keys per stage
+constexpr int kChunk = 16 * kWarps;           // keys per stage
 constexpr int kRows = 16;                     // query rows of a tile
 constexpr int kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -44,6 +52,7 @@ struct DecodeParams {
     long long q_sb, q_sh, o_sb, o_sh;
     int hq, hk, group, tiles;  // tiles of 16 query heads per key head
     int pages, page_size, max_pages;
+    int box;  // rows of a TMA box: 16, 32 or 64, whole inside a page
     const int32_t *page_table, *lens;
     Mask mask;
     float scale_log2;
@@ -52,19 +61,19 @@ struct DecodeParams {
 
 template <int D>
 struct DecodeSmem {
-    static constexpr int kHalf = kChunk * 128;          // 64 columns of 64 keys
-    static constexpr int kTile = kHalf * (D / 64);      // K or V of a chunk
+    static constexpr int kTile = kChunk * D * 2;        // K or V of a chunk
     static constexpr int kStage = 2 * kTile;
     static constexpr int kData = kStages * kStage;
+    static constexpr int kQ = kRows * D * 2;
     // the warps' partial results and the CTA's
     static constexpr int kJoin = (kWarps + 1) * kRows * (D + 2) * 4;
     static_assert(kJoin <= kData, "the join reuses the stages");
-    static constexpr int kAlloc = kData + 256 + 1024;
+    static constexpr int kAlloc = kData + kQ + 256 + 1024;
 };
 
 struct DecodeBars {
     uint64_t full[kStages], empty[kStages];
-    uint32_t groups[kStages];  // which 16-key groups of the stage were loaded
+    uint32_t boxes[kStages];  // which of the stage's boxes were loaded
     int abort;
 };
 
@@ -111,7 +120,7 @@ __device__ __forceinline__ uint32_t cluster_size()
 }
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant__ CUtensorMap tmK,
+__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ CUtensorMap tmK,
                                                           const __grid_constant__ CUtensorMap tmV,
                                                           const DecodeParams p)
 {
@@ -119,7 +128,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
-    DecodeBars *bar = reinterpret_cast<DecodeBars *>(smem + S::kData);
+    const uint32_t sQ = smem_u32(smem + S::kData);
+    DecodeBars *bar = reinterpret_cast<DecodeBars *>(smem + S::kData + S::kQ);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
     const int kvh = blockIdx.y / p.tiles, tile = blockIdx.y - kvh * p.tiles, b = blockIdx.z;
@@ -147,6 +157,18 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
     const int e1 = (int)((long long)(rank + 1) * all / ranks);
     auto chunk_of = [&](int e) { return e < cl.a ? e : skip + e - cl.a; };
     auto kept = [&](int j) { return j < mr.hi && (j >= mr.lo || j < mr.sk); };
+    // the tile's query rows, 16-byte units permuted within a row so that ldmatrix meets no bank
+    // twice; rows past the group are 0
+    const int head0 = kvh * p.group + tile * kRows;
+    const int rows = min(kRows, p.group - tile * kRows);
+    for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
+        const int r = i / (D / 8), u = i - r * (D / 8);
+        const uint4 x = r < rows ? __ldg(reinterpret_cast<const uint4 *>(
+                                             p.q + 2 * (b * p.q_sb + (head0 + r) * p.q_sh)) +
+                                         u)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+        st_shared_v4(sQ + r * (D * 2) + ((u ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+    }
     __syncthreads();
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -158,91 +180,95 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
 
     if (warp == kWarps) {
         // ------------------------------------------------------------------ producer
-        const int g = lane & 3;  // lanes 0-3: one 16-key group each
-        auto page_at = [&](int e) {
-            const int j = chunk_of(e) * kChunk + g * 16;
-            // kept keys of the group: [lo, hi) or the sinks below min(sk, hi)
-            const bool need = j < mr.hi && (j + 16 > mr.lo || j < mr.sk);
-            return need ? __ldg(p.page_table + (long long)b * p.max_pages + j / p.page_size) : -2;
-        };
-        int page = (lane < 4 && e0 < e1) ? page_at(e0) : -2;
         int issued = 0;
-        for (int e = e0; e < e1; ++e, ++issued) {
-            const int s = issued % kStages, round = issued / kStages;
-            const int next = (lane < 4 && e + 1 < e1) ? page_at(e + 1) : -2;
+        // A chunk comes in `per` boxes of p.box rows, a copy each of K and V.  One pass of this
+        // loop is what bounds a CTA alone, so it does little: the rows of the next 32 / per
+        // chunks' boxes are looked up together, one lane a box, a batch ahead of their use.
+        const int per = kChunk / p.box, batch = 32 / per, g = lane & (per - 1);
+        auto row_at = [&](int e) {  // row of this lane's box in the batch from entry e on
+            e += lane / per;
+            if (e >= e1) return -1;
+            const int j = chunk_of(e) * kChunk + g * p.box, slot = j / p.page_size;
+            // any kept key: in [lo, hi), or below the end of the sinks
+            if (j >= mr.hi || !(j + p.box > mr.lo || j < mr.sk)) return -1;
+            const int page = __ldg(p.page_table + (long long)b * p.max_pages + slot);
+            if (page < 0 || page >= p.pages) {
+                if (p.status) atomicCAS(p.status, 0, (int32_t)SVGA_ERR_INVALID_ARG);
+                return -1;
+            }
+            return (page * p.hk + kvh) * p.page_size + j - slot * p.page_size;
+        };
+        int rows_now = row_at(e0), rows_next = row_at(e0 + batch);
+        const int count = e1 - e0;
+        for (int i = 0, s = 0, round = 0, at = 0; i < count; ++i) {
+            if (at == batch) {
+                at = 0;
+                rows_now = rows_next;
+                rows_next = row_at(e0 + i + batch);
+            }
+            const int row = __shfl_sync(0xffffffffu, rows_now, at * per + g);
+            ++at;
             bool ok = true;
             if (round > 0)
                 ok = mbar_wait(smem_u32(&bar->empty[s]), (round - 1) & 1, &bar->abort);
             if (!__all_sync(0xffffffffu, ok)) break;
-            const bool load = page >= 0 && page < p.pages;
-            if (page != -2 && !load && p.status)
-                atomicCAS(p.status, 0, (int32_t)SVGA_ERR_INVALID_ARG);
-            const uint32_t groups = __ballot_sync(0xffffffffu, load) & 15u;
+            const bool load = lane < per && row >= 0;
+            const uint32_t boxes = __ballot_sync(0xffffffffu, load);
             const uint32_t fb = smem_u32(&bar->full[s]);
             if (lane == 0) {
-                bar->groups[s] = groups;
-                mbar_arrive_expect_tx(fb, __popc(groups) * 16 * D * 2 * 2);
+                bar->boxes[s] = boxes;
+                mbar_arrive_expect_tx(fb, __popc(boxes) * p.box * D * 2 * 2);
             }
             __syncwarp();
             if (load) {
-                const int j = chunk_of(e) * kChunk + g * 16;
-                const int row = (page * p.hk + kvh) * p.page_size + j % p.page_size;
-                const uint32_t dst = smem_u32(smem + s * S::kStage) + g * 2048;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    tma_load_2d(dst + c * S::kHalf, &tmK, fb, 64 * c, row);
-                    tma_load_2d(dst + S::kTile + c * S::kHalf, &tmV, fb, 64 * c, row);
-                }
+                const uint32_t dst = smem_u32(smem + s * S::kStage) + g * p.box * (D * 2);
+                tma_load_3d(dst, &tmK, fb, 0, row, 0);
+                tma_load_3d(dst + S::kTile, &tmV, fb, 0, row, 0);
             }
-            page = next;
+            issued = i + 1;
+            if (++s == kStages) {
+                s = 0;
+                ++round;
+            }
         }
-        // copies in flight land before the CTA can exit, also after an abort
-        if (bar->abort && lane == 0)
+        // every copy lands before the CTA can exit, whoever gave up waiting
+        if (lane == 0)
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 mbar_wait_bounded(smem_u32(&bar->full[i % kStages]), (i / kStages) & 1);
     } else {
         // ----------------------------------------------------------------- consumers
-        const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // this thread's rows r0, r0 + 8
-        const int head0 = kvh * p.group + tile * kRows;
-        const int rows = min(kRows, p.group - tile * kRows);
-        uint32_t qa[D / 16][4];
-        {
-            const char *q = p.q + 2 * (b * p.q_sb + head0 * p.q_sh);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int r = r0 + (x & 1) * 8, c = kk * 16 + c0 + (x >> 1) * 8;
-                    qa[kk][x] = r < rows
-                                    ? __ldg(reinterpret_cast<const uint32_t *>(
-                                          q + 2 * (r * p.q_sh + c)))
-                                    : 0u;
-                }
-        }
+        const int c0 = (lane & 3) * 2;
         const int mat = lane >> 3, mrow = lane & 7;
-        for (int e = e0, i = 0; e < e1; ++e, ++i) {
+        // A box lies in a tile as its rows' first 64 columns, then their second: this warp's 16
+        // rows, and the step from one half of the columns to the other
+        const int box_at = warp * 16 / p.box;
+        const uint32_t row_at = box_at * p.box * (D * 2) + (warp * 16 - box_at * p.box) * 128;
+        const uint32_t half_step = p.box * 128;
+        for (int i = 0; i < e1 - e0; ++i) {
             const int s = i % kStages;
             const bool ok = mbar_wait(smem_u32(&bar->full[s]), (i / kStages) & 1, &bar->abort);
             if (!__all_sync(0xffffffffu, ok)) break;
-            const int j0 = chunk_of(e) * kChunk + warp * 16;  // this warp's 16 keys
-            if ((bar->groups[s] >> warp) & 1u) {
-                const uint32_t kb = smem_u32(smem + s * S::kStage);
+            const int j0 = chunk_of(e0 + i) * kChunk + warp * 16;  // this warp's 16 keys
+            if ((bar->boxes[s] >> box_at) & 1u) {
+                const uint32_t kb = smem_u32(smem + s * S::kStage) + row_at;
                 float sc[2][4];
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) sc[n][x] = 0.f;
                 {
-                    const int key = warp * 16 + (mat >> 1) * 8 + mrow;
+                    const int key = (mat >> 1) * 8 + mrow;
+                    const uint32_t qrow = (mat & 1) * 8 + mrow;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const int col = kk * 16 + (mat & 1) * 8;
-                        uint32_t kf[4];
-                        ldsm4(kb + (col >> 6) * S::kHalf + key * 128 +
-                                  ((((col & 63) >> 3) ^ (key & 7)) << 4),
+                        uint32_t kf[4], qf[4];
+                        ldsm4(sQ + qrow * (D * 2) + (((2 * kk + (mat >> 1)) ^ mrow) << 4), qf);
+                        ldsm4(kb + (col >> 6) * half_step + key * 128 +
+                                  ((((col & 63) >> 3) ^ mrow) << 4),
                               kf);
-                        mma16816<F16>(sc[0], qa[kk], kf[0], kf[1]);
-                        mma16816<F16>(sc[1], qa[kk], kf[2], kf[3]);
+                        mma16816<F16>(sc[0], qf, kf[0], kf[1]);
+                        mma16816<F16>(sc[1], qf, kf[2], kf[3]);
                     }
                 }
                 // masked keys: score -inf, and their value rows read as 0 (a probability of 0
@@ -288,13 +314,13 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
                     pa[2 + r] = pack_16x2<F16>(e[2], e[3]);
                 }
                 const uint32_t vb = kb + S::kTile;
-                const int key = warp * 16 + (mat & 1) * 8 + mrow;
+                const int key = (mat & 1) * 8 + mrow;
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
                     const int col = n * 16 + (mat >> 1) * 8;
                     uint32_t vf[4];
-                    ldsm4_t(vb + (col >> 6) * S::kHalf + key * 128 +
-                                ((((col & 63) >> 3) ^ (key & 7)) << 4),
+                    ldsm4_t(vb + (col >> 6) * half_step + key * 128 +
+                                ((((col & 63) >> 3) ^ mrow) << 4),
                             vf);
                     mma16816<F16>(o[2 * n], pa, vf[0] & vm0, vf[1] & vm1);
                     mma16816<F16>(o[2 * n + 1], pa, vf[2] & vm0, vf[3] & vm1);
@@ -330,7 +356,6 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
     }
     __syncthreads();
     // First the warps of this CTA, into comb / cml, in warp order.
-    const int rows = min(kRows, p.group - tile * kRows);
     float *comb = ml + 2 * kWarps * kRows;  // [row][D]
     float *cml = comb + kRows * D;          // [row] (m, l)
     for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads) {
@@ -361,7 +386,6 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
     else
         __syncthreads();
     // Then the CTAs of the cluster, each joining its share of the values, in rank order.
-    const int head0 = kvh * p.group + tile * kRows;
     const bool failed = bar->abort != 0;
     for (int i = rank * kThreads + threadIdx.x; i < rows * (D / 2); i += ranks * kThreads) {
         const int row = i / (D / 2), c = 2 * (i - row * (D / 2));
@@ -405,8 +429,8 @@ svga_status launch(const svga_paged_cache *c, const DecodeParams &p, int ranks, 
     const long long rows = std::max(1ll, (long long)c->pages * c->kv_heads * c->page_size);
     // with no pages nothing is loaded; the maps then only have to be valid
     const void *kb = c->pages > 0 ? c->k_pages : p.q, *vb = c->pages > 0 ? c->v_pages : p.q;
-    if (!make_rows_map(&tk, kb, rows, D, c->dtype, 16) ||
-        !make_rows_map(&tv, vb, rows, D, c->dtype, 16)) {
+    if (!make_rows_map(&tk, kb, rows, D, c->dtype, p.box) ||
+        !make_rows_map(&tv, vb, rows, D, c->dtype, p.box)) {
         set_error("cuTensorMapEncodeTiled failed (driver entry point or arguments)");
         return SVGA_ERR_CUDA;
     }
@@ -438,7 +462,7 @@ svga_status launch(const svga_paged_cache *c, const DecodeParams &p, int ranks, 
 }
 
 // CTAs per (sequence, key head): as many as fill the GPU's two slots an SM, while every CTA
-// keeps at least two chunks of the longest sequence the page table could hold.
+// keeps at least 128 keys of the longest sequence the page table could hold.
 int choose_ranks(const svga_paged_cache *c, const Mask &m, int tiles)
 {
     const int cap = c->max_pages * c->page_size;
@@ -446,7 +470,7 @@ int choose_ranks(const svga_paged_cache *c, const Mask &m, int tiles)
     const int chunks = cap > 0 ? cl.a + std::max(cl.w1 - std::max(cl.a, cl.w0), 0) : 1;
     const long long clusters = (long long)c->batch * c->kv_heads * tiles;
     int ranks = 1;
-    while (ranks < 16 && clusters * ranks * 2 <= 2 * 148 && chunks >= 4 * ranks) ranks *= 2;
+    while (ranks < 16 && clusters * ranks * 2 <= 2 * 148 && chunks * kChunk >= 256 * ranks) ranks *= 2;
     return ranks;
 }
 
@@ -471,6 +495,8 @@ svga_status launch_decode(const svga_view &q, const svga_view &o, float *lse, in
     p.pages = c->pages;
     p.page_size = c->page_size;
     p.max_pages = c->max_pages;
+    p.box = 16;
+    while (p.box < kChunk && c->page_size % (2 * p.box) == 0) p.box *= 2;
     p.page_table = c->page_table;
     p.lens = c->lens;
     p.mask = to_mask(*mask);

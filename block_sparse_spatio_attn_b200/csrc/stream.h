@@ -160,7 +160,8 @@ struct WindowShape {
 // (0 or 1).  False: the driver refused it.
 bool make_view_map(void *map, const svga_view &v, int batch, int heads, int tokens, int d,
                    svga_dtype dt, int box_rows, int *mul_h, int *mul_b);
-// 2-D map (d, rows) of contiguous rows of 16-bit elements, box 64 columns x box_rows.
+// Map of contiguous rows of 16-bit elements as (64 columns, rows, d / 64): one copy of a box
+// brings box_rows whole rows, each 64 columns of them together.
 bool make_rows_map(void *map, const void *base, long long rows, int d, svga_dtype dt,
                    int box_rows);
 void *encode_tiled_entry();  // cuTensorMapEncodeTiled, or NULL

@@ -60,11 +60,11 @@ bool make_rows_map(void *map, const void *base, long long rows, int d, svga_dtyp
 {
     EncodeTiled enc = reinterpret_cast<EncodeTiled>(encode_tiled_entry());
     if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return enc(static_cast<CUtensorMap *>(map), map_type(dt), 2, const_cast<void *>(base), dims,
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(d / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)(d / 64)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(static_cast<CUtensorMap *>(map), map_type(dt), 3, const_cast<void *>(base), dims,
                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
