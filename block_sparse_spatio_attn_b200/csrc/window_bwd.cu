@@ -52,6 +52,7 @@
 
 #include "stream.h"
 #include "svga_device.cuh"
+#include "tile_out.cuh"
 
 namespace svga {
 namespace {
@@ -161,55 +162,6 @@ __global__ void __launch_bounds__(256) bwd_rows_kernel(const BwdParams p)
     out[kT] = -sum;
 }
 
-// Writes NCOL fp32 columns of a TMEM row times `f` as 16-bit values; NULL dst: only loads.
-template <int NCOL, bool F16>
-__device__ __forceinline__ void store_row(uint32_t taddr, char *dst, float f, bool any)
-{
-#pragma unroll 1
-    for (int j = 0; j < NCOL / 32; ++j) {
-        uint32_t o[32];
-        if (any) {
-            tmem_ld32(taddr + j * 32, o);
-            tmem_wait_ld();
-        } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = 0u;
-        }
-        if (!dst) continue;
-        uint4 *to = reinterpret_cast<uint4 *>(dst + 64 * j);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = pack_16x2<F16>(__uint_as_float(o[8 * c + 2 * i]) * f,
-                                      __uint_as_float(o[8 * c + 2 * i + 1]) * f);
-            to[c] = make_uint4(x[0], x[1], x[2], x[3]);
-        }
-    }
-}
-
-template <int NCOL>
-__device__ __forceinline__ void store_part(uint32_t taddr, float *dst, bool any)
-{
-#pragma unroll 1
-    for (int j = 0; j < NCOL / 32; ++j) {
-        uint32_t o[32];
-        if (any) {
-            tmem_ld32(taddr + j * 32, o);
-            tmem_wait_ld();
-        } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = 0u;
-        }
-        if (!dst) continue;
-        uint4 *to = reinterpret_cast<uint4 *>(dst + 32 * j);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            to[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-    }
-}
-
 // Rows [first, 128) of a swizzled 128-row tile read as 0 (whole rows: the swizzle permutes
 // inside a row's 128 bytes).
 template <int D>
@@ -284,6 +236,58 @@ __device__ __forceinline__ bool smem_misplaced(const void *base, int32_t *status
 }
 
 // ----------------------------------------------------------------------------- dkdv
+// One CTA's work, worked out by warp 0 for all.
+struct KvItem {
+    int b, hk, nq, nk, off;
+    int k0, k1;                // keys
+    int qb0, n_blk;            // query blocks that keep any of them
+    int all_first, all_end;    // the queries that keep all of them
+    int steps, g0, blk0;       // this CTA's part of the group's blocks: how many, the first
+    int ragged;                // block whose last rows lie past the sequence's end but inside
+                               // the tensor, or -1
+    int ksplit;
+    long long slot;
+};
+
+__device__ __forceinline__ bool make_item(const BwdParams &p, KvItem &it)
+{
+    int item, part;
+    p.split.of_block(blockIdx.x, item, part);
+    it.ksplit = p.split.k(item);
+    it.slot = it.ksplit > 1 ? p.split.slot(item, part) : 0;
+    const int bh = p.s.batch * p.s.hk;
+    const int kblk = item / bh, r = item - kblk * bh;
+    it.b = r / p.s.hk;
+    it.hk = r - it.b * p.s.hk;
+    it.nq = clamped_len(p.s.q_lens, it.b, p.s.tq);
+    it.nk = clamped_len(p.s.k_lens, it.b, p.s.tk);
+    const int nq = it.nq, off = it.off = it.nk - nq;
+    const int k0 = it.k0 = kblk * kT, k1 = it.k1 = min(k0 + kT, it.nk);
+    if (k0 >= it.nk) return false;
+    int first, end, first1, end1, x;
+    mask_rows(p.s.mask, k0, nq, off, first, end);  // a sink among the keys is the first one
+    mask_rows(p.s.mask, k1 - 1, nq, off, first1, end1);
+    // rows that keep all: each key's are contiguous, and a sink's run to the end
+    it.all_first = max(first, first1);
+    it.all_end = nq;
+    if (p.s.mask.window < 0)
+        it.all_end = end;
+    else if (p.s.mask.sinks < k1)
+        mask_rows(p.s.mask, max(k0, p.s.mask.sinks), nq, off, x, it.all_end);
+    end = max(end, end1);
+    it.qb0 = first / kT;
+    it.n_blk = end > first ? (end + kT - 1) / kT - it.qb0 : 0;
+    const long long all = (long long)it.n_blk * p.s.group;
+    const int first_step = (int)(part * all / it.ksplit);
+    it.steps = (int)((part + 1) * all / it.ksplit) - first_step;
+    it.g0 = it.n_blk > 0 ? first_step / it.n_blk : 0;
+    it.blk0 = first_step - it.g0 * it.n_blk;
+    it.ragged =
+        (p.s.q_lens && nq < p.s.tq && nq % kT && nq / kT == it.qb0 + it.n_blk - 1) ? it.n_blk - 1
+                                                                                    : -1;
+    return true;
+}
+
 struct KvBars {
     uint64_t kv_full;
     uint64_t q_full[3], q_empty[3];      // stages of Q
@@ -295,7 +299,8 @@ struct KvBars {
     uint64_t drain[2];
     uint64_t zero_req[2], zero_done[2];  // Q, dO
     uint32_t tmem_base;
-    int abort;
+    int abort, some;
+    KvItem item;
 };
 static_assert(sizeof(KvBars) <= 512, "barrier space");
 
@@ -317,40 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // this CTA's keys, and the query blocks that keep any of them
-    int item, part;
-    p.split.of_block(blockIdx.x, item, part);
-    const int ksplit = p.split.k(item);
-    const int bh = p.s.batch * p.s.hk;
-    const int kblk = item / bh, r = item - kblk * bh;
-    const int b = r / p.s.hk, hk = r - b * p.s.hk;
-    const int nq = clamped_len(p.s.q_lens, b, p.s.tq), nk = clamped_len(p.s.k_lens, b, p.s.tk);
-    const int k0 = kblk * kT, k1 = min(k0 + kT, nk), off = nk - nq;
-    if (k0 >= nk) return;
-    int first, end, x, end1;
-    mask_rows(p.s.mask, k0, nq, off, first, end);  // a sink among the keys is the first one
-    mask_rows(p.s.mask, k1 - 1, nq, off, x, end1);
-    end = max(end, end1);
-    // the queries that keep all of the keys: each key's are contiguous, a sink's run to the end
-    int all_first, all_end = nq;
-    mask_rows(p.s.mask, k1 - 1, nq, off, all_first, x);
-    all_first = max(all_first, first);
-    if (p.s.mask.window >= 0 && p.s.mask.sinks < k1) {
-        mask_rows(p.s.mask, max(k0, p.s.mask.sinks), nq, off, x, all_end);
-    } else if (p.s.mask.window < 0) {
-        mask_rows(p.s.mask, k0, nq, off, x, all_end);
-    }
-    const int qb0 = first / kT, n_blk = end > first ? (end + kT - 1) / kT - qb0 : 0;
-    // steps run over the group's heads and their blocks; this CTA takes its part of them
-    const long long all = (long long)n_blk * p.s.group;
-    const int first_step = (int)(part * all / ksplit);
-    const int steps = (int)((part + 1) * all / ksplit) - first_step;
-    const int g0 = n_blk > 0 ? first_step / n_blk : 0, blk0 = first_step - g0 * n_blk;
-    // the query block whose last rows lie past the sequence's end but inside the tensor
-    const int ragged =
-        (p.s.q_lens && nq < p.s.tq && nq % kT && nq / kT == qb0 + n_blk - 1) ? n_blk - 1 : -1;
-
     if (threadIdx.x == 0) {
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+        prefetch_tmap(&tmQ);
+        prefetch_tmap(&tmO);
         mbar_init(smem_u32(&bar->kv_full), 1);
         for (int i = 0; i < C::kQStages; ++i) {
             mbar_init(smem_u32(&bar->q_full[i]), 1);
@@ -377,24 +353,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&bar->tmem_base), 512);
         tmem_relinquish();
     }
+    if (warp == 0) {
+        KvItem mine;
+        const bool some = make_item(p, mine);  // false: past the sequence's keys
+        if (lane == 0) {
+            bar->item = mine;
+            bar->some = some;
+            if (some && mine.steps > 0) {  // on their way before the CTA meets
+                const uint32_t kvf = smem_u32(&bar->kv_full);
+                mbar_arrive_expect_tx(kvf, 2 * C::kTile);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem_u32(sK + c * C::kChunk), &tmK, kvf, 64 * c, mine.k0,
+                                mine.hk * p.k_mh, mine.b * p.k_mb);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem_u32(sV + c * C::kChunk), &tmV, kvf, 64 * c, mine.k0,
+                                mine.hk * p.v_mh, mine.b * p.v_mb);
+            }
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem_base;
+    if (!bar->some) {
+        if (warp == 1) tmem_dealloc(tmem, 512);
+        return;
+    }
+    const KvItem &it = bar->item;
+    const int b = it.b, hk = it.hk, nq = it.nq, nk = it.nk, off = it.off, k0 = it.k0;
+    const int qb0 = it.qb0, n_blk = it.n_blk, steps = it.steps, ragged = it.ragged;
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsLow>();
         if (warp == 0 && lane == 0 && steps > 0) {
             // -------------------------------------------------------- TMA producer
-            const uint32_t kvf = smem_u32(&bar->kv_full);
-            mbar_arrive_expect_tx(kvf, 2 * C::kTile);
-            for (int c = 0; c < D / 64; ++c) {
-                tma_load_4d(smem_u32(sK + c * C::kChunk), &tmK, kvf, 64 * c, k0, hk * p.k_mh,
-                            b * p.k_mb);
-                tma_load_4d(smem_u32(sV + c * C::kChunk), &tmV, kvf, 64 * c, k0, hk * p.v_mh,
-                            b * p.v_mb);
-            }
-            int q_issued = 0, o_issued = 0, st_issued = 0, g = g0, blk = blk0;
+            int q_issued = 0, o_issued = 0, st_issued = 0, g = it.g0, blk = it.blk0;
             for (int i = 0; i < steps; ++i) {
                 const int h = hk * p.s.group + g, row = (qb0 + blk) * kT;
                 const int qs = i % C::kQStages, os = i % C::kOStages;
@@ -429,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // every copy lands before the CTA can exit, whichever role aborts
-            mbar_wait_bounded(kvf, 0);
+            mbar_wait_bounded(smem_u32(&bar->kv_full), 0);
             for (int i = max(q_issued - C::kQStages, 0); i < q_issued; ++i)
                 mbar_wait_bounded(smem_u32(&bar->q_full[i % C::kQStages]), (i / C::kQStages) & 1);
             for (int i = max(o_issued - C::kOStages, 0); i < o_issued; ++i)
@@ -453,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : mbar_wait(smem_u32(&bar->q_full[i % C::kQStages]),
                                      (i / C::kQStages) & 1, abort_flag);
             };
-            int blk[2] = {blk0, blk0}, cleaned[2] = {0, 0};  // walks of Q's and dO's steps
+            int blk[2] = {it.blk0, it.blk0}, cleaned[2] = {0, 0};  // walks of Q's and dO's steps
             // landed, and its rows past the sequence's end are 0 (asked of warp 2 once, by the
             // issuer whose first product on the stage it is)
             auto take = [&](int i, int w, bool ask) {
@@ -528,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 2 && ragged >= 0) {
             // ------------------------ rows of Q and dO past the sequence's end read as 0
             int time = 0;
-            for (int i = ragged - blk0 + (ragged < blk0 ? n_blk : 0); i < steps;
+            for (int i = ragged - it.blk0 + (ragged < it.blk0 ? n_blk : 0); i < steps;
                  i += n_blk, ++time) {
                 bool ok = true;
                 for (int w = 0; w < 2 && ok; ++w) {
@@ -557,7 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (key < nk) mask_rows(p.s.mask, key, nq, off, ra, re);
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
-        int blk = blk0;
+        const int all_first = it.all_first, all_end = it.all_end;
+        int blk = it.blk0;
         for (int i = 0; i < steps; ++i) {
             const int r0 = (qb0 + blk) * kT;
             if (++blk == n_blk) blk = 0;
@@ -651,15 +645,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->acc_done), 0, abort_flag));
             tc_fence_after();
         }
-        if (ok && ksplit > 1) {
-            float *dst = key < nk ? p.parts + ((p.split.slot(item, part) * 2 + wg) * kT + row) * D
-                                  : nullptr;
-            store_part<D>(tmem + lane_base + (wg ? kDK : kDV), dst, steps > 0);
-        } else if (ok) {
-            const View &w = wg ? p.dk : p.dv;
-            char *dst = key < nk ? w.p + 2 * (b * w.sb + hk * w.sh + key * w.st) : nullptr;
-            store_row<D, F16>(tmem + lane_base + (wg ? kDK : kDV), dst, wg ? p.scale : 1.f,
-                              steps > 0);
+        if (ok) {  // through K's and V's tiles, whose products are done
+            const uint32_t acc = tmem + lane_base + (wg ? kDK : kDV);
+            const uint32_t tile = smem_u32(wg ? sK : sV);
+            const int valid = nk - (key - lane);  // of the warp's rows
+            if (it.ksplit > 1) {  // (a tile holds half of a row of fp32)
+                char *dst = reinterpret_cast<char *>(
+                    p.parts + ((it.slot * 2 + wg) * kT + row - lane) * D);
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {
+                    put_row_32<D / 2>(acc + j * (D / 2), tile, C::kChunk, row, steps > 0);
+                    copy_rows_out<D / 8>(tile, C::kChunk, row - lane, 0, dst + 2 * D * j, 4 * D,
+                                         valid, lane);
+                }
+            } else {
+                const View &w = wg ? p.dk : p.dv;
+                put_row_16<D, F16>(acc, tile, C::kChunk, row, 0, wg ? p.scale : 1.f, steps > 0);
+                copy_rows_out<D / 8>(tile, C::kChunk, row - lane, 0,
+                                     w.p + 2 * (b * w.sb + hk * w.sh + (key - lane) * w.st),
+                                     2 * w.st, valid, lane);
+            }
         }
     }
     tc_fence_before();
@@ -714,6 +719,31 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const BwdParams p)
 }
 
 // ------------------------------------------------------------------------------- dq
+struct DqItem {
+    int b, h, hk, blk, nq, nk;
+    ChunkList list;
+    int skip, E;  // the chunks: 0 .. list.a - 1, then skip, skip + 1, ...; how many
+};
+
+__device__ __forceinline__ bool make_item(const BwdParams &p, DqItem &it)
+{
+    // last blocks first: the longest under a causal mask
+    const int bh = p.s.batch * p.s.hq;
+    const int slot = blockIdx.x / bh, r = blockIdx.x - slot * bh;
+    it.b = r / p.s.hq;
+    it.h = r - it.b * p.s.hq;
+    it.hk = it.h / p.s.group;
+    it.blk = p.n_qblk - 1 - slot;
+    it.nq = clamped_len(p.s.q_lens, it.b, p.s.tq);
+    it.nk = clamped_len(p.s.k_lens, it.b, p.s.tk);
+    const int off = it.nk - it.nq, r0 = it.blk * kT;
+    if (r0 >= it.nq) return false;
+    it.list = chunk_list<kT>(p.s.mask, r0 + off, min(r0 + kT, it.nq) - 1 + off, it.nk);
+    it.skip = max(it.list.a, it.list.w0);
+    it.E = it.list.a + max(it.list.w1 - it.skip, 0);
+    return true;
+}
+
 struct DqBars {
     uint64_t q_full;           // Q and dO are in shared memory
     uint64_t a_ready;          // Q is in TMEM (8 warps)
@@ -725,7 +755,8 @@ struct DqBars {
     uint64_t drain[3];
     uint64_t zero_done;
     uint32_t tmem_base;
-    int abort;
+    int abort, some;
+    DqItem item;
 };
 static_assert(sizeof(DqBars) <= 512, "barrier space");
 
@@ -746,22 +777,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // this CTA's queries (last blocks first: the longest under a causal mask) and their keys
-    const int bhq = p.s.batch * p.s.hq;
-    const int slot = blockIdx.x / bhq, r = blockIdx.x - slot * bhq;
-    const int b = r / p.s.hq, h = r - b * p.s.hq, hk = h / p.s.group;
-    const int blk = p.n_qblk - 1 - slot, r0 = blk * kT;
-    const int nq = clamped_len(p.s.q_lens, b, p.s.tq), nk = clamped_len(p.s.k_lens, b, p.s.tk);
-    const int off = nk - nq;
-    if (r0 >= nq) return;
-    const ChunkList cl =
-        chunk_list<kT>(p.s.mask, r0 + off, min(r0 + kT, nq) - 1 + off, nk);
-    const int skip = max(cl.a, cl.w0);
-    const int E = cl.a + max(cl.w1 - skip, 0);
-    auto chunk_of = [&](int e) { return e < cl.a ? e : skip + e - cl.a; };
-    const int ragged = (p.s.k_lens && nk < p.s.tk && nk % kT) ? nk / kT : -1;
-
     if (threadIdx.x == 0) {
+        prefetch_tmap(&tmQ);
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmO);
+        prefetch_tmap(&tmV);
         mbar_init(smem_u32(&bar->q_full), 1);
         mbar_init(smem_u32(&bar->a_ready), 8);
         for (int i = 0; i < C::kKStages; ++i) {
@@ -787,10 +807,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&bar->tmem_base), 512);
         tmem_relinquish();
     }
+    if (warp == 0) {
+        DqItem mine;
+        const bool some = make_item(p, mine);  // false: past the sequence's queries
+        if (lane == 0) {
+            bar->item = mine;
+            bar->some = some;
+            if (some && mine.E > 0) {  // on their way before the CTA meets
+                const uint32_t qf = smem_u32(&bar->q_full);
+                mbar_arrive_expect_tx(qf, 2 * C::kTile);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem_u32(sQ + c * C::kChunk), &tmQ, qf, 64 * c, mine.blk * kT,
+                                mine.h * p.q_mh, mine.b * p.q_mb);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem_u32(sO + c * C::kChunk), &tmO, qf, 64 * c, mine.blk * kT,
+                                mine.h * p.o_mh, mine.b * p.o_mb);
+            }
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem_base;
+    if (!bar->some) {
+        if (warp == 1) tmem_dealloc(tmem, 512);
+        return;
+    }
+    const DqItem &it = bar->item;
+    const int b = it.b, h = it.h, hk = it.hk, blk = it.blk, nq = it.nq, nk = it.nk, E = it.E;
+    const int off = nk - nq, r0 = blk * kT, sinks = it.list.a, skip = it.skip;
+    auto chunk_of = [&](int e) { return e < sinks ? e : skip + e - sinks; };
+    const int ragged = (p.s.k_lens && nk < p.s.tk && nk % kT) ? nk / kT : -1;
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsLow>();
@@ -800,14 +847,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- TMA producer
             int k_issued = 0, v_issued = 0;
             if (lane == 0) {
-                const uint32_t qf = smem_u32(&bar->q_full);
-                mbar_arrive_expect_tx(qf, 2 * C::kTile);
-                for (int c = 0; c < D / 64; ++c) {
-                    tma_load_4d(smem_u32(sQ + c * C::kChunk), &tmQ, qf, 64 * c, r0, h * p.q_mh,
-                                b * p.q_mb);
-                    tma_load_4d(smem_u32(sO + c * C::kChunk), &tmO, qf, 64 * c, r0, h * p.o_mh,
-                                b * p.o_mb);
-                }
                 for (int i = 0; i < E; ++i) {
                     const int row = chunk_of(i) * kT, ks = i % C::kKStages, vs = i % C::kVStages;
                     const int kr = i / C::kKStages, vr = i / C::kVStages;
@@ -944,9 +983,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(smem_u32(&bar->a_ready));
         }
+        const ChunkList list = it.list;
         for (int i = 0; ok && i < E; ++i) {
             const int c = chunk_of(i), base = c * kT + 64 * wg;
-            const bool full = cl.full(c);
+            const bool full = list.full(c);
             uint32_t keep[2] = {0u, 0u};
             if (!full) {
 #pragma unroll
@@ -1021,11 +1061,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->dq_done), (E - 1) & 1, abort_flag));
             tc_fence_after();
         }
-        if (ok) {
-            char *dst = qrow < nq ? p.dq.p + 2 * (b * p.dq.sb + h * p.dq.sh + qrow * p.dq.st +
-                                                  wg * (D / 2))
-                                  : nullptr;
-            store_row<D / 2, F16>(tmem + lane_base + kDQ + wg * (D / 2), dst, p.scale, E > 0);
+        if (ok) {  // through Q's tile, which went to TMEM before the first step
+            put_row_16<D / 2, F16>(tmem + lane_base + kDQ + wg * (D / 2), smem_u32(sQ), C::kChunk,
+                                   row, wg * (D / 16), p.scale, E > 0);
+            copy_rows_out<D / 16>(smem_u32(sQ), C::kChunk, row - lane, wg * (D / 16),
+                                  p.dq.p + 2 * (b * p.dq.sb + h * p.dq.sh + (qrow - lane) * p.dq.st +
+                                                wg * (D / 2)),
+                                  2 * p.dq.st, nq - (qrow - lane), lane);
         }
     }
     tc_fence_before();

@@ -32,6 +32,7 @@
 
 #include "stream.h"
 #include "svga_device.cuh"
+#include "tile_out.cuh"
 
 namespace svga {
 namespace {
@@ -82,21 +83,6 @@ struct Cfg {
     static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
 };
 
-struct Barriers {
-    uint64_t q_full;
-    uint64_t kv_full[8], kv_empty[8];
-    uint64_t s_full[2];    // [group]: that group's S is in the S columns
-    uint64_t s_free[2];    // S columns were read into registers (4 warps); [group] with an S
-                           // tile each, [0] when they share one
-    uint64_t s_issued[8];  // [visit % 8]: the S issuer has issued the S of that visit
-    uint64_t p_full[2];    // [group]: P of the group's tile is in its P columns (4 warps)
-    uint64_t o_done[2];    // [group]: the group's last P V product is done
-    uint64_t drain[2];     // abort: [issuer]: the MMAs that issuer started are done
-    uint64_t zero_req, zero_done;  // the ragged V chunk landed / its rows past the end are 0
-    uint32_t tmem_base;
-    int abort;
-};
-
 constexpr uint32_t kV0 = 1, kF0 = 2, kV1 = 4, kF1 = 8;
 
 // One CTA's work: two query blocks of one head and its share of their merged chunk list.
@@ -119,6 +105,23 @@ struct Item {
         if (valid1 && l1.visits(c)) f |= kV1 | (l1.full(c) ? kF1 : 0u);
         return f;
     }
+};
+
+struct Barriers {
+    uint64_t q_full;
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t s_full[2];    // [group]: that group's S is in the S columns
+    uint64_t s_free[2];    // S columns were read into registers (4 warps); [group] with an S
+                           // tile each, [0] when they share one
+    uint64_t s_issued[8];  // [visit % 8]: the S issuer has issued the S of that visit
+    uint64_t p_full[2];    // [group]: P of the group's tile is in its P columns (4 warps)
+    uint64_t o_done[2];    // [group]: the group's last P V product is done
+    uint64_t drain[2];     // abort: [issuer]: the MMAs that issuer started are done
+    uint64_t zero_req, zero_done;  // the ragged V chunk landed / its rows past the end are 0
+    uint32_t tmem_base;
+    int abort;
+    int some;   // the item has queries
+    Item item;  // worked out by warp 0 for all: by every warp it took 2,000 cycles more
 };
 
 // The merged chunk list of two consecutive runs of queries.  The windows of consecutive
@@ -202,12 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    Item it;
-    if (!make_item(p, it)) return;  // past the sequence's queries (uniform over the CTA)
-    // the chunk whose last rows lie past the sequence's end but inside the tensor
-    const int ragged = (p.s.k_lens && it.nk < p.s.tk && it.nk % kKN) ? it.nk / kKN : -1;
-
     if (threadIdx.x == 0) {
+        prefetch_tmap(&tmQ);
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
         mbar_init(smem_u32(&bar->q_full), 1);
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(smem_u32(&bar->kv_full[s]), 1);
@@ -230,42 +231,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&bar->tmem_base), 512);
         tmem_relinquish();
     }
+    Item it;
+    bool some = false;
+    if (warp == 0) {
+        some = make_item(p, it);  // false: past the sequence's queries
+        if (lane == 0) {
+            bar->item = it;
+            bar->some = some;
+        }
+    }
+    // K (idx even) or V of entry idx / 2 into its stage
+    auto fetch = [&](int idx) {
+        const int s = idx % C::kStages, t = idx & 1, row = it.chunk(idx >> 1) * kKN;
+        const int hk = it.h / p.s.group;
+        const uint32_t fb = smem_u32(&bar->kv_full[s]);
+        mbar_arrive_expect_tx(fb, C::kKVBytes);
+        for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(smem_u32(sKV + s * C::kKVBytes + c * C::kKVChunk), t ? &tmV : &tmK, fb,
+                        64 * c, row, hk * (t ? p.v_mh : p.k_mh), it.b * (t ? p.v_mb : p.k_mb));
+    };
+    // The first loads are on their way before the CTA meets: the producer is the thread that
+    // set the barriers up.
+    int fetched = 0;
+    if (some && threadIdx.x == 0 && it.E > 0) {
+        const uint32_t qf = smem_u32(&bar->q_full);
+        const int nq_tiles = it.valid1 ? 2 : 1;
+        mbar_arrive_expect_tx(qf, nq_tiles * C::kQBytes);
+        for (int i = 0; i < nq_tiles; ++i) {
+            for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(smem_u32(sQ + i * C::kQBytes + c * C::kQChunk), &tmQ, qf, 64 * c,
+                            (it.b0 + (p.by_heads ? 0 : i)) * kBlockM,
+                            (it.h + (p.by_heads ? i : 0)) * p.q_mh, it.b * p.q_mb);
+            if (i == 0) fetch(fetched++);  // K of the first entry behind the first Q tile
+        }
+        while (fetched < min(C::kStages, 2 * it.E)) fetch(fetched++);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem_base;
+    if (!bar->some) {
+        if (warp == 1) tmem_dealloc(tmem, 512);
+        return;
+    }
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsLow>();
+        it = bar->item;
+        // the chunk whose last rows lie past the sequence's end but inside the tensor
+        const int ragged = (p.s.k_lens && it.nk < p.s.tk && it.nk % kKN) ? it.nk / kKN : -1;
         if (warp == 0 && lane == 0 && it.E > 0) {
             // -------------------------------------------------------- TMA producer
             const uint32_t qf = smem_u32(&bar->q_full);
-            const int nq_tiles = it.valid1 ? 2 : 1, hk = it.h / p.s.group;
-            mbar_arrive_expect_tx(qf, nq_tiles * C::kQBytes);
-            for (int i = 0; i < nq_tiles; ++i)
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem_u32(sQ + i * C::kQBytes + c * C::kQChunk), &tmQ, qf, 64 * c,
-                                (it.b0 + (p.by_heads ? 0 : i)) * kBlockM,
-                                (it.h + (p.by_heads ? i : 0)) * p.q_mh, it.b * p.q_mb);
-            int issued = 0;
-            bool ok = true;
-            for (int n = 0; n < it.E && ok; ++n) {
-                const int row = it.chunk(n) * kKN;
-                for (int t = 0; t < 2; ++t) {
-                    const int idx = 2 * n + t, s = idx % C::kStages, round = idx / C::kStages;
-                    if (round > 0 &&
-                        !mbar_wait(smem_u32(&bar->kv_empty[s]), (round - 1) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = smem_u32(&bar->kv_full[s]);
-                    mbar_arrive_expect_tx(fb, C::kKVBytes);
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_4d(smem_u32(sKV + s * C::kKVBytes + c * C::kKVChunk),
-                                    t ? &tmV : &tmK, fb, 64 * c, row,
-                                    hk * (t ? p.v_mh : p.k_mh), it.b * (t ? p.v_mb : p.k_mb));
-                    issued = idx + 1;
-                }
+            int issued = fetched;
+            for (; issued < 2 * it.E; ++issued) {
+                const int s = issued % C::kStages, round = issued / C::kStages;
+                if (!mbar_wait(smem_u32(&bar->kv_empty[s]), (round - 1) & 1, abort_flag)) break;
+                fetch(issued);
             }
             // every copy lands before the CTA can exit, whichever role aborts
             mbar_wait_bounded(qf, 0);
@@ -408,19 +430,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_base + wg * T::kS1;
         const uint32_t tP = tmem + lane_base + T::kP + wg * 64;
         const uint32_t tO = tmem + lane_base + T::kO + wg * T::kOStep;
-        const int qrow = (it.b0 + (p.by_heads ? 0 : wg)) * kBlockM + row;
-        const bool row_valid = qrow < it.nq;
+        // what the loop needs of the item stays in registers, the rest in shared memory
+        const Item &item = bar->item;
+        const ChunkList list = wg ? item.l1 : item.l0;
+        const bool mine = wg == 0 || item.valid1;
+        const int first = item.e0, end = mine ? first + item.E : first;
+        const int sinks = item.a, skip = item.skip;
+        const int qrow = (item.b0 + (p.by_heads ? 0 : wg)) * kBlockM + row;
+        const bool row_valid = qrow < item.nq;
         MaskRange mr = {0, 0, 0};
-        if (row_valid) mr = mask_range(p.s.mask, qrow + it.nk - it.nq, it.nk);
-        const uint32_t vbit = wg ? kV1 : kV0, fbit = wg ? kF1 : kF0;
+        if (row_valid) mr = mask_range(p.s.mask, qrow + item.nk - item.nq, item.nk);
         const float sl2 = p.scale_log2;
         float m_used = -INFINITY, l = 0.f;
         int visit = 0;
         bool ok = true;
-        for (int n = 0; n < it.E; ++n) {
-            const int chunk = it.chunk(n);
-            const uint32_t f = it.flags(chunk);
-            if (!(f & vbit)) continue;
+        for (int e = first; e < end; ++e) {
+            const int chunk = e < sinks ? e : skip + e - sinks;
+            if (!list.visits(chunk)) continue;
             ok = __all_sync(0xffffffffu,
                             mbar_wait(smem_u32(&bar->s_full[wg]), visit & 1, abort_flag));
             tc_fence_after();
@@ -433,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();  // S is in registers: its columns may take another visit's
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar->s_free[T::kTwoS ? wg : 0]));
-            if (!(f & fbit)) {
+            if (!list.full(chunk)) {
                 const int k0 = chunk * kKN;
 #pragma unroll
                 for (int w = 0; w < kKN / 32; ++w) {
@@ -521,42 +547,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_wait(smem_u32(&bar->o_done[wg]), (visit - 1) & 1, abort_flag));
             tc_fence_after();
         }
+        const Item &it = item;
         const bool split = it.ksplit > 1;
         if (ok && (wg == 0 || it.valid1)) {
             const float inv = split ? 1.f : (l == 0.f ? 0.f : 1.f / l);
             const int h = it.h + (p.by_heads ? wg : 0);
             const long long flat = ((long long)it.b * p.s.hq + h) * p.s.tq + qrow;
             const long long part = it.slot * 2 * kBlockM + wg * kBlockM + row;
-            char *orow = p.o.p + 2 * (it.b * p.o.sb + h * p.o.sh + qrow * p.o.st);
+            // through this group's Q tile, whose last product is done
+            const uint32_t tile = smem_u32(sQ + wg * C::kQBytes);
+            const int valid = it.nq - (qrow - lane);  // of the warp's rows
+            if (!split) {
+                put_row_16<D, F16>(tO, tile, C::kQChunk, row, 0, inv, visit > 0);
+                copy_rows_out<D / 8>(tile, C::kQChunk, row - lane, 0,
+                                     p.o.p + 2 * (it.b * p.o.sb + h * p.o.sh +
+                                                  (qrow - lane) * p.o.st),
+                                     2 * p.o.st, valid, lane);
+            } else {  // the tile holds half of a row of fp32
 #pragma unroll 1
-            for (int j = 0; j < D / 32; ++j) {
-                uint32_t o[32];
-                if (visit > 0) {
-                    tmem_ld32(tO + j * 32, o);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) o[c] = 0u;
-                }
-                if (!row_valid) continue;
-                if (split) {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + part * D + j * 32);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                             __uint_as_float(o[4 * c + 2]),
-                                             __uint_as_float(o[4 * c + 3]));
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(orow + 64 * j);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[i] = pack_16x2<F16>(__uint_as_float(o[8 * c + 2 * i]) * inv,
-                                                  __uint_as_float(o[8 * c + 2 * i + 1]) * inv);
-                        dst[c] = make_uint4(x[0], x[1], x[2], x[3]);
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    put_row_32<D / 2>(tO + j * (D / 2), tile, C::kQChunk, row, visit > 0);
+                    copy_rows_out<D / 8>(tile, C::kQChunk, row - lane, 0,
+                                         reinterpret_cast<char *>(p.part_o + (part - lane) * D +
+                                                                  j * (D / 2)),
+                                         4 * D, valid, lane);
                 }
             }
             if (row_valid && split)
