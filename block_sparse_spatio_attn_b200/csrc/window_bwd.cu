@@ -72,6 +72,7 @@ struct BwdParams {
     float *stats;  // [batch * hq][query block][2][128]: -lse log2(e), -D
     float scale, scale_log2;
     int n_qblk, n_kblk;
+    int n_dkdv;    // CTAs of dkdv
     Split split;   // over dkdv's items, key blocks ascending
     float *parts;  // [slot][dV, dK][128][d]
     int q_mb, q_mh, o_mb, o_mh, k_mb, k_mh, v_mb, v_mh;  // coordinate multipliers (o: dO)
@@ -249,10 +250,10 @@ struct KvItem {
     long long slot;
 };
 
-__device__ __forceinline__ bool make_item(const BwdParams &p, KvItem &it)
+__device__ __forceinline__ bool make_item(const BwdParams &p, int block, KvItem &it)
 {
     int item, part;
-    p.split.of_block(blockIdx.x, item, part);
+    p.split.of_block(block, item, part);
     it.ksplit = p.split.k(item);
     it.slot = it.ksplit > 1 ? p.split.slot(item, part) : 0;
     const int bh = p.s.batch * p.s.hk;
@@ -305,15 +306,12 @@ struct KvBars {
 static_assert(sizeof(KvBars) <= 512, "barrier space");
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
-    bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
-                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const BwdParams p)
+__device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorMap &tmO,
+                                         const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                         const BwdParams &p, uint8_t *smem, int block)
 {
     using C = Cfg<D>;
     constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    if (smem_misplaced(smem, p.s.status)) return;
     uint8_t *sK = smem, *sV = smem + C::kTile;
     uint8_t *sQ = smem + 2 * C::kTile;              // [stage]
     uint8_t *sO = sQ + C::kQStages * C::kTile;      // [stage]
@@ -355,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0) {
         KvItem mine;
-        const bool some = make_item(p, mine);  // false: past the sequence's keys
+        const bool some = make_item(p, block, mine);  // false: past the sequence's keys
         if (lane == 0) {
             bar->item = mine;
             bar->some = some;
@@ -725,11 +723,11 @@ struct DqItem {
     int skip, E;  // the chunks: 0 .. list.a - 1, then skip, skip + 1, ...; how many
 };
 
-__device__ __forceinline__ bool make_item(const BwdParams &p, DqItem &it)
+__device__ __forceinline__ bool make_item(const BwdParams &p, int block, DqItem &it)
 {
     // last blocks first: the longest under a causal mask
     const int bh = p.s.batch * p.s.hq;
-    const int slot = blockIdx.x / bh, r = blockIdx.x - slot * bh;
+    const int slot = block / bh, r = block - slot * bh;
     it.b = r / p.s.hq;
     it.h = r - it.b * p.s.hq;
     it.hk = it.h / p.s.group;
@@ -761,15 +759,12 @@ struct DqBars {
 static_assert(sizeof(DqBars) <= 512, "barrier space");
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
-    bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
-                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const BwdParams p)
+__device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap &tmO,
+                                       const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                       const BwdParams &p, uint8_t *smem, int block)
 {
     using C = Cfg<D>;
     constexpr uint32_t kS = 0, kDP = 128, kDQ = 256, kDS = 384, kQ = 448;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    if (smem_misplaced(smem, p.s.status)) return;
     uint8_t *sQ = smem, *sO = smem + C::kTile;
     uint8_t *sK = smem + 2 * C::kTile;          // [stage]
     uint8_t *sV = sK + C::kKStages * C::kTile;  // [stage]
@@ -809,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0) {
         DqItem mine;
-        const bool some = make_item(p, mine);  // false: past the sequence's queries
+        const bool some = make_item(p, block, mine);  // false: past the sequence's queries
         if (lane == 0) {
             bar->item = mine;
             bar->some = some;
@@ -1080,6 +1075,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicExch(p.s.status, (int32_t)SVGA_ERR_TIMEOUT);
 }
 
+// dkdv's CTAs, the longer ones, then dq's: the two need nothing of each other, and in one launch
+// dq's fill the SMs that dkdv's last round leaves idle.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+               const __grid_constant__ BwdParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_misplaced(smem, p.s.status)) return;
+    if ((int)blockIdx.x < p.n_dkdv)
+        dkdv_cta<D, F16>(tmQ, tmO, tmK, tmV, p, smem, blockIdx.x);
+    else
+        dq_cta<D, F16>(tmQ, tmO, tmK, tmV, p, smem, blockIdx.x - p.n_dkdv);
+}
+
 template <typename K>
 svga_status prepare(K kfn, int smem, const char *what)
 {
@@ -1109,9 +1120,8 @@ svga_status launch(const svga_view &d_o, const svga_view &q, const svga_view &k,
 {
     using C = Cfg<D>;
     svga_status rc;
-    if ((rc = prepare(bwd_dkdv_kernel<D, F16>, C::kKvAlloc, "window dK/dV")) != SVGA_OK ||
-        (rc = prepare(bwd_dq_kernel<D, F16>, C::kDqAlloc, "window dQ")) != SVGA_OK)
-        return rc;
+    constexpr int kAlloc = C::kKvAlloc > C::kDqAlloc ? C::kKvAlloc : C::kDqAlloc;
+    if ((rc = prepare(bwd_kernel<D, F16>, kAlloc, "window backward")) != SVGA_OK) return rc;
     alignas(64) CUtensorMap tq, to, tk, tv;
     // an empty side is never loaded: its maps only have to be valid
     const bool hq = p->q_tokens > 0, hk = p->k_tokens > 0;
@@ -1130,21 +1140,15 @@ svga_status launch(const svga_view &d_o, const svga_view &q, const svga_view &k,
         bwd_rows_kernel<D, F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp);
         if ((rc = check_launch_of("window backward rows")) != SVGA_OK) return rc;
     }
-    if (hk) {
-        const unsigned grid = (unsigned)kp.split.ctas();
-        bwd_dkdv_kernel<D, F16><<<grid, kThreads, C::kKvAlloc, st>>>(tq, to, tk, tv, kp);
-        if ((rc = check_launch_of("window dK/dV")) != SVGA_OK) return rc;
-        if (kp.split.slots() > 0) {
-            const long long n =
-                (long long)(kp.split.split_to() - kp.split.split_from()) * 2 * kT * (D / 8);
-            bwd_join_kernel<D, F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp);
-            if ((rc = check_launch_of("window dK/dV join")) != SVGA_OK) return rc;
-        }
-    }
-    if (hq) {
-        const unsigned grid = (unsigned)((long long)p->batch * p->q_heads * kp.n_qblk);
-        bwd_dq_kernel<D, F16><<<grid, kThreads, C::kDqAlloc, st>>>(tq, to, tk, tv, kp);
-        rc = check_launch_of("window dQ");
+    kp.n_dkdv = hk ? (int)kp.split.ctas() : 0;
+    const long long n_dq = hq ? (long long)p->batch * p->q_heads * kp.n_qblk : 0;
+    bwd_kernel<D, F16><<<(unsigned)(kp.n_dkdv + n_dq), kThreads, kAlloc, st>>>(tq, to, tk, tv, kp);
+    if ((rc = check_launch_of("window backward")) != SVGA_OK) return rc;
+    if (hk && kp.split.slots() > 0) {
+        const long long n =
+            (long long)(kp.split.split_to() - kp.split.split_from()) * 2 * kT * (D / 8);
+        bwd_join_kernel<D, F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp);
+        rc = check_launch_of("window backward join");
     }
     return rc;
 }
