@@ -1168,10 +1168,15 @@ static size_t stats_bytes(const svga_window_problem *p)
 
 // How dkdv's items are split.  Items are key blocks; the ones that hold sinks, first in launch
 // order, are kept by every later query of a causal mask, the others by a window of them.
-// `per_sm` is the launch's steps divided by the SMs: an item longer than that holds up the
-// whole launch.  With fewer items than SMs parts are as short as still fit in one round of
-// CTAs; otherwise an item is split when it is longer than per_sm (sinks: 3/4 of it, they are
-// launched first and the rest fills in behind them).  Measured: FIGURES_DKDV.
+// `per_sm` is the launch's work divided by the SMs, in steps of dkdv (dq has as many steps,
+// at about three quarters of the time): a longer item holds up the whole launch, while parts
+// cost their sums in memory and a join.  Sinks are split above per_sm, others, which overlap
+// less, above 1.25 of it, and nothing into parts of fewer than 8 steps, unless the whole launch
+// is less than one round of CTAs: then as finely as still fits in one.  Measured (backward in
+// all, split against not, us): 8,192 tokens causal, 8 heads on 2: 391 against 442; 13 frames of
+// 960 tokens, sinks of 98 steps, per_sm 133: 281 against 266; 2,048 tokens causal, 4 heads: 53
+// against 41; 2 x 2,001 tokens in a window with sinks, per_sm 18, sinks of 64 steps: 56 against
+// 165; 500 tokens, 2 heads on 1: 21 against 27.
 static Split choose_bwd_split(const svga_window_problem *p)
 {
     const long long heads = (long long)p->batch * p->kv_heads;
@@ -1203,20 +1208,18 @@ static Split choose_bwd_split(const svga_window_problem *p)
         }
         mean[w] /= std::max(count, 1);
     }
-    const double per_sm = heads * (sinks * mean[0] + (blocks - sinks) * mean[1]) / kSms;
+    const double per_sm = 1.75 * heads * (sinks * mean[0] + (blocks - sinks) * mean[1]) / kSms;
     auto parts = [](long long x, double most) {
         return (int)std::max(1ll, std::min(64ll, (long long)std::ceil(x / most)));
     };
     s.n1 = (int)(heads * sinks);
-    if (n < kSms) {
-        for (double most = std::max(per_sm, 2.0);; most *= 1.1) {
-            s.k1 = parts(top[0], most);
-            s.k2 = parts(top[1], most);
-            if (s.ctas() <= kSms || (s.k1 == 1 && s.k2 == 1)) break;
-        }
-    } else {
-        s.k1 = parts(top[0], std::max(0.75 * per_sm, 4.0));
-        s.k2 = parts(top[1], std::max(per_sm, 4.0));
+    s.k1 = parts(top[0], std::max(per_sm, 8.0));
+    s.k2 = parts(top[1], std::max(1.25 * per_sm, 8.0));
+    const long long free = kSms - (long long)p->batch * p->q_heads * ((p->q_tokens + kT - 1) / kT);
+    for (double most = 2.0; n <= free; most *= 1.25) {  // one round in all: fill it
+        s.k1 = parts(top[0], most);
+        s.k2 = parts(top[1], most);
+        if (s.ctas() <= free) break;
     }
     return s;
 }
