@@ -195,6 +195,28 @@ svga_status launch_window_bwd(const svga_view &d_o, const svga_view &q, const sv
 
 svga_status check_launch_of(const char *what);  // cudaGetLastError as a status
 
+#ifdef __CUDACC__
+// Launch of a kernel that begins while the one before it in the stream is still running and
+// waits for it itself (pdl_wait, in every CTA, before it touches what that one writes).
+template <typename... Params, typename... Args>
+svga_status launch_after(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem,
+                         cudaStream_t st, const char *what, const Args &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return check_launch_of(what);
+    return SVGA_OK;
+}
+#endif
+
 inline Mask to_mask(const svga_window_mask &m)
 {
     return {m.causal, m.window, m.sinks, m.block};

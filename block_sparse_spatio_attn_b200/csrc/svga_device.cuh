@@ -546,6 +546,16 @@ __device__ __forceinline__ float fmax3(float a, float b, float c)
     return d;
 }
 
+// Programmatic dependent launch.  pdl_start lets the next kernel of the stream be launched once
+// every CTA of this one has called it; pdl_wait, which that kernel calls, returns when this one
+// has completed and its writes can be read (at once, if it was launched the ordinary way).
+__device__ __forceinline__ void pdl_start()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <uint32_t N>
 __device__ __forceinline__ void setmaxnreg_inc()
 {

@@ -134,6 +134,7 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) bwd_rows_kernel(const BwdParams p)
 {
+    pdl_start();
     constexpr int kPer = D / 8;
     const long long i = blockIdx.x * 256ll + threadIdx.x;
     const long long row = i / kPer, bh = row / (p.n_qblk * kT);
@@ -369,6 +370,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
             }
         }
     }
+    pdl_start();  // the join, if there is one
+    pdl_wait();   // the rows' statistics
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -679,6 +682,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) bwd_join_kernel(const BwdParams p)
 {
+    pdl_wait();  // the parts
     constexpr int kPer = D / 8;
     const long long i = blockIdx.x * 256ll + threadIdx.x;
     const int c = 8 * (int)(i % kPer);
@@ -820,6 +824,8 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
             }
         }
     }
+    pdl_start();  // the join, if there is one
+    pdl_wait();   // the rows' statistics
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1142,13 +1148,20 @@ svga_status launch(const svga_view &d_o, const svga_view &q, const svga_view &k,
     }
     kp.n_dkdv = hk ? (int)kp.split.ctas() : 0;
     const long long n_dq = hq ? (long long)p->batch * p->q_heads * kp.n_qblk : 0;
-    bwd_kernel<D, F16><<<(unsigned)(kp.n_dkdv + n_dq), kThreads, kAlloc, st>>>(tq, to, tk, tv, kp);
-    if ((rc = check_launch_of("window backward")) != SVGA_OK) return rc;
+    const unsigned grid = (unsigned)(kp.n_dkdv + n_dq);
+    if (hq) {
+        rc = launch_after(bwd_kernel<D, F16>, grid, kThreads, kAlloc, st, "window backward", tq, to,
+                          tk, tv, kp);
+    } else {  // no rows kernel before it
+        bwd_kernel<D, F16><<<grid, kThreads, kAlloc, st>>>(tq, to, tk, tv, kp);
+        rc = check_launch_of("window backward");
+    }
+    if (rc != SVGA_OK) return rc;
     if (hk && kp.split.slots() > 0) {
         const long long n =
             (long long)(kp.split.split_to() - kp.split.split_from()) * 2 * kT * (D / 8);
-        bwd_join_kernel<D, F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp);
-        rc = check_launch_of("window backward join");
+        rc = launch_after(bwd_join_kernel<D, F16>, (unsigned)((n + 255) / 256), 256, 0, st,
+                          "window backward join", kp);
     }
     return rc;
 }

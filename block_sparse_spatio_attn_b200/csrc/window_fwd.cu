@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         while (fetched < min(C::kStages, 2 * it.E)) fetch(fetched++);
     }
+    pdl_start();  // the join, if there is one
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -596,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool F16>
 __global__ void __launch_bounds__(256) join_kernel(const FwdParams p, int d)
 {
+    pdl_wait();  // the parts
     const int per = d / 8;
     const long long i = blockIdx.x * 256ll + threadIdx.x;
     const long long all = i / per;
@@ -726,8 +728,8 @@ svga_status launch(const svga_view &q, const svga_view &k, const svga_view &v, F
     if (rc != SVGA_OK || kp.split.slots() == 0) return rc;
     const long long n = (long long)(kp.split.split_to() - kp.split.split_from()) * 2 * kBlockM *
                         (D / 8);
-    join_kernel<F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp, D);
-    return check_launch_of("window attention join");
+    return launch_after(join_kernel<F16>, (unsigned)((n + 255) / 256), 256, 0, st,
+                        "window attention join", kp, D);
 }
 
 }  // namespace
