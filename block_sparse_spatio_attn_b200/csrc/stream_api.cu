@@ -353,6 +353,9 @@ svga_status svga_window_attention_fwd(const svga_view *q, const svga_view *k, co
     if ((rc = check_workspace(workspace, workspace_bytes, window_fwd_workspace(p))) != SVGA_OK)
         return rc;
     if (B == 0 || p->q_tokens == 0) return SVGA_OK;
+    if (o->data == q->data || o->data == k->data || o->data == v->data)
+        return bad(SVGA_ERR_INVALID_ARG, "%so starts where q, k or v does: it is written while they "
+                                         "are read");
     return launch_window_fwd(*q, *k, *v, *o, lse, p, scale, workspace, stream);
 }
 
@@ -383,6 +386,13 @@ svga_status svga_window_attention_bwd(const svga_view *d_o, const svga_view *q, 
     if ((rc = check_workspace(workspace, workspace_bytes, window_bwd_workspace(p))) != SVGA_OK)
         return rc;
     if (B == 0 || (p->q_tokens == 0 && p->k_tokens == 0)) return SVGA_OK;
+    for (const auto &x : views)
+        for (const auto &y : views)
+            if (x.write && !y.write && x.tokens > 0 && y.tokens > 0 && x.v->data == y.v->data) {
+                set_error("%s starts where %s does: it is written while that is read", x.name,
+                          y.name);
+                return SVGA_ERR_INVALID_ARG;
+            }
     return launch_window_bwd(*d_o, *q, *k, *v, *o, lse, *dq, *dk, *dv, p, scale, workspace, stream);
 }
 

@@ -189,6 +189,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// The same for a role that waits for a late moment of its CTA's work, which may be many waits of
+// the other roles away: a limit of 64 seconds.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *abort)
+{
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_sleep(bar, parity)) {
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > 64 * kWaitLimitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // Bounded wait that ignores the abort flag: used while draining after an abort.
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity)
 {

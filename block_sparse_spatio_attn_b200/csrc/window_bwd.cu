@@ -526,8 +526,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                  i += n_blk, ++time) {
                 bool ok = true;
                 for (int w = 0; w < 2 && ok; ++w) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->zero_req[w]), time & 1,
-                                                           abort_flag));
+                    ok = __all_sync(0xffffffffu, mbar_wait_long(smem_u32(&bar->zero_req[w]),
+                                                                time & 1, abort_flag));
                     if (!ok) break;
                     zero_rows<D>(smem_u32(w ? sO + (i % C::kOStages) * C::kTile
                                             : sQ + (i % C::kQStages) * C::kTile),
@@ -1208,11 +1208,11 @@ static Split choose_bwd_split(const svga_window_problem *p)
         end = std::max(end, end1);
         return end > first ? (long long)group * ((end + kT - 1) / kT - first / kT) : 0ll;
     };
-    // the longest and the mean of either kind, over at most 256 blocks of each
+    // the longest and the mean of either kind, over at most 64 blocks of each
     long long top[2] = {0, 0};
     double mean[2] = {0, 0};
     for (int w = 0; w < 2; ++w) {
-        const int from = w ? sinks : 0, to = w ? blocks : sinks, stride = (to - from) / 256 + 1;
+        const int from = w ? sinks : 0, to = w ? blocks : sinks, stride = (to - from) / 64 + 1;
         int count = 0;
         for (int kb = from; kb < to; kb += stride, ++count) {
             const long long x = steps_of(kb);

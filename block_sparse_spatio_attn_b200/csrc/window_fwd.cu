@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = it.E - 1;  // the ragged chunk is a sequence's last: its entry, if any
             while (n >= 0 && it.chunk(n) > ragged) --n;
             if (n >= 0 && it.chunk(n) == ragged) {
-                const bool ok = mbar_wait(smem_u32(&bar->zero_req), 0, abort_flag);
+                const bool ok = mbar_wait_long(smem_u32(&bar->zero_req), 0, abort_flag);
                 if (__all_sync(0xffffffffu, ok)) {
                     const uint32_t base =
                         smem_u32(sKV + ((2 * n + 1) % C::kStages) * C::kKVBytes);

@@ -549,7 +549,7 @@ def _binding():
     return _native
 
 
-@dataclass
+@dataclass(frozen=True)
 class RotarySpec:
     """Rotary positions on the three axes of a grid (svga_rotary_spec): frames x grid_h x
     grid_w tokens, pairs = turned pairs of the frame, row and column axis; order = a token
@@ -563,13 +563,17 @@ class RotarySpec:
     order: Optional[Sequence[int]] = None
 
     def __post_init__(self):
-        self._od = None if self.order is None else (ctypes.c_int32 * len(self.order))(*self.order)
-        self.c = RotarySpecC(self.num_frames, self.grid_h, self.grid_w,
-                             (ctypes.c_int * 3)(*self.pairs), int(self.interleaved), self._od)
-
-        self.rows = (self.num_frames * self.pairs[0] + self.grid_h * self.pairs[1] +
-                     self.grid_w * self.pairs[2])
-        self.ordered_heads = -1 if self.order is None else len(self.order)
+        if len(self.pairs) != 3:
+            raise SvgaError(2, f"pairs names {len(self.pairs)} axes, not 3")
+        od = None if self.order is None else (ctypes.c_int32 * len(self.order))(*self.order)
+        c = RotarySpecC(self.num_frames, self.grid_h, self.grid_w, (ctypes.c_int * 3)(*self.pairs),
+                        int(self.interleaved), od)
+        rows = (self.num_frames * self.pairs[0] + self.grid_h * self.pairs[1] +
+                self.grid_w * self.pairs[2])
+        # what the library reads, filled once (frozen: it cannot fall behind the fields)
+        for name, x in (("_od", od), ("c", c), ("rows", rows),
+                        ("ordered_heads", -1 if od is None else len(self.order))):
+            object.__setattr__(self, name, x)
 
     @property
     def table_shape(self):
@@ -599,7 +603,7 @@ def svga_rotary(src, dst, spec: RotarySpec, table, positions=None, first_token: 
     return dst
 
 
-@dataclass
+@dataclass(frozen=True)
 class WindowMask:
     """The mask of the window calls (svga_window_mask): block = 1 counts the window in
     tokens, block = grid_h * grid_w in frames; window = -1 is unbounded."""
@@ -609,11 +613,14 @@ class WindowMask:
     block: int = 1
 
     def __post_init__(self):
-        self.c = WindowMaskC(int(self.causal), self.window, self.sinks, self.block)
+        object.__setattr__(self, "c", WindowMaskC(int(self.causal), self.window, self.sinks,
+                                                  self.block))
 
 
 def svga_window_attention_size(q, k, mask: WindowMask) -> dict:
     """Bytes of workspace of the forward and the backward call on tensors shaped like q and k."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise SvgaError(2, "q and k must be tensors of 4 dimensions")
     (B, H, Tq, d), (_, G, Tk, _) = q.shape, k.shape
     c = WindowProblemC(B, H, G, Tq, Tk, d, 1 if q.dtype == torch.float16 else 0, mask.c)
     n = [ctypes.c_size_t() for _ in range(2)]

@@ -534,8 +534,9 @@ typedef struct {
  *                    own queries and keys, clamped to 0 .. q_tokens / k_tokens.  Rows at
  *                    and past them are never written, and what they hold (NaN included)
  *                    changes nothing.
- * A non-finite value in a key or value row a sequence does own can reach every query of
- * the 128 x 128 tiles that visit the key, also those whose mask drops it. */
+ * A non-finite value in a row a sequence does own (of k or v; of q or d_o in the backward
+ * call) can reach the whole 128 x 128 tiles that visit the row, also the pairs whose mask
+ * drops it.  Written tensors must not overlap read ones (the same start is refused). */
 typedef struct {
     int batch;
     int q_heads;

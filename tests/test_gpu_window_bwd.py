@@ -141,6 +141,24 @@ def test_padded_batch_with_garbage_past_the_lengths(dtype, d):
         run(q, k, v, do, mask, 0.1, q_lens, k_lens)
 
 
+def test_sinks_split_over_ctas():
+    """Sink blocks of 60 steps beside others of a few, more items than one round of CTAs, a
+    padded batch: the split and joined path with whole items beside it."""
+    B, H, G, T = 2, 10, 5, 1500
+    q, do = (values(B, H, T, 64, dtype=BF, seed=s) for s in (1, 2))
+    k, v = (values(B, G, T, 64, dtype=BF, seed=s) for s in (3, 4))
+    mask, q_lens, k_lens = M(window=100, sinks=130), [1500, 1111], [1500, 1300]
+    dev = [x.cuda() for x in (q, k, v, do)]
+    size = svga.svga_window_attention_size(dev[0], dev[1], mask)["bwd_bytes"]
+    assert size > 4 * B * H * 12 * 256  # the rows' statistics and the parts
+    _, _, grads = both_passes(*dev, mask, 0.125, q_lens, k_lens)
+    for b in range(B):  # one key head of each sequence
+        g, pair = 4 * b, slice(8 * b, 8 * b + 2)
+        check(q[b:b + 1, pair], k[b:b + 1, g:g + 1], v[b:b + 1, g:g + 1], do[b:b + 1, pair], mask, 0.125,
+              [grads[0][b:b + 1, pair], grads[1][b:b + 1, g:g + 1], grads[2][b:b + 1, g:g + 1]],
+              q_lens[b:b + 1], k_lens[b:b + 1])
+
+
 def test_gradients_are_the_differences_of_the_forward_pass():
     """d/dt <o(x + t u), g> at t = 0 in 64 bits, by a central difference of step 2^-12 (its
     error is below 1e-6 of values of order 1), against <gradient, u>."""

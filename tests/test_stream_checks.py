@@ -135,6 +135,15 @@ def rejected(fn, status, words):
     assert e.value.status == status and words in str(e.value), str(e.value)
 
 
+def test_specs_and_masks_cannot_fall_behind_their_fields():
+    import dataclasses
+    for x, name in ((svga.RotarySpec(1, 2, 5, (10, 11, 11)), "num_frames"), (svga.WindowMask(), "window")):
+        with pytest.raises(dataclasses.FrozenInstanceError):
+            setattr(x, name, 3)
+    assert dataclasses.replace(svga.WindowMask(sinks=2), window=5).c.window == 5
+    rejected(lambda: svga.RotarySpec(1, 2, 5, (10, 11)), 2, "2 axes")
+
+
 def test_binding_checks():
     spec = svga.RotarySpec(1, 2, 5, (10, 11, 11))
     x, t = torch.zeros(1, 2, 10, 64, dtype=torch.bfloat16), torch.zeros(spec.table_shape)
@@ -233,6 +242,17 @@ def test_window_scale_lse_and_workspace_refusals(lib):
         refused(window_calls(lib, p, ws=ws, n=have, **long)[0](), WORK, "workspace", lib)
     for have, ws in ((bwd - 1, A), (bwd, None), (bwd, A + 128)):
         refused(window_calls(lib, p, ws=ws, n=have, **long)[1](), WORK, "workspace", lib)
+    # an output that starts where an input does
+    good = {x: view(A + i * (1 << 24), 300 * 64 * (4 if x in ("d_o", "q", "o", "dq") else 2), 300 * 64, 64)
+            for i, x in enumerate(("d_o", "q", "k", "v", "o", "dq", "dk", "dv"))}
+    for name in ("q", "k", "v"):
+        same = svga.View(good[name].data, good["o"].stride_batch, good["o"].stride_head, 64)
+        fwd = window_calls(lib, problem(), **{**good, "o": same})[0]
+        refused(fwd(), ARG, "o starts where", lib)
+    for name in ("dq", "dk", "dv"):
+        for other in ("d_o", "q", "k", "v", "o"):
+            same = svga.View(good[other].data, good[name].stride_batch, good[name].stride_head, 64)
+            refused(window_calls(lib, problem(), **{**good, name: same})[1](), ARG, f"{name} starts where {other}", lib)
     # nothing to do: accepted without a launch, pointers not looked at
     empty = problem(batch=0)
     for call in window_calls(lib, empty, ws=None, n=0, lse=None):
