@@ -115,6 +115,12 @@ __device__ __forceinline__ void set_pair(float *x, float a, float b)
     *reinterpret_cast<float2 *>(x) = make_float2(a, b);
 }
 
+// The lanes of one row's pieces: `units` of them from lane `first` on.
+__device__ __forceinline__ uint32_t row_lanes(int units, int first)
+{
+    return units >= 32 ? 0xffffffffu : ((1u << units) - 1u) << first;
+}
+
 // Turns the first np of the piece's NP pairs: within a (interleaved), or between a and c.
 template <typename T, int LAY, int V, int NP>
 __device__ __forceinline__ void turn_piece(T (&a)[V], T (&c)[V], const float (&cs)[NP],
@@ -127,10 +133,6 @@ __device__ __forceinline__ void turn_piece(T (&a)[V], T (&c)[V], const float (&c
                 const float2 x = pair_of(a + 2 * j);
                 set_pair(a + 2 * j, x.x * cs[j] - x.y * sn[j], x.y * cs[j] + x.x * sn[j]);
             }
-    } else if constexpr (V == 1) {
-        const float x0 = to_f(a[0]), x1 = to_f(c[0]);
-        from_f(a[0], x0 * cs[0] - x1 * sn[0]);
-        from_f(c[0], x1 * cs[0] + x0 * sn[0]);
     } else {  // whole vectors only: the halves layout has no partial piece
 #pragma unroll
         for (int j = 0; j < NP; j += 2) {
@@ -145,7 +147,7 @@ template <typename T, int LAY, int DST, typename Ord>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
                                                           const __grid_constant__ Ord ord)
 {
-    constexpr int V = LAY == LAY_HALVES_ODD ? 1 : Vec<T>::N;  // values of a piece
+    constexpr int V = Vec<T>::N;  // values of a piece
     const long long idx = blockIdx.x * (long long)kThreads + threadIdx.x;
     // 32-bit divisions where the piece index fits (64-bit ones cost a tenth of the kernel)
     const bool small = (long long)p.batch * p.tokens * p.units <= 0x7fffffffll;
@@ -197,9 +199,9 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
 
     // the piece: values lo .. lo + V - 1 and, with halves, hi .. hi + V - 1
     int lo, hi = -1, pair0 = -1;  // pair0 < 0: copied unchanged
-    if (LAY == LAY_INTERLEAVED) {
+    if (LAY != LAY_HALVES) {
         lo = unit * V;
-        if (turn && lo / 2 < p.P) pair0 = lo / 2;
+        if (turn && lo < 2 * p.P) pair0 = LAY == LAY_INTERLEAVED ? lo / 2 : lo;
     } else {
         const int n = p.P / V;  // pieces of the turned half
         if (unit < n) {
@@ -236,10 +238,9 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
     // Heads go by one at a time, kDepth of them in flight: each thread copies its own pieces
     // of the coming heads into its own slots of shared memory (cp.async) and waits for
     // nothing but its own copies.
-    constexpr int kVecs = LAY == LAY_INTERLEAVED ? 1 : 2;
+    constexpr int kVecs = LAY == LAY_HALVES ? 2 : 1;
     constexpr int kDepth = kSlots / kVecs;
-    constexpr bool kAsync = LAY != LAY_HALVES_ODD;
-    __shared__ uint4 slots[kAsync ? kSlots : 1][kThreads];
+    __shared__ uint4 slots[kSlots][kThreads];
     const int h0 = blockIdx.y * p.heads_per_thread;
     const int h1 = min(h0 + p.heads_per_thread, p.heads);
     auto pick = [&](const long long (&at)[3], int h) {
@@ -251,46 +252,59 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
         }
     };
     auto fetch = [&](int h) {
-        if constexpr (kAsync) {
-            if (h < h1) {
-                const T *from = src + h * sv.sh + pick(src_at, h);
-                const int at = (h - h0) % kDepth * kVecs;
-                cp_async_16(smem_u32(&slots[at][threadIdx.x]), from + lo, 16);
-                if (kVecs == 2 && hi >= 0)
-                    cp_async_16(smem_u32(&slots[at + 1][threadIdx.x]), from + hi, 16);
-            }
-            cp_async_commit();  // (an empty group where no head is left keeps the count)
+        if (h < h1) {
+            const T *from = src + h * sv.sh + pick(src_at, h);
+            const int at = (h - h0) % kDepth * kVecs;
+            cp_async_16(smem_u32(&slots[at][threadIdx.x]), from + lo, 16);
+            if (kVecs == 2 && hi >= 0)
+                cp_async_16(smem_u32(&slots[at + 1][threadIdx.x]), from + hi, 16);
         }
+        cp_async_commit();  // (an empty group where no head is left keeps the count)
     };
     for (int u = 0; u < kDepth; ++u) fetch(h0 + u);
 
-    constexpr int NP = LAY == LAY_INTERLEAVED ? (V + 1) / 2 : V;  // pairs of a piece
-    const int np = pair0 < 0 ? 0 : min(NP, p.P - pair0);          // of them turned
+    // np of the piece's NP angles turn something; with odd halves one angle a value, and the
+    // value it goes with (its sine taken negative in the first half) is another piece's
+    constexpr int NP = LAY == LAY_INTERLEAVED ? V / 2 : V;
+    const int last = LAY == LAY_HALVES_ODD ? 2 * p.P : p.P;
+    const int np = pair0 < 0 ? 0 : min(NP, last - pair0);
     float cs[NP], sn[NP];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-        const float2 a = j < np ? pair_cs(p, pair0 + j, f, row, col) : make_float2(1.f, 0.f);
+        float2 a = make_float2(1.f, 0.f);
+        if (j < np) {
+            const int i = pair0 + j;
+            const bool second = LAY == LAY_HALVES_ODD && i >= p.P;
+            a = pair_cs(p, second ? i - p.P : i, f, row, col);
+            if (LAY == LAY_HALVES_ODD && !second) a.y = -a.y;
+        }
         cs[j] = a.x;
         sn[j] = p.inverse ? -a.y : a.y;
     }
+    // the lanes that hold the row's other pieces (all of one row take the same branches)
+    const uint32_t mine = row_lanes(p.units, (threadIdx.x & 31) - unit);
     for (int h = h0; h < h1; ++h) {
         Piece a, c;
-        if constexpr (kAsync) {
-            cp_async_wait<kDepth - 1>();
-            const int at = (h - h0) % kDepth * kVecs;
-            a = *reinterpret_cast<const Piece *>(&slots[at][threadIdx.x]);
-            if (kVecs == 2) c = *reinterpret_cast<const Piece *>(&slots[at + 1][threadIdx.x]);
-            fetch(h + kDepth);
-        } else {
-            const T *from = src + h * sv.sh + pick(src_at, h);
-            a = *reinterpret_cast<const Piece *>(from + lo);
-            if (hi >= 0) c = *reinterpret_cast<const Piece *>(from + hi);
-        }
-        if (np == NP) {
+        cp_async_wait<kDepth - 1>();
+        const int at = (h - h0) % kDepth * kVecs;
+        a = *reinterpret_cast<const Piece *>(&slots[at][threadIdx.x]);
+        if constexpr (kVecs == 2) c = *reinterpret_cast<const Piece *>(&slots[at + 1][threadIdx.x]);
+        if constexpr (LAY == LAY_HALVES_ODD) {
+            __syncwarp(mine);  // the others' copies have landed too
+            const T *whole = reinterpret_cast<const T *>(&slots[at][threadIdx.x - unit]);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j < np) {
+                    const int i = lo + j, other = i < p.P ? i + p.P : i - p.P;
+                    from_f(a.x[j], to_f(a.x[j]) * cs[j] + to_f(whole[other]) * sn[j]);
+                }
+            __syncwarp(mine);  // and were read: the slot takes a later head
+        } else if (np == NP) {
             turn_piece<T, LAY, V, NP>(a.x, c.x, cs, sn, NP);
         } else if (np > 0) {  // the piece the turned values end in: the rest stays as it is
             turn_piece<T, LAY, V, NP>(a.x, c.x, cs, sn, np);
         }
+        fetch(h + kDepth);
         T *to = dst + h * dst_sh + pick(dst_at, h);
         *reinterpret_cast<Piece *>(to + lo) = a;
         if (kVecs == 2 && hi >= 0) *reinterpret_cast<Piece *>(to + hi) = c;
@@ -332,8 +346,8 @@ View to_view(const svga_view &v)
 template <typename T, int LAY, int DST, typename Ord>
 svga_status launch(RotParams &p, const Ord &ord, cudaStream_t st)
 {
-    constexpr int V = LAY == LAY_HALVES_ODD ? 1 : Vec<T>::N;
-    p.units = LAY == LAY_INTERLEAVED ? p.d / V : p.P / V + (p.d - 2 * p.P) / V;
+    constexpr int V = Vec<T>::N;
+    p.units = LAY == LAY_HALVES ? p.P / V + (p.d - 2 * p.P) / V : p.d / V;
     const long long pieces = (long long)p.batch * p.tokens * p.units;
     const long long blocks = (pieces + kThreads - 1) / kThreads;
     if (blocks == 0 || p.heads == 0) return SVGA_OK;
@@ -354,7 +368,8 @@ template <typename T, int DST, typename Ord>
 svga_status launch_layout(RotParams &p, bool interleaved, const Ord &ord, cudaStream_t st)
 {
     if (interleaved) return launch<T, LAY_INTERLEAVED, DST>(p, ord, st);
-    // halves: pieces of 16 bytes need P and the rest behind 2P to be whole pieces
+    // halves: with P no multiple of a piece the two values of a pair sit at different places of
+    // theirs, and pieces are turned through shared memory
     if (p.P % Vec<T>::N == 0) return launch<T, LAY_HALVES, DST>(p, ord, st);
     return launch<T, LAY_HALVES_ODD, DST>(p, ord, st);
 }

@@ -656,19 +656,19 @@ bool pair_heads(const svga_window_problem *p)
 // Which items are split, from the shapes alone.  An item's list is as long as the shapes allow;
 // the GPU runs kSms items at a time.
 //   * less than one round of items: all split, to fill it once;
-//   * one to two rounds of lists of about one length (mean at least 0.65 of the longest): those
-//     behind the first round are split to fill the second (12,480 tokens of 4 heads, 196
-//     items: 110 us against 128 unsplit; all split in two 137, the partial sums cost more);
-//   * from two rounds on nothing (512 items of 11 chunks: 87 us against 94 with the last 68
-//     split), nor where a causal list without a window makes lengths run from 1 to the
-//     longest: those are launched longest first and pack by themselves.
+//   * more, of lists of about one length (mean at least 0.65 of the longest): those behind the
+//     last whole round are split to fill one more, where that shortens it by at least 8 chunks
+//     (12,480 tokens of 4 heads, 196 items of 30 chunks: 110 us against 128 unsplit, all split in
+//     two 137, the partial sums cost more; 512 items of 11 chunks: 94 against 87, so not there);
+//   * nothing from eight rounds on, nor where a causal list without a window makes lengths run
+//     from 1 to the longest: those are launched longest first and pack by themselves.
 // A part keeps at least kMinChunksPerSplit chunks.
 Split choose_split(const svga_window_problem *p)
 {
     const long long pairs = (p->q_tokens + 2 * kBlockM - 1) / (2 * kBlockM);
     const long long n = (long long)p->batch * (pair_heads(p) ? p->q_heads / 2 : p->q_heads) * pairs;
     Split s = {(int)n, (int)n, 1, 1};
-    if (n == 0 || n >= 2 * kSms || n == kSms || p->k_tokens == 0) return s;
+    if (n == 0 || n >= 8 * kSms || n % kSms == 0 || p->k_tokens == 0) return s;
     const Mask m = to_mask(p->mask);
     const int off = p->k_tokens - p->q_tokens;
     long long longest = 0, sum = 0;
@@ -683,8 +683,11 @@ Split choose_split(const svga_window_problem *p)
     if (n < kSms) {
         s.k1 = (int)std::min<long long>(kSms / n, most);
     } else if (20 * sum >= 13 * longest * pairs) {
-        s.n1 = kSms;
-        s.k2 = (int)std::min<long long>(kSms / (n - kSms), most);
+        const int tail = (int)(n % kSms), k = (int)std::min<long long>(kSms / tail, most);
+        if (longest - longest / k >= 8) {
+            s.n1 = (int)n - tail;
+            s.k2 = k;
+        }
     }
     return s;
 }

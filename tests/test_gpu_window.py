@@ -157,11 +157,11 @@ def test_split_key_lists(B, H, G, nq, nk):
     assert e.value.status == 5
 
 
-@pytest.mark.parametrize("mask,dtype,split", [(M(window=700, sinks=100), BF, True), (M(), FP, False)],
+@pytest.mark.parametrize("mask,dtype,split", [(M(window=1800, sinks=100), BF, True), (M(window=700, sinks=100), BF, False), (M(), FP, False)],
                          ids=str)
 def test_launches_split_in_part(mask, dtype, split):
-    """160 items for 148 SMs: the last ones split where lists are of one length, none under a
-    causal mask without a window.  Three heads are compared."""
+    """160 items for 148 SMs: the last ones split where lists are of one length and long, none where
+    they are short or under a causal mask without a window.  Three heads are compared."""
     q = values(1, 10, 4000, 64, dtype=dtype)
     k, v = (values(1, 5, 4000, 64, dtype=dtype, seed=s) for s in (1, 2))
     assert (svga.svga_window_attention_size(q, k, mask)["fwd_bytes"] > 0) == split
