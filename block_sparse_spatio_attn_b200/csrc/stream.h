@@ -90,10 +90,10 @@ struct ChunkList {
     }
 };
 
+// From the ranges of the run's first and last query.
 template <int KN>
-__host__ __device__ __forceinline__ ChunkList chunk_list(const Mask &m, int p0, int p1, int nk)
+__host__ __device__ __forceinline__ ChunkList chunk_list(const MaskRange &r0, const MaskRange &r1)
 {
-    const MaskRange r0 = mask_range(m, p0, nk), r1 = mask_range(m, p1, nk);
     ChunkList c;
     c.a = (r1.sk + KN - 1) / KN;
     c.w0 = r0.lo / KN;
@@ -103,6 +103,20 @@ __host__ __device__ __forceinline__ ChunkList chunk_list(const Mask &m, int p0, 
     c.f1 = r0.hi / KN;
     return c;
 }
+
+template <int KN>
+__host__ __device__ __forceinline__ ChunkList chunk_list(const Mask &m, int p0, int p1, int nk)
+{
+    return chunk_list<KN>(mask_range(m, p0, nk), mask_range(m, p1, nk));
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ MaskRange range_of_lane(const MaskRange &r, int lane)
+{
+    return {__shfl_sync(0xffffffffu, r.lo, lane), __shfl_sync(0xffffffffu, r.hi, lane),
+            __shfl_sync(0xffffffffu, r.sk, lane)};
+}
+#endif
 
 // --------------------------------------------------------------------------- splitting
 // Work items in launch order, the first n1 of them split k1 ways and the others k2 ways over
@@ -117,14 +131,11 @@ struct Split {
     }
     __device__ __forceinline__ void of_block(int blk, int &item, int &part) const
     {
-        if (blk < n1 * k1) {
-            item = blk / k1;
-            part = blk - item * k1;
-        } else {
-            const int r = blk - n1 * k1;
-            item = n1 + r / k2;
-            part = r % k2;
-        }
+        const bool head = blk < n1 * k1;
+        const int r = head ? blk : blk - n1 * k1, k = head ? k1 : k2;
+        const int q = k == 1 ? r : r / k;
+        item = head ? q : n1 + q;
+        part = r - q * k;
     }
     __host__ __device__ __forceinline__ long long slot(int item, int part) const
     {
@@ -154,8 +165,9 @@ struct WindowShape {
     int32_t *status;
 };
 
-// tensor_map.cu: 4-D map (d, token, head, batch) of a strided view of 16-bit elements, box
-// 64 columns x box_rows tokens, 128-byte swizzle.  A broadcast (stride 0) or one-entry
+// tensor_map.cu: map (64 columns, token, d / 64, head, batch) of a strided view of 16-bit
+// elements, 128-byte swizzle: one copy brings box_rows tokens whole, their first 64 columns
+// together and then their second.  A broadcast (stride 0) or one-entry
 // dimension is mapped with extent 1: coordinates in it are multiplied by *mul_h / *mul_b
 // (0 or 1).  False: the driver refused it.
 bool make_view_map(void *map, const svga_view &v, int batch, int heads, int tokens, int d,

@@ -43,14 +43,14 @@ bool make_view_map(void *map, const svga_view &v, int batch, int heads, int toke
     // a dimension of one entry never uses its stride: any valid one will do
     const cuuint64_t row = (cuuint64_t)d * 2;
     const bool tok = tokens > 1 && v.stride_token != 0;
-    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)tokens,
+    const cuuint64_t dims[5] = {64, (cuuint64_t)tokens, (cuuint64_t)(d / 64),
                                 (cuuint64_t)(*mul_h ? heads : 1), (cuuint64_t)(*mul_b ? batch : 1)};
-    const cuuint64_t strides[3] = {tok ? (cuuint64_t)v.stride_token * 2 : row,
+    const cuuint64_t strides[4] = {tok ? (cuuint64_t)v.stride_token * 2 : row, 128,
                                    *mul_h ? (cuuint64_t)v.stride_head * 2 : row,
                                    *mul_b ? (cuuint64_t)v.stride_batch * 2 : row};
-    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(static_cast<CUtensorMap *>(map), map_type(dt), 4, v.data, dims, strides, box, estr,
+    const cuuint32_t box[5] = {64, (cuuint32_t)box_rows, (cuuint32_t)(d / 64), 1, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(static_cast<CUtensorMap *>(map), map_type(dt), 5, v.data, dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

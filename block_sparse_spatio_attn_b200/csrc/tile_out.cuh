@@ -73,13 +73,19 @@ __device__ __forceinline__ void copy_rows_out(uint32_t tile, uint32_t half_step,
 {
     constexpr int kRows = 32 / UNITS;  // rows an instruction stores
     const int u = lane % UNITS, r = lane / UNITS;
+    constexpr int kAtOnce = 32 / kRows < 8 ? 32 / kRows : 8;  // loads before the first store
     __syncwarp();  // the rows are in shared memory
-#pragma unroll 4
-    for (int i = 0; i < 32; i += kRows) {
-        if (i + r < valid) {
-            uint4 x;
-            ld_shared_v4(unit_addr(tile, half_step, row0 + i + r, u0 + u), x.x, x.y, x.z, x.w);
-            *reinterpret_cast<uint4 *>(dst + (i + r) * step + 16 * u) = x;
+#pragma unroll 1
+    for (int i = 0; i < 32; i += kRows * kAtOnce) {
+        uint4 x[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            ld_shared_v4(unit_addr(tile, half_step, row0 + i + k * kRows + r, u0 + u), x[k].x,
+                         x[k].y, x[k].z, x[k].w);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int row = i + k * kRows + r;
+            if (row < valid) *reinterpret_cast<uint4 *>(dst + row * step + 16 * u) = x[k];
         }
     }
     __syncwarp();  // and may be overwritten

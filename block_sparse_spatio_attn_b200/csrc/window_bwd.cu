@@ -238,7 +238,7 @@ __device__ __forceinline__ bool smem_misplaced(const void *base, int32_t *status
 }
 
 // ----------------------------------------------------------------------------- dkdv
-// One CTA's work, worked out by warp 0 for all.
+// One CTA's work, worked out by warp 0, its lanes together, for all.
 struct KvItem {
     int b, hk, nq, nk, off;
     int k0, k1;                // keys
@@ -266,23 +266,31 @@ __device__ __forceinline__ bool make_item(const BwdParams &p, int block, KvItem 
     const int nq = it.nq, off = it.off = it.nk - nq;
     const int k0 = it.k0 = kblk * kT, k1 = it.k1 = min(k0 + kT, it.nk);
     if (k0 >= it.nk) return false;
-    int first, end, first1, end1, x;
-    mask_rows(p.s.mask, k0, nq, off, first, end);  // a sink among the keys is the first one
-    mask_rows(p.s.mask, k1 - 1, nq, off, first1, end1);
+    // the rows that keep the first key (a sink, if one is among them), the last, and the first
+    // that is no sink: a lane each
+    const int e = threadIdx.x & 3;
+    const int key = e == 0 ? k0 : (e == 1 ? k1 - 1 : max(k0, min(p.s.mask.sinks, k1 - 1)));
+    int first, end;
+    mask_rows(p.s.mask, key, nq, off, first, end);
+    const int first0 = __shfl_sync(0xffffffffu, first, 0), end0 = __shfl_sync(0xffffffffu, end, 0);
+    const int first1 = __shfl_sync(0xffffffffu, first, 1), end1 = __shfl_sync(0xffffffffu, end, 1);
+    const int end2 = __shfl_sync(0xffffffffu, end, 2);
     // rows that keep all: each key's are contiguous, and a sink's run to the end
-    it.all_first = max(first, first1);
-    it.all_end = nq;
-    if (p.s.mask.window < 0)
-        it.all_end = end;
-    else if (p.s.mask.sinks < k1)
-        mask_rows(p.s.mask, max(k0, p.s.mask.sinks), nq, off, x, it.all_end);
-    end = max(end, end1);
+    it.all_first = max(first0, first1);
+    it.all_end = p.s.mask.window < 0 ? end0 : (p.s.mask.sinks < k1 ? end2 : nq);
+    first = first0;
+    end = max(end0, end1);
     it.qb0 = first / kT;
     it.n_blk = end > first ? (end + kT - 1) / kT - it.qb0 : 0;
     const long long all = (long long)it.n_blk * p.s.group;
-    const int first_step = (int)(part * all / it.ksplit);
-    it.steps = (int)((part + 1) * all / it.ksplit) - first_step;
-    it.g0 = it.n_blk > 0 ? first_step / it.n_blk : 0;
+    int first_step = 0;
+    it.steps = (int)all;
+    it.g0 = 0;
+    if (it.ksplit > 1) {
+        first_step = (int)(part * all / it.ksplit);
+        it.steps = (int)((part + 1) * all / it.ksplit) - first_step;
+        it.g0 = it.n_blk > 0 ? first_step / it.n_blk : 0;
+    }
     it.blk0 = first_step - it.g0 * it.n_blk;
     it.ragged =
         (p.s.q_lens && nq < p.s.tq && nq % kT && nq / kT == it.qb0 + it.n_blk - 1) ? it.n_blk - 1
@@ -361,12 +369,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
             if (some && mine.steps > 0) {  // on their way before the CTA meets
                 const uint32_t kvf = smem_u32(&bar->kv_full);
                 mbar_arrive_expect_tx(kvf, 2 * C::kTile);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem_u32(sK + c * C::kChunk), &tmK, kvf, 64 * c, mine.k0,
-                                mine.hk * p.k_mh, mine.b * p.k_mb);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem_u32(sV + c * C::kChunk), &tmV, kvf, 64 * c, mine.k0,
-                                mine.hk * p.v_mh, mine.b * p.v_mb);
+                tma_load_5d(smem_u32(sK), &tmK, kvf, 0, mine.k0, 0, mine.hk * p.k_mh, mine.b * p.k_mb);
+                tma_load_5d(smem_u32(sV), &tmV, kvf, 0, mine.k0, 0, mine.hk * p.v_mh, mine.b * p.v_mb);
             }
         }
     }
@@ -397,17 +401,13 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                     break;
                 uint32_t fb = smem_u32(&bar->q_full[qs]);
                 mbar_arrive_expect_tx(fb, C::kTile);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem_u32(sQ + qs * C::kTile + c * C::kChunk), &tmQ, fb, 64 * c, row,
-                                h * p.q_mh, b * p.q_mb);
+                tma_load_5d(smem_u32(sQ + qs * C::kTile), &tmQ, fb, 0, row, 0, h * p.q_mh, b * p.q_mb);
                 q_issued = i + 1;
                 if (orr > 0 && !mbar_wait(smem_u32(&bar->o_empty[os]), (orr - 1) & 1, abort_flag))
                     break;
                 fb = smem_u32(&bar->o_full[os]);
                 mbar_arrive_expect_tx(fb, C::kTile);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem_u32(sO + os * C::kTile + c * C::kChunk), &tmO, fb, 64 * c, row,
-                                h * p.o_mh, b * p.o_mb);
+                tma_load_5d(smem_u32(sO + os * C::kTile), &tmO, fb, 0, row, 0, h * p.o_mh, b * p.o_mb);
                 o_issued = i + 1;
                 if (orr > 0 && !mbar_wait(smem_u32(&bar->st_empty[os]), (orr - 1) & 1, abort_flag))
                     break;
@@ -740,7 +740,10 @@ __device__ __forceinline__ bool make_item(const BwdParams &p, int block, DqItem 
     it.nk = clamped_len(p.s.k_lens, it.b, p.s.tk);
     const int off = it.nk - it.nq, r0 = it.blk * kT;
     if (r0 >= it.nq) return false;
-    it.list = chunk_list<kT>(p.s.mask, r0 + off, min(r0 + kT, it.nq) - 1 + off, it.nk);
+    // first and last query, a lane each
+    const MaskRange mr = mask_range(
+        p.s.mask, (threadIdx.x & 1 ? min(r0 + kT, it.nq) - 1 : r0) + off, it.nk);
+    it.list = chunk_list<kT>(range_of_lane(mr, 0), range_of_lane(mr, 1));
     it.skip = max(it.list.a, it.list.w0);
     it.E = it.list.a + max(it.list.w1 - it.skip, 0);
     return true;
@@ -815,12 +818,8 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
             if (some && mine.E > 0) {  // on their way before the CTA meets
                 const uint32_t qf = smem_u32(&bar->q_full);
                 mbar_arrive_expect_tx(qf, 2 * C::kTile);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem_u32(sQ + c * C::kChunk), &tmQ, qf, 64 * c, mine.blk * kT,
-                                mine.h * p.q_mh, mine.b * p.q_mb);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem_u32(sO + c * C::kChunk), &tmO, qf, 64 * c, mine.blk * kT,
-                                mine.h * p.o_mh, mine.b * p.o_mb);
+                tma_load_5d(smem_u32(sQ), &tmQ, qf, 0, mine.blk * kT, 0, mine.h * p.q_mh, mine.b * p.q_mb);
+                tma_load_5d(smem_u32(sO), &tmO, qf, 0, mine.blk * kT, 0, mine.h * p.o_mh, mine.b * p.o_mb);
             }
         }
     }
@@ -855,17 +854,13 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
                         break;
                     uint32_t fb = smem_u32(&bar->k_full[ks]);
                     mbar_arrive_expect_tx(fb, C::kTile);
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_4d(smem_u32(sK + ks * C::kTile + c * C::kChunk), &tmK, fb, 64 * c,
-                                    row, hk * p.k_mh, b * p.k_mb);
+                    tma_load_5d(smem_u32(sK + ks * C::kTile), &tmK, fb, 0, row, 0, hk * p.k_mh, b * p.k_mb);
                     k_issued = i + 1;
                     if (vr > 0 && !mbar_wait(smem_u32(&bar->v_empty[vs]), (vr - 1) & 1, abort_flag))
                         break;
                     fb = smem_u32(&bar->v_full[vs]);
                     mbar_arrive_expect_tx(fb, C::kTile);
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_4d(smem_u32(sV + vs * C::kTile + c * C::kChunk), &tmV, fb, 64 * c,
-                                    row, hk * p.v_mh, b * p.v_mb);
+                    tma_load_5d(smem_u32(sV + vs * C::kTile), &tmV, fb, 0, row, 0, hk * p.v_mh, b * p.v_mb);
                     v_issued = i + 1;
                 }
             }

@@ -157,6 +157,7 @@ __device__ __forceinline__ void place_item(const FwdParams &p, int i, int &b, in
     b0 = 2 * (p.n_pairs - 1 - pair);
 }
 
+// By a whole warp.
 __device__ __forceinline__ bool make_item(const FwdParams &p, Item &it)
 {
     int item, part;
@@ -168,16 +169,24 @@ __device__ __forceinline__ bool make_item(const FwdParams &p, Item &it)
     it.nk = clamped_len(p.s.k_lens, it.b, p.s.tk);
     const int off = it.nk - it.nq, r0 = it.b0 * kBlockM;
     if (r0 >= it.nq) return false;
-    it.l0 = it.l1 = chunk_list<kKN>(p.s.mask, r0 + off, min(r0 + kBlockM, it.nq) - 1 + off, it.nk);
     it.valid1 = p.by_heads || r0 + kBlockM < it.nq;
-    if (!p.by_heads && it.valid1)
-        it.l1 = chunk_list<kKN>(p.s.mask, r0 + kBlockM + off,
-                                min(r0 + 2 * kBlockM, it.nq) - 1 + off, it.nk);
+    // first and last query of the two blocks, a lane each
+    const int lane = threadIdx.x & 31, e = lane & 3;
+    const int row = e == 0 ? r0 : min(r0 + (e == 1 ? kBlockM : e == 2 ? kBlockM + 1 : 2 * kBlockM),
+                                      it.nq) - 1;
+    const MaskRange mr = mask_range(p.s.mask, row + off, it.nk);
+    it.l0 = it.l1 = chunk_list<kKN>(range_of_lane(mr, 0), range_of_lane(mr, 1));
+    const ChunkList l1 = chunk_list<kKN>(range_of_lane(mr, 2), range_of_lane(mr, 3));
+    if (!p.by_heads && it.valid1) it.l1 = l1;
     int end;
     merge_lists(it.l0, it.l1, it.valid1, it.a, it.skip, end);
-    const long long all = it.a + end - it.skip;
-    it.e0 = (int)(part * all / it.ksplit);
-    it.E = (int)((part + 1) * all / it.ksplit) - it.e0;
+    const int all = it.a + end - it.skip;  // below 2^18; times a part's number below 2^31
+    it.e0 = 0;
+    it.E = all;
+    if (it.ksplit > 1) {
+        it.e0 = part * all / it.ksplit;
+        it.E = (part + 1) * all / it.ksplit - it.e0;
+    }
     return true;
 }
 
@@ -246,9 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hk = it.h / p.s.group;
         const uint32_t fb = smem_u32(&bar->kv_full[s]);
         mbar_arrive_expect_tx(fb, C::kKVBytes);
-        for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(smem_u32(sKV + s * C::kKVBytes + c * C::kKVChunk), t ? &tmV : &tmK, fb,
-                        64 * c, row, hk * (t ? p.v_mh : p.k_mh), it.b * (t ? p.v_mb : p.k_mb));
+        tma_load_5d(smem_u32(sKV + s * C::kKVBytes), t ? &tmV : &tmK, fb, 0, row, 0,
+                    hk * (t ? p.v_mh : p.k_mh), it.b * (t ? p.v_mb : p.k_mb));
     };
     // The first loads are on their way before the CTA meets: the producer is the thread that
     // set the barriers up.
@@ -258,10 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nq_tiles = it.valid1 ? 2 : 1;
         mbar_arrive_expect_tx(qf, nq_tiles * C::kQBytes);
         for (int i = 0; i < nq_tiles; ++i) {
-            for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(smem_u32(sQ + i * C::kQBytes + c * C::kQChunk), &tmQ, qf, 64 * c,
-                            (it.b0 + (p.by_heads ? 0 : i)) * kBlockM,
-                            (it.h + (p.by_heads ? i : 0)) * p.q_mh, it.b * p.q_mb);
+            tma_load_5d(smem_u32(sQ + i * C::kQBytes), &tmQ, qf, 0,
+                        (it.b0 + (p.by_heads ? 0 : i)) * kBlockM, 0,
+                        (it.h + (p.by_heads ? i : 0)) * p.q_mh, it.b * p.q_mb);
             if (i == 0) fetch(fetched++);  // K of the first entry behind the first Q tile
         }
         while (fetched < min(C::kStages, 2 * it.E)) fetch(fetched++);
@@ -509,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             s1 = fadd2(s1, ev);
                         else
                             s0 = fadd2(s0, ev);
-                        pk[c2] = F16 ? pack_f16x2(ev.x, ev.y) : pack_bf16x2_int(ev.x, ev.y);
+                        pk[c2] = pack_16x2<F16>(ev.x, ev.y);
                     }
                     tmem_st16(tP + j * 16, pk);
                 }
