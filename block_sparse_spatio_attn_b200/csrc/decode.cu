@@ -8,7 +8,7 @@
 //     the FP32 pipe does not limit shared heads.  tcgen05 has nothing to add here: its
 //     smallest tile has 64 query rows and the operand bytes, not the products, set the time.
 //   * A cluster of CTAs splits the keys of one (sequence, key head): CTA r takes the r-th
-//     run of 32-key chunks of the mask's chunk list (sinks, then window; chunks in between
+//     run of 64-key chunks of the mask's chunk list (sinks, then window; chunks in between
 //     are never read).  The CTAs join over distributed shared memory, so the call is one
 //     launch with no workspace, and two calls can never share scratch.
 //   * Warp 4 looks up pages and streams K and V with TMA through kStages stages of 64 keys: a

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
         pos = p.positions ? (long long)__ldg(p.positions + tok_all) : p.first + t;
     }
     int f = 0, s = 0, row = 0, col = 0;
-    if (turn || DST == DST_ORDERED) {
+    if (p.turn || DST == DST_ORDERED) {  // (a value goes where its key does, or neither)
         if (pos < 0 || pos >= (long long)p.F * p.S) {
             if (unit == 0) set_status(p.status);
             return;

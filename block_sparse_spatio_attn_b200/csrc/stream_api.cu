@@ -388,9 +388,9 @@ svga_status svga_window_attention_bwd(const svga_view *d_o, const svga_view *q, 
     if (B == 0 || (p->q_tokens == 0 && p->k_tokens == 0)) return SVGA_OK;
     for (const auto &x : views)
         for (const auto &y : views)
-            if (x.write && !y.write && x.tokens > 0 && y.tokens > 0 && x.v->data == y.v->data) {
-                set_error("%s starts where %s does: it is written while that is read", x.name,
-                          y.name);
+            if (&x != &y && x.write && x.tokens > 0 && y.tokens > 0 && x.v->data == y.v->data) {
+                set_error("%s starts where %s does: it is written while that is read or written",
+                          x.name, y.name);
                 return SVGA_ERR_INVALID_ARG;
             }
     return launch_window_bwd(*d_o, *q, *k, *v, *o, lse, *dq, *dk, *dv, p, scale, workspace, stream);
@@ -445,6 +445,9 @@ svga_status svga_cache_decode(const svga_view *q, const svga_view *o, float *lse
         return rc;
     if (lse && !aligned(lse, 4)) return bad(SVGA_ERR_ALIGNMENT, "%slse is not 4-byte aligned");
     if (c->batch == 0) return SVGA_OK;
+    if (o->data == q->data || (c->pages > 0 && (o->data == c->k_pages || o->data == c->v_pages)))
+        return bad(SVGA_ERR_INVALID_ARG, "%so starts where q or the cache does: it is written while "
+                                         "they are read");
     return launch_decode(*q, *o, lse, q_heads, c, mask, scale, stream);
 }
 

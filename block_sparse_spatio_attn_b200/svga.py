@@ -549,6 +549,13 @@ def _binding():
     return _native
 
 
+def _int32(name: str, *values: int) -> None:
+    """ctypes cuts an int down to 32 bits without a word; what does not fit is refused here."""
+    for x in values:
+        if not -2**31 <= x < 2**31:
+            raise SvgaError(2, f"{name}: {x} does not fit 32 bits")
+
+
 @dataclass(frozen=True)
 class RotarySpec:
     """Rotary positions on the three axes of a grid (svga_rotary_spec): frames x grid_h x
@@ -565,6 +572,8 @@ class RotarySpec:
     def __post_init__(self):
         if len(self.pairs) != 3:
             raise SvgaError(2, f"pairs names {len(self.pairs)} axes, not 3")
+        _int32("RotarySpec", self.num_frames, self.grid_h, self.grid_w, *self.pairs,
+               *(self.order or ()))
         od = None if self.order is None else (ctypes.c_int32 * len(self.order))(*self.order)
         c = RotarySpecC(self.num_frames, self.grid_h, self.grid_w, (ctypes.c_int * 3)(*self.pairs),
                         int(self.interleaved), od)
@@ -613,6 +622,7 @@ class WindowMask:
     block: int = 1
 
     def __post_init__(self):
+        _int32("WindowMask", self.window, self.sinks, self.block)
         object.__setattr__(self, "c", WindowMaskC(int(self.causal), self.window, self.sinks,
                                                   self.block))
 
@@ -622,7 +632,8 @@ def svga_window_attention_size(q, k, mask: WindowMask) -> dict:
     if q.dim() != 4 or k.dim() != 4:
         raise SvgaError(2, "q and k must be tensors of 4 dimensions")
     (B, H, Tq, d), (_, G, Tk, _) = q.shape, k.shape
-    c = WindowProblemC(B, H, G, Tq, Tk, d, 1 if q.dtype == torch.float16 else 0, mask.c)
+    c = WindowProblemC(B, H, G, Tq, Tk, d,
+                       {torch.bfloat16: 0, torch.float16: 1}.get(q.dtype, 2), mask.c)
     n = [ctypes.c_size_t() for _ in range(2)]
     _check(load().svga_window_attention_size(ctypes.byref(c), ctypes.byref(n[0]),
                                              ctypes.byref(n[1])))

@@ -536,7 +536,7 @@ typedef struct {
  *                    changes nothing.
  * A non-finite value in a row a sequence does own (of k or v; of q or d_o in the backward
  * call) can reach the whole 128 x 128 tiles that visit the row, also the pairs whose mask
- * drops it.  Written tensors must not overlap read ones (the same start is refused). */
+ * drops it.  Written tensors must not overlap others (the same start is refused). */
 typedef struct {
     int batch;
     int q_heads;
@@ -590,8 +590,10 @@ SVGA_API svga_status svga_window_attention_bwd(const svga_view *d_o, const svga_
  *                not read
  *   lens       : DEVICE int32 [batch], each sequence's length (0 .. max_pages * page_size)
  *   status     : SVGA_ERR_INVALID_ARG when a length, or a page a length needs, is out of
- *                range: svga_cache_append leaves such a row unwritten, svga_cache_decode
- *                treats a length out of range as 0 and a page's keys as masked. */
+ *                range (svga_cache_append with a spec: or a position, of the grid):
+ *                svga_cache_append leaves such a row of both pages unwritten,
+ *                svga_cache_decode treats a length out of range as 0 and a page's keys as
+ *                masked. */
 typedef struct {
     void *k_pages;
     void *v_pages;
@@ -623,8 +625,8 @@ SVGA_API svga_status svga_cache_append(const svga_view *k, const svga_view *v, i
  * svga_window_attention_fwd gives for its last query (position lens[b] - 1; the mask's
  * causal flag changes nothing there).  q, o: [batch, q_heads, head_dim] of the cache's
  * type, q_heads a multiple of kv_heads; strides of batch and head as in svga_view
- * (stride_token is not read).  lse: fp32 contiguous [batch, q_heads] or NULL.  An empty
- * sequence gives O = 0 and lse = -inf.  Rows of a page past the length are read but change
+ * (stride_token is not read); o must not overlap q or the cache.  lse: fp32 contiguous
+ * [batch, q_heads] or NULL.  An empty sequence gives O = 0 and lse = -inf.  Rows of a page past the length are read but change
  * nothing, NaN included.  One launch, no workspace: the CTAs of a cluster split the keys
  * and join over distributed shared memory, in a fixed order. */
 SVGA_API svga_status svga_cache_decode(const svga_view *q, const svga_view *o, float *lse,

@@ -212,6 +212,18 @@ def test_append_reports_and_skips_bad_rows():
     assert c.status.item() == 1 and int((~c.k.isnan()).sum()) == 2 * 64
 
 
+def test_append_leaves_both_rows_of_a_position_outside_the_grid():
+    spec = svga.RotarySpec(1, 4, 4, (1, 1, 1))  # 16 positions
+    table = svga.svga_rotary_table(spec, 1e4, torch.empty(spec.table_shape, device="cuda"))
+    c = Cache([18], 1, 16, 64, BF)
+    k, v = c.randn(1, 1, 4, 64).cuda(), c.randn(1, 1, 4, 64).cuda()
+    svga.svga_cache_append(k, v, *c.args(), None, spec, table, status=c.status)
+    assert c.status.item() == 1
+    written = c.rows(c.v, 0).isnan().logical_not().all(-1)[0].tolist()
+    assert written == [False] * 14 + [True] * 2 + [False] * 2
+    assert c.rows(c.k, 0).isnan().logical_not().all(-1)[0].tolist() == written
+
+
 def test_a_stream_of_steps_as_a_generator_runs_them():
     """Prompt, then token by token: rotate q, append rotated k, attend with a window and
     sinks, captured once and replayed with the lengths moved on the device."""

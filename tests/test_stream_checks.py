@@ -276,3 +276,31 @@ def test_window_binding_checks():
     rejected(lambda: bwd(q, q, k, k, q, lse, q, k, k[:, :1], m, 0.1), 2, "dv has shape")
     rejected(lambda: bwd(q, q, k, k, q, lse, k, k, k, m, 0.1), 2, "dq has shape")
     rejected(lambda: bwd(q, q, k, k, q, lse, q, k, k, m, 0.1), 1, "CUDA device")
+
+
+def test_outputs_that_start_together_are_refused(lib):
+    good = {x: view(A + i * (1 << 24), 300 * 64 * (4 if x in ("d_o", "q", "o", "dq") else 2), 300 * 64, 64)
+            for i, x in enumerate(("d_o", "q", "k", "v", "o", "dq", "dk", "dv"))}
+    for name, other in (("dq", "dk"), ("dk", "dv"), ("dq", "dv")):
+        both = {**good, other: svga.View(good[name].data, good[other].stride_batch, good[other].stride_head, 64)}
+        refused(window_calls(lib, problem(), **both)[1](), ARG, f"{name} starts where {other}", lib)
+    c, m = cache(k_pages=Z, v_pages=2 * Z), svga.WindowMask()
+    for o in (A, Z, 2 * Z):
+        refused(lib.svga_cache_decode(ctypes.byref(view(A)), ctypes.byref(view(o)), None, 4, ctypes.byref(c),
+                                      ctypes.byref(m.c), 0.1, None), ARG, "o starts where", lib)
+
+
+def test_numbers_that_32_bits_cannot_hold_are_refused():
+    # ctypes would make 2^32 a window of 0
+    for kw in (dict(window=2**32), dict(sinks=2**31), dict(block=2**32 + 1), dict(window=-2**31 - 1)):
+        rejected(lambda: svga.WindowMask(**kw), 2, "does not fit 32 bits")
+    rejected(lambda: svga.RotarySpec(2**32 + 1, 2, 5, (1, 1, 1)), 2, "does not fit 32 bits")
+    rejected(lambda: svga.RotarySpec(1, 2, 5, (1, 2**33, 1)), 2, "does not fit 32 bits")
+    rejected(lambda: svga.RotarySpec(1, 2, 5, (1, 1, 1), order=[0, 2**32]), 2, "does not fit 32 bits")
+
+
+def test_workspace_size_names_its_types():
+    q, k = torch.zeros(1, 4, 10, 64), torch.zeros(1, 2, 10, 64)
+    rejected(lambda: svga.svga_window_attention_size(q, k, svga.WindowMask()), 4, "dtype")
+    n = svga.svga_window_attention_size(q.half(), k.half(), svga.WindowMask())
+    assert n["bwd_bytes"] > 0
