@@ -119,6 +119,26 @@ __device__ __forceinline__ MaskRange range_of_lane(const MaskRange &r, int lane)
 #endif
 
 // --------------------------------------------------------------------------- splitting
+// Division by a number the host knows: n / d = n ceil(2^shift / d) >> shift for 0 <= n < 2^31,
+// with shift = 31 + ceil(log2 d) (the error n (2^shift mod d) / (d 2^shift) stays below 1 / d).
+// A CTA's place among the items takes five divisions in a row before its first load, a hundred
+// cycles or two each when the hardware's reciprocal has to do them.
+struct FastDiv {
+    uint32_t mul;
+    int shift;
+    __host__ __device__ __forceinline__ int of(int n) const
+    {
+        return (int)(((unsigned long long)(uint32_t)n * mul) >> shift);
+    }
+};
+
+inline FastDiv fast_div(int d)
+{
+    int s = 0;
+    while ((1ll << s) < d) ++s;
+    return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 // Work items in launch order, the first n1 of them split k1 ways and the others k2 ways over
 // as many CTAs.  Parts of a split item leave partial sums in the workspace, in slots
 // numbered over the split items' parts in launch order.
@@ -129,13 +149,14 @@ struct Split {
     {
         return (long long)n1 * k1 + (long long)(items - n1) * k2;
     }
-    __device__ __forceinline__ void of_block(int blk, int &item, int &part) const
+    // (by1, by2: division by k1 and k2)
+    __device__ __forceinline__ void of_block(int blk, const FastDiv &by1, const FastDiv &by2,
+                                             int &item, int &part) const
     {
         const bool head = blk < n1 * k1;
-        const int r = head ? blk : blk - n1 * k1, k = head ? k1 : k2;
-        const int q = k == 1 ? r : r / k;
+        const int r = head ? blk : blk - n1 * k1, q = head ? by1.of(r) : by2.of(r);
         item = head ? q : n1 + q;
-        part = r - q * k;
+        part = r - q * (head ? k1 : k2);
     }
     __host__ __device__ __forceinline__ long long slot(int item, int part) const
     {

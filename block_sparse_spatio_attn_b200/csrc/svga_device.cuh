@@ -551,6 +551,24 @@ __device__ __forceinline__ float fmax3(float a, float b, float c)
     return d;
 }
 
+// True in one thread of the warp.  Roles that issue TMA copies and MMAs are entered by it (or by
+// `threadIdx.x == constant`): these take their operands from the warp's uniform registers, and
+// behind a test such as `lane == 0`, which the compiler does not know to leave one thread, each
+// is wrapped in a loop over the threads there are (the backward kernel: 57 us against 48 for
+// 2 x 2,001 tokens; a CTA's first copies 3,000 cycles later).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        ".reg .pred P;\n"
+        "elect.sync _|P, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, P;\n"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Programmatic dependent launch.  pdl_start lets the next kernel of the stream be launched once
 // every CTA of this one has called it; pdl_wait, which that kernel calls, returns when this one
 // has completed and its writes can be read (at once, if it was launched the ordinary way).

@@ -74,6 +74,8 @@ struct BwdParams {
     int n_qblk, n_kblk;
     int n_dkdv;    // CTAs of dkdv
     Split split;   // over dkdv's items, key blocks ascending
+    // the split's parts, (sequence, key head) and (sequence, query head) pairs, heads, the group
+    FastDiv by_k1, by_k2, by_bk, by_hk, by_bq, by_hq, by_group;
     float *parts;  // [slot][dV, dK][128][d]
     int q_mb, q_mh, o_mb, o_mh, k_mb, k_mh, v_mb, v_mh;  // coordinate multipliers (o: dO)
 };
@@ -254,12 +256,12 @@ struct KvItem {
 __device__ __forceinline__ bool make_item(const BwdParams &p, int block, KvItem &it)
 {
     int item, part;
-    p.split.of_block(block, item, part);
+    p.split.of_block(block, p.by_k1, p.by_k2, item, part);
     it.ksplit = p.split.k(item);
     it.slot = it.ksplit > 1 ? p.split.slot(item, part) : 0;
     const int bh = p.s.batch * p.s.hk;
-    const int kblk = item / bh, r = item - kblk * bh;
-    it.b = r / p.s.hk;
+    const int kblk = p.by_bk.of(item), r = item - kblk * bh;
+    it.b = p.by_hk.of(r);
     it.hk = r - it.b * p.s.hk;
     it.nq = clamped_len(p.s.q_lens, it.b, p.s.tq);
     it.nk = clamped_len(p.s.k_lens, it.b, p.s.tk);
@@ -361,9 +363,10 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
         tmem_relinquish();
     }
     if (warp == 0) {
+        __syncwarp();  // (or the item is worked out for lane 0 and for the others, one after the other)
         KvItem mine;
         const bool some = make_item(p, block, mine);  // false: past the sequence's keys
-        if (lane == 0) {
+        if (threadIdx.x == 0) {
             bar->item = mine;
             bar->some = some;
             if (some && mine.steps > 0) {  // on their way before the CTA meets
@@ -390,7 +393,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsLow>();
-        if (warp == 0 && lane == 0 && steps > 0) {
+        if (threadIdx.x == 0 && steps > 0) {
             // -------------------------------------------------------- TMA producer
             int q_issued = 0, o_issued = 0, st_issued = 0, g = it.g0, blk = it.blk0;
             for (int i = 0; i < steps; ++i) {
@@ -430,7 +433,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                 mbar_wait_bounded(smem_u32(&bar->o_full[i % C::kOStages]), (i / C::kOStages) & 1);
             for (int i = max(st_issued - C::kOStages, 0); i < st_issued; ++i)
                 mbar_wait_bounded(smem_u32(&bar->st_full[i % C::kOStages]), (i / C::kOStages) & 1);
-        } else if ((warp == 1 || warp == 3) && lane == 0 && steps > 0) {
+        } else if ((warp == 1 || warp == 3) && steps > 0 && elect_one()) {
             // --------------------------------------------------------- MMA issuers
             // warp 1: S^T and dV, warp 3: dP^T and dK.  Each accumulator and tile belongs to
             // one of them, so its products stay in order.
@@ -692,8 +695,8 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const BwdParams p)
     if (it >= p.split.split_to()) return;
     const int item = (int)it, k = p.split.k(item);
     const int bh = p.s.batch * p.s.hk;
-    const int kblk = item / bh, r = item - kblk * bh;
-    const int b = r / p.s.hk, hk = r - b * p.s.hk, key = kblk * kT + row;
+    const int kblk = p.by_bk.of(item), r = item - kblk * bh;
+    const int b = p.by_hk.of(r), hk = r - b * p.s.hk, key = kblk * kT + row;
     if (key >= clamped_len(p.s.k_lens, b, p.s.tk)) return;
     const float *src = p.parts + ((p.split.slot(item, 0) * 2 + w) * kT + row) * D + c;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -731,10 +734,10 @@ __device__ __forceinline__ bool make_item(const BwdParams &p, int block, DqItem 
 {
     // last blocks first: the longest under a causal mask
     const int bh = p.s.batch * p.s.hq;
-    const int slot = block / bh, r = block - slot * bh;
-    it.b = r / p.s.hq;
+    const int slot = p.by_bq.of(block), r = block - slot * bh;
+    it.b = p.by_hq.of(r);
     it.h = r - it.b * p.s.hq;
-    it.hk = it.h / p.s.group;
+    it.hk = p.by_group.of(it.h);
     it.blk = p.n_qblk - 1 - slot;
     it.nq = clamped_len(p.s.q_lens, it.b, p.s.tq);
     it.nk = clamped_len(p.s.k_lens, it.b, p.s.tk);
@@ -810,9 +813,10 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
         tmem_relinquish();
     }
     if (warp == 0) {
+        __syncwarp();
         DqItem mine;
         const bool some = make_item(p, block, mine);  // false: past the sequence's queries
-        if (lane == 0) {
+        if (threadIdx.x == 0) {
             bar->item = mine;
             bar->some = some;
             if (some && mine.E > 0) {  // on their way before the CTA meets
@@ -846,7 +850,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
         if (warp == 0 && E > 0) {
             // -------------------------------------------------------- TMA producer
             int k_issued = 0, v_issued = 0;
-            if (lane == 0) {
+            if (threadIdx.x == 0) {
                 for (int i = 0; i < E; ++i) {
                     const int row = chunk_of(i) * kT, ks = i % C::kKStages, vs = i % C::kVStages;
                     const int kr = i / C::kKStages, vr = i / C::kVStages;
@@ -887,7 +891,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
                     mbar_wait_bounded(smem_u32(&bar->v_full[i % C::kVStages]),
                                       (i / C::kVStages) & 1);
             }
-        } else if (warp >= 1 && lane == 0 && E > 0) {
+        } else if (warp >= 1 && E > 0 && elect_one()) {
             // --------------------------------------------------------- MMA issuers
             // warp 1: S, warp 2: dQ, warp 3: dP
             constexpr uint32_t idS = idesc_16_f32(F16, kT, kT, 0, 0);
@@ -1257,6 +1261,13 @@ svga_status launch_window_bwd(const svga_view &d_o, const svga_view &q, const sv
     kp.n_qblk = (p->q_tokens + kT - 1) / kT;
     kp.n_kblk = (p->k_tokens + kT - 1) / kT;
     kp.split = choose_bwd_split(p);
+    kp.by_k1 = fast_div(kp.split.k1);
+    kp.by_k2 = fast_div(kp.split.k2);
+    kp.by_bk = fast_div(p->batch * p->kv_heads);
+    kp.by_hk = fast_div(p->kv_heads);
+    kp.by_bq = fast_div(p->batch * p->q_heads);
+    kp.by_hq = fast_div(p->q_heads);
+    kp.by_group = fast_div(p->q_heads / p->kv_heads);
     kp.parts = kp.stats + stats_bytes(p) / sizeof(float);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (p->head_dim == 128)

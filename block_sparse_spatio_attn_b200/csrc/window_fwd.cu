@@ -45,14 +45,8 @@ constexpr uint32_t kNegInfBits = 0xff800000u;
 // kRegsHigh (checked against the launch's on the host)
 constexpr int kRegsLaunch = 168, kRegsLow = 120, kRegsHigh = 192;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "register split");
-// TMEM columns: S at 0, then a P tile (64 columns) and an O per group
-// (head_dim 128: one S tile for both, head_dim 64: one each)
-template <int D>
-struct Tm {
-    static constexpr bool kTwoS = D == 64;
-    static constexpr uint32_t kS1 = kTwoS ? 128 : 0, kP = kTwoS ? 256 : 128, kO = kP + 128;
-    static constexpr uint32_t kOStep = kTwoS ? 64 : 128;
-};
+// TMEM columns: S of whichever group's turn it is, then a P tile (packed pairs) and an O a group
+constexpr uint32_t kTmS = 0, kTmP = 128, kTmO = 256;
 constexpr int kMinChunksPerSplit = 4;
 constexpr int kSms = 148;
 
@@ -64,6 +58,7 @@ struct FwdParams {
     int n_pairs;    // items per (sequence, head or pair of heads)
     int by_heads;   // 1: an item's two blocks are block 0 of two heads
     Split split;    // over items, last query blocks first
+    FastDiv by_k1, by_k2, by_bh, by_h;  // the split's parts, (sequence, head) pairs, heads
     int q_mb, q_mh, k_mb, k_mh, v_mb, v_mh;  // coordinate multipliers (0: broadcast)
     float *part_o;    // [slot][256][d], unnormalised
     float2 *part_ml;  // [slot][256] (reference maximum, sum)
@@ -111,9 +106,7 @@ struct Barriers {
     uint64_t q_full;
     uint64_t kv_full[8], kv_empty[8];
     uint64_t s_full[2];    // [group]: that group's S is in the S columns
-    uint64_t s_free[2];    // S columns were read into registers (4 warps); [group] with an S
-                           // tile each, [0] when they share one
-    uint64_t s_issued[8];  // [visit % 8]: the S issuer has issued the S of that visit
+    uint64_t s_free;       // the S columns were read into registers (4 warps)
     uint64_t p_full[2];    // [group]: P of the group's tile is in its P columns (4 warps)
     uint64_t o_done[2];    // [group]: the group's last P V product is done
     uint64_t drain[2];     // abort: [issuer]: the MMAs that issuer started are done
@@ -151,25 +144,31 @@ __device__ __forceinline__ int clamped_len(const int32_t *lens, int b, int most)
 __device__ __forceinline__ void place_item(const FwdParams &p, int i, int &b, int &h, int &b0)
 {
     const int heads = p.by_heads ? p.s.hq / 2 : p.s.hq, bh = p.s.batch * heads;
-    const int pair = i / bh, r = i - pair * bh;
-    b = r / heads;
+    const int pair = p.by_bh.of(i), r = i - pair * bh;
+    b = p.by_h.of(r);
     h = (r - b * heads) << p.by_heads;
     b0 = 2 * (p.n_pairs - 1 - pair);
 }
 
-// By a whole warp.
-__device__ __forceinline__ bool make_item(const FwdParams &p, Item &it)
+// In two steps, by a whole warp: where the item's queries are (false: past the sequence's end),
+// which is all their load needs, and which keys they visit.
+__device__ __forceinline__ bool make_item(const FwdParams &p, Item &it, int &part)
 {
-    int item, part;
-    p.split.of_block(blockIdx.x, item, part);
+    int item;
+    p.split.of_block(blockIdx.x, p.by_k1, p.by_k2, item, part);
     place_item(p, item, it.b, it.h, it.b0);
     it.ksplit = p.split.k(item);
     it.slot = it.ksplit > 1 ? p.split.slot(item, part) : 0;
     it.nq = clamped_len(p.s.q_lens, it.b, p.s.tq);
     it.nk = clamped_len(p.s.k_lens, it.b, p.s.tk);
-    const int off = it.nk - it.nq, r0 = it.b0 * kBlockM;
-    if (r0 >= it.nq) return false;
+    const int r0 = it.b0 * kBlockM;
     it.valid1 = p.by_heads || r0 + kBlockM < it.nq;
+    return r0 < it.nq;
+}
+
+__device__ __forceinline__ void make_lists(const FwdParams &p, Item &it, int part)
+{
+    const int off = it.nk - it.nq, r0 = it.b0 * kBlockM;
     // first and last query of the two blocks, a lane each
     const int lane = threadIdx.x & 31, e = lane & 3;
     const int row = e == 0 ? r0 : min(r0 + (e == 1 ? kBlockM : e == 2 ? kBlockM + 1 : 2 * kBlockM),
@@ -187,7 +186,6 @@ __device__ __forceinline__ bool make_item(const FwdParams &p, Item &it)
         it.e0 = part * all / it.ksplit;
         it.E = (part + 1) * all / it.ksplit - it.e0;
     }
-    return true;
 }
 
 // bits [0, n) of a 32-bit word
@@ -203,7 +201,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tmV, const FwdParams p)
 {
     using C = Cfg<D>;
-    using T = Tm<D>;
     constexpr float kSumLimit = F16 ? 32768.f : 65536.f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -214,23 +211,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        prefetch_tmap(&tmQ);
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-        mbar_init(smem_u32(&bar->q_full), 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(smem_u32(&bar->kv_full[s]), 1);
-            mbar_init(smem_u32(&bar->kv_empty[s]), 1);
-        }
+    // warp 0 sets up what the first loads need, works out the item and starts them; warp 2 sets
+    // up the rest
+    if (threadIdx.x == 64) {
+        for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&bar->kv_empty[s]), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bar->s_full[i]), 1);
-            mbar_init(smem_u32(&bar->s_free[i]), 4);
             mbar_init(smem_u32(&bar->p_full[i]), 4);
             mbar_init(smem_u32(&bar->o_done[i]), 1);
             mbar_init(smem_u32(&bar->drain[i]), 1);
         }
-        for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&bar->s_issued[i]), 1);
+        mbar_init(smem_u32(&bar->s_free), 4);
         mbar_init(smem_u32(&bar->zero_req), 1);
         mbar_init(smem_u32(&bar->zero_done), 1);
         bar->abort = 0;
@@ -241,14 +232,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     Item it;
-    bool some = false;
-    if (warp == 0) {
-        some = make_item(p, it);  // false: past the sequence's queries
-        if (lane == 0) {
-            bar->item = it;
-            bar->some = some;
-        }
-    }
     // K (idx even) or V of entry idx / 2 into its stage
     auto fetch = [&](int idx) {
         const int s = idx % C::kStages, t = idx & 1, row = it.chunk(idx >> 1) * kKN;
@@ -258,20 +241,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_5d(smem_u32(sKV + s * C::kKVBytes), t ? &tmV : &tmK, fb, 0, row, 0,
                     hk * (t ? p.v_mh : p.k_mh), it.b * (t ? p.v_mb : p.k_mb));
     };
-    // The first loads are on their way before the CTA meets: the producer is the thread that
-    // set the barriers up.
+    // Q and the first K and V are on their way before the CTA meets, Q before the list of keys
+    // is known: the first S of a CTA waited 5,600 cycles when they were loaded behind both.
     int fetched = 0;
-    if (some && threadIdx.x == 0 && it.E > 0) {
+    if (warp == 0) {
         const uint32_t qf = smem_u32(&bar->q_full);
-        const int nq_tiles = it.valid1 ? 2 : 1;
-        mbar_arrive_expect_tx(qf, nq_tiles * C::kQBytes);
-        for (int i = 0; i < nq_tiles; ++i) {
-            tma_load_5d(smem_u32(sQ + i * C::kQBytes), &tmQ, qf, 0,
-                        (it.b0 + (p.by_heads ? 0 : i)) * kBlockM, 0,
-                        (it.h + (p.by_heads ? i : 0)) * p.q_mh, it.b * p.q_mb);
-            if (i == 0) fetch(fetched++);  // K of the first entry behind the first Q tile
+        if (lane == 0) {
+            prefetch_tmap(&tmQ);
+            prefetch_tmap(&tmK);
+            prefetch_tmap(&tmV);
+            mbar_init(qf, 1);
+            for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&bar->kv_full[s]), 1);
+            fence_barrier_init();
         }
-        while (fetched < min(C::kStages, 2 * it.E)) fetch(fetched++);
+        __syncwarp();  // (or what follows is run for lane 0 and for the others one after the other)
+        int part;
+        const bool some = make_item(p, it, part);
+        if (lane == 0) bar->some = some;
+        if (some) {
+            if (threadIdx.x == 0) {
+                const int nq_tiles = it.valid1 ? 2 : 1;
+                mbar_arrive_expect_tx(qf, nq_tiles * C::kQBytes);
+                for (int i = 0; i < nq_tiles; ++i)
+                    tma_load_5d(smem_u32(sQ + i * C::kQBytes), &tmQ, qf, 0,
+                                (it.b0 + (p.by_heads ? 0 : i)) * kBlockM, 0,
+                                (it.h + (p.by_heads ? i : 0)) * p.q_mh, it.b * p.q_mb);
+            }
+            __syncwarp();
+            make_lists(p, it, part);
+            if (lane == 0) {
+                if (it.E > 0)
+                    while (fetched < 2) fetch(fetched++);
+                bar->item = it;
+            }
+        }
     }
     pdl_start();  // the join, if there is one
     tc_fence_before();
@@ -285,16 +288,96 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsLow>();
-        it = bar->item;
+        if (warp != 0) it = bar->item;
         // the chunk whose last rows lie past the sequence's end but inside the tensor
         const int ragged = (p.s.k_lens && it.nk < p.s.tk && it.nk % kKN) ? it.nk / kKN : -1;
-        if (warp == 0 && lane == 0 && it.E > 0) {
+        // Two threads issue the products: warp 1's S = Q K^T, warp 3's O += P V.  Each waits on its
+        // own barriers only, its loads before the softmax threads; the hazards between them go
+        // through the softmax groups' barriers.  Both walk the visits: (entry n, group g), entries
+        // ascending, group 0 before group 1.
+        auto landed = [&](int idx) {
+            return mbar_wait(smem_u32(&bar->kv_full[idx % C::kStages]), (idx / C::kStages) & 1,
+                             abort_flag);
+        };
+        auto release = [&](int idx) {
+            if (idx + C::kStages < 2 * it.E) mma_commit(smem_u32(&bar->kv_empty[idx % C::kStages]));
+        };
+        auto stage_at = [&](int idx) {
+            return (smem_u32(sKV) >> 4) + (idx % C::kStages) * (C::kKVBytes >> 4);
+        };
+        auto give_up = [&](int i) {  // every MMA the thread issued ends before TMEM is freed
+            mma_commit(smem_u32(&bar->drain[i]));
+            mbar_wait_bounded(smem_u32(&bar->drain[i]), 0);
+        };
+        auto issue_s = [&]() {
+            constexpr uint32_t id = idesc_16_f32(F16, kBlockM, kKN, 0, 0);
+            const uint64_t desc = smem_desc_sw128(0, 16, 1024);
+            bool ok = it.E == 0 || mbar_wait(smem_u32(&bar->q_full), 0, abort_flag);
+            int k = 0;  // visits done
+            for (int n = 0; ok && n < it.E; ++n) {
+                const uint32_t f = it.flags(it.chunk(n));
+                ok = landed(2 * n);
+#pragma unroll 1
+                for (int g = (f & kV0) ? 0 : 1; ok && g < 2; ++g) {
+                    if (g == 1 && !(f & kV1)) break;
+                    // once the owner of the previous visit has read its S
+                    if (k > 0 && !(ok = mbar_wait(smem_u32(&bar->s_free), (k - 1) & 1, abort_flag)))
+                        break;
+                    tc_fence_after();
+                    const uint64_t a0 = desc + ((smem_u32(sQ) + g * C::kQBytes) >> 4);
+                    const uint64_t b0 = desc + stage_at(2 * n);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ss(tmem + kTmS,
+                               a0 + (uint32_t)(((kk >> 2) * C::kQChunk + (kk & 3) * 32) >> 4),
+                               b0 + (uint32_t)(((kk >> 2) * C::kKVChunk + (kk & 3) * 32) >> 4), id,
+                               kk > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&bar->s_full[g]));
+                    if (g == 1 || !(f & kV1)) release(2 * n);
+                    ++k;
+                }
+            }
+            if (!ok) give_up(0);
+        };
+        auto issue_pv = [&]() {
+            constexpr uint32_t id = idesc_16_f32(F16, kBlockM, D, 0, 1);
+            const uint64_t desc = smem_desc_sw128(0, C::kKVChunk, 1024);
+            bool ok = true;
+            int done[2] = {0, 0};
+            for (int n = 0; ok && n < it.E; ++n) {
+                const int chunk = it.chunk(n);
+                const uint32_t f = it.flags(chunk);
+                ok = landed(2 * n + 1);
+                if (ok && chunk == ragged) {  // warp 2 clears the rows past the end
+                    mbar_arrive(smem_u32(&bar->zero_req));
+                    ok = mbar_wait(smem_u32(&bar->zero_done), 0, abort_flag);
+                }
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (!ok || !(f & (g ? kV1 : kV0))) continue;
+                    ok = mbar_wait(smem_u32(&bar->p_full[g]), done[g] & 1, abort_flag);
+                    tc_fence_after();
+                    if (!ok) break;
+                    const uint64_t b0 = desc + stage_at(2 * n + 1);
+#pragma unroll
+                    for (int kk = 0; kk < kKN / 16; ++kk)
+                        mma_ts(tmem + kTmO + g * 128, tmem + kTmP + g * 64 + kk * 8,
+                               b0 + (uint32_t)(kk * (2048 >> 4)), id,
+                               (done[g] != 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(smem_u32(&bar->o_done[g]));
+                    if (g == 1 || !(f & kV1)) release(2 * n + 1);
+                    ++done[g];
+                }
+            }
+            if (!ok) give_up(1);
+        };
+        if (threadIdx.x == 0) {
             // -------------------------------------------------------- TMA producer
             const uint32_t qf = smem_u32(&bar->q_full);
             int issued = fetched;
             for (; issued < 2 * it.E; ++issued) {
                 const int s = issued % C::kStages, round = issued / C::kStages;
-                if (!mbar_wait(smem_u32(&bar->kv_empty[s]), (round - 1) & 1, abort_flag)) break;
+                if (round > 0 && !mbar_wait(smem_u32(&bar->kv_empty[s]), (round - 1) & 1, abort_flag)) break;
                 fetch(issued);
             }
             // every copy lands before the CTA can exit, whichever role aborts
@@ -302,116 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int idx = max(issued - C::kStages, 0); idx < issued; ++idx)
                 mbar_wait_bounded(smem_u32(&bar->kv_full[idx % C::kStages]),
                                   (idx / C::kStages) & 1);
-        } else if ((warp == 1 || warp == 3) && lane == 0) {
-            // ------------------------------------------------------- MMA issuers
-            // warp 1: S = Q K^T, warp 3: O += P V; each waits on its own barriers only, the
-            // hazards between them go through the softmax groups' barriers (attention.cu)
-            const bool s_role = warp == 1;
-            constexpr uint32_t idS = idesc_16_f32(F16, kBlockM, kKN, 0, 0);
-            constexpr uint32_t idO = idesc_16_f32(F16, kBlockM, D, 0, 1);
-            const uint64_t dK = smem_desc_sw128(0, 16, 1024);
-            const uint64_t dV = smem_desc_sw128(0, C::kKVChunk, 1024);
-            const uint32_t q_addr = smem_u32(sQ) >> 4, kv_addr = smem_u32(sKV) >> 4;
-            const int total = 2 * it.E;
-            bool ok = it.E == 0 || !s_role || mbar_wait(smem_u32(&bar->q_full), 0, abort_flag);
-            auto wait_full = [&](int idx) {
-                return mbar_wait(smem_u32(&bar->kv_full[idx % C::kStages]),
-                                 (idx / C::kStages) & 1, abort_flag);
-            };
-            auto release = [&](int idx) {
-                if (idx + C::kStages < total)
-                    mma_commit(smem_u32(&bar->kv_empty[idx % C::kStages]));
-            };
-            // the visits: (entry n, group g), entries ascending, group 0 before group 1
-            // k: visits done, gn: of each group
-            int n = 0, k = 0, gn0 = 0, gn1 = 0;
-            auto run = [&](auto role_tag) {
-                constexpr bool kSRole = decltype(role_tag)::value;
-                for (; ok && n < it.E; ++n) {
-                    const int chunk = it.chunk(n);
-                    const uint32_t f = it.flags(chunk);
-                    bool waited = false;
-#pragma unroll 1
-                    for (int g = (f & kV0) ? 0 : 1; g < 2; ++g) {
-                        if (g == 1 && !(f & kV1)) break;
-                        const bool last = g == 1 || !(f & kV1);
-                        if constexpr (kSRole) {
-                            // once the owner of the previous visit has read its S
-                            const int before = T::kTwoS ? (g ? gn1 : gn0) : k;
-                            if (before > 0 &&
-                                !(ok = mbar_wait(smem_u32(&bar->s_free[T::kTwoS ? g : 0]),
-                                                 (before - 1) & 1, abort_flag)))
-                                break;
-                            tc_fence_after();
-                            if (!waited && !(ok = wait_full(2 * n))) break;
-                            waited = true;
-                            const uint64_t a0 = dK + (q_addr + g * (C::kQBytes >> 4));
-                            const uint64_t b0 =
-                                dK + (kv_addr + ((2 * n) % C::kStages) * (C::kKVBytes >> 4));
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                mma_ss(tmem + g * T::kS1,
-                                       a0 + (uint32_t)(((kk >> 2) * C::kQChunk + (kk & 3) * 32) >> 4),
-                                       b0 + (uint32_t)(((kk >> 2) * C::kKVChunk + (kk & 3) * 32) >> 4),
-                                       idS, kk > 0 ? 1u : 0u);
-                            mma_commit(smem_u32(&bar->s_full[g]));
-                            if (last) release(2 * n);
-                            mbar_arrive(smem_u32(&bar->s_issued[k & 7]));
-                            (g ? gn1 : gn0)++;
-                        } else {
-                            if (!waited) {
-                                if (!(ok = wait_full(2 * n + 1))) break;
-                                if (chunk == ragged) {  // warp 2 clears the rows past the end
-                                    mbar_arrive(smem_u32(&bar->zero_req));
-                                    if (!(ok = mbar_wait(smem_u32(&bar->zero_done), 0, abort_flag)))
-                                        break;
-                                }
-                                waited = true;
-                            }
-                            int &pvn = g ? gn1 : gn0;
-                            ok = mbar_wait(smem_u32(&bar->p_full[g]), pvn & 1, abort_flag);
-                            // Right behind the S two visits ahead, where it runs while that S
-                            // is being read.  The S of visit m completes phase m / 8 of
-                            // s_issued[m % 8].  While this P V (visit k) is not issued, a
-                            // group can have read the S of at most one visit past the one
-                            // whose P it wrote last, and with an S tile of its own have one
-                            // more issued: S runs to visit k + 4 at most (k + 2, k + 3 and
-                            // k + 4 when the other group has the last two), and the two
-                            // arrivals behind the last S reach k + 6, below k + 2 + 8: a
-                            // parity wait is never a whole round behind.
-                            ok = ok && mbar_wait(smem_u32(&bar->s_issued[(k + 2) & 7]),
-                                                 ((k + 2) >> 3) & 1, abort_flag);
-                            tc_fence_after();
-                            if (!ok) break;
-                            const uint64_t b0 =
-                                dV + (kv_addr + ((2 * n + 1) % C::kStages) * (C::kKVBytes >> 4));
-#pragma unroll
-                            for (int kk = 0; kk < kKN / 16; ++kk)
-                                mma_ts(tmem + T::kO + g * T::kOStep, tmem + T::kP + g * 64 + kk * 8,
-                                       b0 + (uint32_t)(kk * (2048 >> 4)), idO,
-                                       (pvn != 0 || kk > 0) ? 1u : 0u);
-                            mma_commit(smem_u32(&bar->o_done[g]));
-                            if (last) release(2 * n + 1);
-                            ++pvn;
-                        }
-                        ++k;
-                    }
-                }
-            };
-            if (s_role)
-                run(std::true_type{});
-            else
-                run(std::false_type{});
-            if (ok && s_role) {  // the last two P V products wait for no later S
-                mbar_arrive(smem_u32(&bar->s_issued[k & 7]));
-                mbar_arrive(smem_u32(&bar->s_issued[(k + 1) & 7]));
-            }
-            if (!ok) {
-                // abort: wait for every MMA this thread issued before TMEM is freed
-                const uint32_t drain = smem_u32(&bar->drain[s_role ? 0 : 1]);
-                mma_commit(drain);
-                mbar_wait_bounded(drain, 0);
-            }
+        } else if (warp == 1) {
+            if (elect_one()) issue_s();
+        } else if (warp == 3) {
+            if (elect_one()) issue_pv();
         } else if (warp == 2 && ragged >= 0) {
             // --------------------------------- rows of V past the sequence's end read as 0
             int n = it.E - 1;  // the ragged chunk is a sequence's last: its entry, if any
@@ -435,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         setmaxnreg_inc<kRegsHigh>();
         const int wg = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-        const uint32_t tS = tmem + lane_base + wg * T::kS1;
-        const uint32_t tP = tmem + lane_base + T::kP + wg * 64;
-        const uint32_t tO = tmem + lane_base + T::kO + wg * T::kOStep;
+        const uint32_t tS = tmem + lane_base + kTmS;
+        const uint32_t tP = tmem + lane_base + kTmP + wg * 64;
+        const uint32_t tO = tmem + lane_base + kTmO + wg * 128;
         // what the loop needs of the item stays in registers, the rest in shared memory
         const Item &item = bar->item;
         const ChunkList list = wg ? item.l1 : item.l0;
@@ -466,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
             tc_fence_before();  // S is in registers: its columns may take another visit's
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar->s_free[T::kTwoS ? wg : 0]));
+            if (lane == 0) mbar_arrive(smem_u32(&bar->s_free));
             if (!list.full(chunk)) {
                 const int k0 = chunk * kKN;
 #pragma unroll
@@ -555,6 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_wait(smem_u32(&bar->o_done[wg]), (visit - 1) & 1, abort_flag));
             tc_fence_after();
         }
+        // a group without a visit waited for nothing yet: its Q tile, which the rows go out
+        // through, may still be on its way
+        if (ok && mine && visit == 0)
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->q_full), 0, abort_flag));
         const Item &it = item;
         const bool split = it.ksplit > 1;
         if (ok && (wg == 0 || it.valid1)) {
@@ -761,6 +742,11 @@ svga_status launch_window_fwd(const svga_view &q, const svga_view &k, const svga
     kp.n_pairs = (p->q_tokens + 2 * kBlockM - 1) / (2 * kBlockM);
     kp.by_heads = pair_heads(p);
     kp.split = choose_split(p);
+    const int heads = kp.by_heads ? p->q_heads / 2 : p->q_heads;
+    kp.by_k1 = fast_div(kp.split.k1);
+    kp.by_k2 = fast_div(kp.split.k2);
+    kp.by_bh = fast_div(p->batch * heads);
+    kp.by_h = fast_div(heads);
     kp.part_o = static_cast<float *>(ws);
     kp.part_ml = reinterpret_cast<float2 *>(kp.part_o + (size_t)kp.split.slots() * 2 * kBlockM *
                                                             p->head_dim);

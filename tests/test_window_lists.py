@@ -1,6 +1,6 @@
 """The window mask's arithmetic (csrc/stream.h) against brute force, compiled for the host: the
 keys of a query, the queries of a key, the chunks a run of queries visits and keeps whole, and
-the queries that keep a whole block of keys."""
+the queries that keep a whole block of keys; and the division by numbers known to the host."""
 import os
 import subprocess
 
@@ -59,6 +59,13 @@ int main()
     for (int p : {-(1 << 24), -1, 0, 1, (1 << 24) - 1}) {
         const MaskRange r = mask_range(wide, p, 1 << 24);
         bad += r.lo != 0 || r.hi != (p < 0 ? 0 : 1 << 24) || r.sk != r.hi;
+    }
+    for (int t = 0; t < 200000; ++t) {  // division by a known number, over the whole range
+        const int d = rand() % 3 ? rand() % 5000 + 1 : (int)((unsigned)rand() % 0x7fffffffu) + 1;
+        const FastDiv f = fast_div(d);
+        const long long k = rand() % (0x7fffffff / d + 1ll);
+        for (long long n : {0ll, 1ll, (long long)rand() & 0x7fffffff, k * d, k * d - 1, k * d + d - 1, 0x7fffffffll})
+            if (n >= 0 && n <= 0x7fffffff) bad += f.of((int)n) != n / d;
     }
     printf("%ld checks, %ld bad, %ld missed\n", checks, bad, missed);
     return bad != 0;
