@@ -15,6 +15,10 @@
 // Consecutive threads hold consecutive pieces, so rows move whole.  When there are few
 // tokens (a decoding step) the heads are dealt over blocks instead, so that the launch
 // still covers the GPU.
+//
+// Bound by HBM.  Measured: 75,600 tokens of 10 heads of 128 (bf16) into each head's order, 387 MB:
+// 69 us, 5.6 TB/s (86 % of the measured copy); append of 2 x 12,480 tokens of 10 heads, 256 MB:
+// 45 us, 5.7 TB/s; 64 single tokens of 16 heads: 4 us, the time of a launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -3,7 +3,8 @@
 // With P = exp(scale Q K^T - lse) on the kept pairs and D = rowsum(dO o O):
 //   dV = P^T dO,   dS = P o (dO V^T - D),   dQ = scale dS K,   dK = scale dS^T Q.
 //
-// Three kernels:
+// Three launches, each begun while the one before it ends (programmatic dependent launch): the
+// rows, one of dkdv's and dq's CTAs together, and a join where some of dkdv's items were split.
 //   rows    D and lse of every query row in the exp2 domain, negated, 1 KB per 128 rows;
 //   dkdv    one CTA per 128 keys of a key head; walks the query blocks that keep any of
 //           them, over all query heads of the group, with dK and dV in TMEM throughout, so
@@ -28,20 +29,24 @@
 // threads take some 200 cycles beside it; an issuing thread that waits before every product
 // leaves the tensor pipe idle between them (one issuer: 2,870 cycles a step of dq, 967 of
 // them in waits).  So
-//   * two threads issue, each the products of its own accumulators and tiles (dkdv: dV and S^T,
-//     dK and dP^T; dq: S, dQ and dP), and each waits for its loads before it waits for the
-//     softmax threads;
+//   * two threads issue in dkdv (dV and S^T; dK and dP^T) and three in dq (S; dQ; dP), each the
+//     products of its own accumulators and tiles, and each waits for its loads before it waits
+//     for the softmax threads;
 //   * dkdv: a step's S^T cannot be computed before the last P^T is used up, and no TMEM is
-//     left for a second tile.  The groups are therefore two chains of their own (barriers,
-//     products of 64 columns or 64 terms each): while one waits, the other has the
-//     exponential unit and the tensor pipe;
-//   * dq has three issuers and gives dS columns of its own (S | dP | dQ | dS | Q, the last two
+//     left for a second tile.  The groups are therefore two chains of their own (barriers, an
+//     S^T product of 64 columns each, dV and dK products of 64 terms each): while one waits,
+//     the other has the exponential unit and the tensor pipe.  dP^T, which the groups need later,
+//     is one product of 128 columns: two of 64 take half as long again (2,048 causal tokens of
+//     4 heads: 32.2 us against 33.2; S^T in one as well: 36);
+//   * dq gives dS columns of its own (S | dP | dQ | dS | Q, the last two
 //     64 columns of packed pairs each): S and dP are computed again as soon as they were
 //     read, so the softmax threads wait for no product (with dS over dP the chain dS -> dQ ->
 //     dP -> dS alone took 2,440 cycles a step).  Q as an operand in TMEM spares a quarter of
 //     the shared memory's reads;
 //   * shared memory holds, beside the resident tiles, three stages of the operand that is
 //     needed longest (dkdv: Q, dq: K) and two of the other.
+// Measured: 12,480 tokens, 4 heads of 128, frames of 960, window 2 and a sink frame: 250 us, 870
+// TFLOP/s of the five products of kept pairs; 2 x 2,001 tokens, 8 heads on 2, window of 512: 49 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -305,7 +310,7 @@ struct KvBars {
     uint64_t q_full[3], q_empty[3];      // stages of Q
     uint64_t o_full[2], o_empty[2];      // stages of dO
     uint64_t st_full[2], st_empty[2];    // of the statistics (needed longer than dO)
-    uint64_t s_full[2], dp_full[2];      // [group]: its columns of S^T / dP^T are in TMEM
+    uint64_t s_full[2], dp_full;         // [group]: its columns of S^T are in TMEM; dP^T is
     uint64_t p_ready[2], ds_ready[2];    // [group]: its P^T / dS^T is (4 warps)
     uint64_t acc_done;                   // every product is done (both issuers)
     uint64_t drain[2];
@@ -347,13 +352,13 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
             mbar_init(smem_u32(&bar->st_full[i]), 1);
             mbar_init(smem_u32(&bar->st_empty[i]), 1);
             mbar_init(smem_u32(&bar->s_full[i]), 1);
-            mbar_init(smem_u32(&bar->dp_full[i]), 1);
             mbar_init(smem_u32(&bar->p_ready[i]), 4);
             mbar_init(smem_u32(&bar->ds_ready[i]), 4);
             mbar_init(smem_u32(&bar->zero_req[i]), 1);
             mbar_init(smem_u32(&bar->zero_done[i]), 1);
             mbar_init(smem_u32(&bar->drain[i]), 1);
         }
+        mbar_init(smem_u32(&bar->dp_full), 1);
         mbar_init(smem_u32(&bar->acc_done), 2);
         bar->abort = 0;
         fence_barrier_init();
@@ -439,6 +444,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
             // one of them, so its products stay in order.
             const int role = warp == 3;
             constexpr uint32_t idS = idesc_16_f32(F16, kT, 64, 0, 0);
+            constexpr uint32_t idDP = idesc_16_f32(F16, kT, kT, 0, 0);
             constexpr uint32_t idA = idesc_16_f32(F16, kT, D, 0, 1);
             const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);         // rows of terms
             const uint64_t nmaj = smem_desc_sw128(0, C::kChunk, 1024);  // terms down the rows
@@ -489,15 +495,12 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                 }
             } else {
                 const uint64_t a = kmaj + (smem_u32(sV) >> 4);
-                auto issue = [&](int i, int g) {
-                    product_ss<D>(tmem + kDP, a, kmaj + o_at(i), g, idS);
-                    mma_commit(smem_u32(&bar->dp_full[g]));
-                    if (g == 1) mma_commit(smem_u32(&bar->o_empty[i % C::kOStages]));
+                auto issue = [&](int i) {
+                    product_ss<D>(tmem + kDP, a, kmaj + o_at(i), idDP);
+                    mma_commit(smem_u32(&bar->dp_full));
+                    mma_commit(smem_u32(&bar->o_empty[i % C::kOStages]));
                 };
-                if (ok) {
-                    issue(0, 0);
-                    issue(0, 1);
-                }
+                if (ok) issue(0);
                 for (int i = 0; ok && i < steps; ++i) {
                     const bool next = i + 1 < steps;
                     ok = landed(i, 0) && (!next || take(i + 1, 1, true));
@@ -511,8 +514,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                         if (g == 1) {  // the last to use the step's Q; the statistics were read
                             mma_commit(smem_u32(&bar->q_empty[i % C::kQStages]));
                             mma_commit(smem_u32(&bar->st_empty[i % C::kOStages]));
+                            if (next) issue(i + 1);
                         }
-                        if (next) issue(i + 1, g);
                     }
                 }
             }
@@ -609,7 +612,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
             if (lane == 0) mbar_arrive(smem_u32(&bar->p_ready[wg]));
 
             ok = __all_sync(0xffffffffu,
-                            mbar_wait(smem_u32(&bar->dp_full[wg]), i & 1, abort_flag));
+                            mbar_wait(smem_u32(&bar->dp_full), i & 1, abort_flag));
             tc_fence_after();
             if (!ok) break;
             tmem_ld64(tDP, x);

@@ -6,21 +6,33 @@
 // The design is the block-sparse kernel's (attention.cu: two 128-row query blocks a CTA,
 // TMA ring, two tcgen05.mma issuers, S | P0 | P1 | O0 | O1 in TMEM, one row per softmax
 // thread, the reference maximum of the first tile kept until a tile's sum would pass a
-// limit).  What differs:
+// limit).  The one S tile the two groups share keeps them half a visit apart, so that one has
+// the exponential unit while the other waits; with a tile each (head_dim 64 has the room, and
+// P over S would make it) they drift into step and both wait together: 115 us against 106 for
+// 148 items of 64 chunks at head_dim 64, 173 against 140 at 128.  What differs:
 //   * the visited key chunks need no map: the keys a run of queries keeps are [0, sk) and
 //     [lo, hi), all monotone in the position (stream.h), so every role computes its list;
 //   * rows are masked by those two intervals, two shifts a 32-key word;
-//   * tensors are strided and batched (4-D tensor maps), query heads share key heads, every
-//     sequence may have its own lengths; rows of V past a sequence's end are set to 0 in
-//     shared memory before they meet P (0 times a NaN left there is not 0);
+//   * tensors are strided and batched (5-D tensor maps, one copy a tile), query heads share key
+//     heads, every sequence may have its own lengths; rows of V past a sequence's end are set
+//     to 0 in shared memory before they meet P (0 times a NaN left there is not 0);
 //   * bf16 or fp16.  P reaches at most the tile-sum limit: 2^16 in bf16, 2^15 in fp16 (65504
 //     is its largest value); what underflows in fp16 (below 2^-24 of a sum >= 1) is lost
 //     below the rounding of O;
 //   * with few items for the GPU's SMs some or all key lists are split over CTAs that leave
-//     fp32 partial rows in the workspace, joined in a fixed order by a second kernel;
+//     fp32 partial rows in the workspace, joined in a fixed order by a second kernel, whose
+//     launch overlaps the first (programmatic dependent launch);
 //   * one query block's worth of rows (up to 128) and an even number of query heads to a key
-//     head: the two blocks of a CTA are two heads over one stream of keys;
-//   * head_dim 64 leaves TMEM for an S tile per group, so that S runs two visits ahead.
+//     head: the two blocks of a CTA are two heads over one stream of keys.
+// Bound by the softmax threads: a chunk of both blocks takes 2,700 cycles, 2,048 of them the
+// exponential unit's (16 a cycle and SM), 2,060 (head_dim 64: 1,260) the tensor pipe's; a warp
+// alone keeps the exponential unit 72 % busy, and loads, barriers and the row's state take a
+// visit 700 cycles beside it.  Four softmax warps a sub-partition with half a row each (2,740
+// cycles), barriers tested ahead of need and a quarter of the exponentials as polynomials
+// (3,300) did not help.  A CTA's start and end take 8,000 cycles (2,700 until its loads are
+// out, 2,000 to the first S, 1,000 for the last P V, 2,000 for the rows).
+// Measured: 12,480 tokens, 4 heads of 128, frames of 960, window 2 and a sink frame: 90 us, 965
+// TFLOP/s of kept pairs; 2 x 4,000 tokens, 16 heads of 64 on 4, window of 1,024 tokens: 76 us.
 // Query blocks are launched last first: under a causal mask those are the longest, and the
 // hardware hands CTAs out in index order.  Neighbouring CTAs are heads of one group, so
 // the K and V chunks they share meet in L2.
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     hk * (t ? p.v_mh : p.k_mh), it.b * (t ? p.v_mb : p.k_mb));
     };
     // Q and the first K and V are on their way before the CTA meets, Q before the list of keys
-    // is known: the first S of a CTA waited 5,600 cycles when they were loaded behind both.
+    // is known (behind both, the first S came 600 cycles later).
     int fetched = 0;
     if (warp == 0) {
         const uint32_t qf = smem_u32(&bar->q_full);

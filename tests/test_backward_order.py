@@ -141,7 +141,7 @@ def dkdv_cta(n_blk, group, first, steps, ragged, rng, warps=2, QS=3, OS=2):
     qf, qe = [Bar() for _ in range(QS)], [Bar() for _ in range(QS)]
     of, oe = [Bar() for _ in range(OS)], [Bar(2) for _ in range(OS)]
     tf, te = [Bar() for _ in range(OS)], [Bar() for _ in range(OS)]
-    s_full, dp_full = [Bar(), Bar()], [Bar(), Bar()]
+    s_full, dp_full = [Bar(), Bar()], Bar()
     p_ready, ds_ready = [Bar(warps), Bar(warps)], [Bar(warps), Bar(warps)]
     req, done_z = [Bar(), Bar()], [Bar(), Bar()]
     q_in, o_in, t_in = [None] * QS, [None] * OS, [None] * OS
@@ -190,12 +190,12 @@ def dkdv_cta(n_blk, group, first, steps, ragged, rng, warps=2, QS=3, OS=2):
             s_full[g].arrive()
         m.product("x", done)
 
-    def issue_dp(i, g):
+    def issue_dp(i):
         def done():
-            dp_tile[g] = ("dP", i)
-            dp_full[g].arrive()
-            if g:
-                oe[i % OS].arrive()
+            assert o_in[i % OS] == i
+            dp_tile[:] = [("dP", i)] * 2
+            dp_full.arrive()
+            oe[i % OS].arrive()
         m.product("y", done)
 
     def issuer_x():
@@ -221,8 +221,7 @@ def dkdv_cta(n_blk, group, first, steps, ragged, rng, warps=2, QS=3, OS=2):
     def issuer_y():
         cleaned = [0, 0]
         yield from take(0, 1, True, cleaned)
-        issue_dp(0, 0)
-        issue_dp(0, 1)
+        issue_dp(0)
         for i in range(steps):
             yield lambda: qf[i % QS].passed(i // QS)
             assert q_in[i % QS] == i
@@ -237,8 +236,8 @@ def dkdv_cta(n_blk, group, first, steps, ragged, rng, warps=2, QS=3, OS=2):
                         qe[i % QS].arrive()
                         te[i % OS].arrive()
                 m.product("y", dk)
-                if i + 1 < steps:
-                    issue_dp(i + 1, g)
+            if i + 1 < steps:
+                issue_dp(i + 1)
 
     left = {}
 
@@ -251,7 +250,7 @@ def dkdv_cta(n_blk, group, first, steps, ragged, rng, warps=2, QS=3, OS=2):
             if left[g, i, "p"] == warps:
                 s_tile[g] = ("P", i)
             p_ready[g].arrive()
-            yield lambda: dp_full[g].passed(i)
+            yield lambda: dp_full.passed(i)
             assert dp_tile[g][1] == i and t_in[i % OS] == i
             left[g, i, "d"] = left.get((g, i, "d"), 0) + 1
             if left[g, i, "d"] == warps:
