@@ -367,6 +367,14 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
         tmem_alloc(smem_u32(&bar->tmem_base), 512);
         tmem_relinquish();
     }
+    // Q or dO of step i (query head h, block blk) into its stage
+    auto fetch = [&](int i, bool o, int row, int h, int b) {
+        const int st = i % (o ? C::kOStages : C::kQStages);
+        const uint32_t fb = smem_u32(o ? &bar->o_full[st] : &bar->q_full[st]);
+        mbar_arrive_expect_tx(fb, C::kTile);
+        tma_load_5d(smem_u32((o ? sO : sQ) + st * C::kTile), o ? &tmO : &tmQ, fb, 0, row, 0,
+                    h * (o ? p.o_mh : p.q_mh), b * (o ? p.o_mb : p.q_mb));
+    };
     if (warp == 0) {
         __syncwarp();  // (or the item is worked out for lane 0 and for the others, one after the other)
         KvItem mine;
@@ -379,6 +387,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                 mbar_arrive_expect_tx(kvf, 2 * C::kTile);
                 tma_load_5d(smem_u32(sK), &tmK, kvf, 0, mine.k0, 0, mine.hk * p.k_mh, mine.b * p.k_mb);
                 tma_load_5d(smem_u32(sV), &tmV, kvf, 0, mine.k0, 0, mine.hk * p.v_mh, mine.b * p.v_mb);
+                for (int o = 0; o < 2; ++o)
+                    fetch(0, o, (mine.qb0 + mine.blk0) * kT, mine.hk * p.s.group + mine.g0, mine.b);
             }
         }
     }
@@ -407,19 +417,15 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                 const int qr = i / C::kQStages, orr = i / C::kOStages;
                 if (qr > 0 && !mbar_wait(smem_u32(&bar->q_empty[qs]), (qr - 1) & 1, abort_flag))
                     break;
-                uint32_t fb = smem_u32(&bar->q_full[qs]);
-                mbar_arrive_expect_tx(fb, C::kTile);
-                tma_load_5d(smem_u32(sQ + qs * C::kTile), &tmQ, fb, 0, row, 0, h * p.q_mh, b * p.q_mb);
+                if (i > 0) fetch(i, false, row, h, b);  // (the first are on their way)
                 q_issued = i + 1;
                 if (orr > 0 && !mbar_wait(smem_u32(&bar->o_empty[os]), (orr - 1) & 1, abort_flag))
                     break;
-                fb = smem_u32(&bar->o_full[os]);
-                mbar_arrive_expect_tx(fb, C::kTile);
-                tma_load_5d(smem_u32(sO + os * C::kTile), &tmO, fb, 0, row, 0, h * p.o_mh, b * p.o_mb);
+                if (i > 0) fetch(i, true, row, h, b);
                 o_issued = i + 1;
                 if (orr > 0 && !mbar_wait(smem_u32(&bar->st_empty[os]), (orr - 1) & 1, abort_flag))
                     break;
-                fb = smem_u32(&bar->st_full[os]);
+                const uint32_t fb = smem_u32(&bar->st_full[os]);
                 mbar_arrive_expect_tx(fb, C::kStats);
                 bulk_load(smem_u32(sStats + os * C::kStats),
                           p.stats + (((long long)b * p.s.hq + h) * p.n_qblk + qb0 + blk) * 2 * kT,
@@ -815,6 +821,14 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
         tmem_alloc(smem_u32(&bar->tmem_base), 512);
         tmem_relinquish();
     }
+    // K or V of step i (chunk c of key head hk) into its stage
+    auto fetch = [&](int i, bool v, int c, int hk, int b) {
+        const int st = i % (v ? C::kVStages : C::kKStages);
+        const uint32_t fb = smem_u32(v ? &bar->v_full[st] : &bar->k_full[st]);
+        mbar_arrive_expect_tx(fb, C::kTile);
+        tma_load_5d(smem_u32((v ? sV : sK) + st * C::kTile), v ? &tmV : &tmK, fb, 0, c * kT, 0,
+                    hk * (v ? p.v_mh : p.k_mh), b * (v ? p.v_mb : p.k_mb));
+    };
     if (warp == 0) {
         __syncwarp();
         DqItem mine;
@@ -827,6 +841,8 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
                 mbar_arrive_expect_tx(qf, 2 * C::kTile);
                 tma_load_5d(smem_u32(sQ), &tmQ, qf, 0, mine.blk * kT, 0, mine.h * p.q_mh, mine.b * p.q_mb);
                 tma_load_5d(smem_u32(sO), &tmO, qf, 0, mine.blk * kT, 0, mine.h * p.o_mh, mine.b * p.o_mb);
+                for (int v = 0; v < 2; ++v)
+                    fetch(0, v, mine.list.a > 0 ? 0 : mine.skip, mine.hk, mine.b);
             }
         }
     }
@@ -855,19 +871,15 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
             int k_issued = 0, v_issued = 0;
             if (threadIdx.x == 0) {
                 for (int i = 0; i < E; ++i) {
-                    const int row = chunk_of(i) * kT, ks = i % C::kKStages, vs = i % C::kVStages;
+                    const int c = chunk_of(i), ks = i % C::kKStages, vs = i % C::kVStages;
                     const int kr = i / C::kKStages, vr = i / C::kVStages;
                     if (kr > 0 && !mbar_wait(smem_u32(&bar->k_empty[ks]), (kr - 1) & 1, abort_flag))
                         break;
-                    uint32_t fb = smem_u32(&bar->k_full[ks]);
-                    mbar_arrive_expect_tx(fb, C::kTile);
-                    tma_load_5d(smem_u32(sK + ks * C::kTile), &tmK, fb, 0, row, 0, hk * p.k_mh, b * p.k_mb);
+                    if (i > 0) fetch(i, false, c, hk, b);  // (the first are on their way)
                     k_issued = i + 1;
                     if (vr > 0 && !mbar_wait(smem_u32(&bar->v_empty[vs]), (vr - 1) & 1, abort_flag))
                         break;
-                    fb = smem_u32(&bar->v_full[vs]);
-                    mbar_arrive_expect_tx(fb, C::kTile);
-                    tma_load_5d(smem_u32(sV + vs * C::kTile), &tmV, fb, 0, row, 0, hk * p.v_mh, b * p.v_mb);
+                    if (i > 0) fetch(i, true, c, hk, b);
                     v_issued = i + 1;
                 }
             }
