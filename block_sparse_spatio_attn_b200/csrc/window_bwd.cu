@@ -1200,10 +1200,11 @@ static size_t stats_bytes(const svga_window_problem *p)
 // cost their sums in memory and a join.  Sinks are split above per_sm, others, which overlap
 // less, above 1.25 of it, and nothing into parts of fewer than 8 steps, unless the whole launch
 // is less than one round of CTAs: then as finely as still fits in one.  Measured (backward in
-// all, split against not, us): 8,192 tokens causal, 8 heads on 2: 391 against 442; 13 frames of
-// 960 tokens, sinks of 98 steps, per_sm 133: 281 against 266; 2,048 tokens causal, 4 heads: 53
-// against 41; 2 x 2,001 tokens in a window with sinks, per_sm 18, sinks of 64 steps: 56 against
-// 165; 500 tokens, 2 heads on 1: 21 against 27.
+// all, us): 8,192 tokens causal, 8 heads on 2, per_sm 200: in two 367, unsplit 450; 13 frames of
+// 960 tokens, per_sm 129, sinks of 98 steps: unsplit 252, sinks in two 260, in four 265; 2,048
+// tokens causal, 4 heads, per_sm 6: unsplit 34, in two 37; 2 x 2,001 tokens in a window, per_sm
+// 15, sinks of 64 steps: sinks in five and the others in two 48, unsplit 121; 1,000 tokens, 8
+// heads of 64 on 2, a window of 300, one round: in five 21, in two 26, unsplit 36.
 static Split choose_bwd_split(const svga_window_problem *p)
 {
     const long long heads = (long long)p->batch * p->kv_heads;

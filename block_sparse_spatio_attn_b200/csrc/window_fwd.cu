@@ -655,14 +655,31 @@ bool pair_heads(const svga_window_problem *p)
 
 // Which items are split, from the shapes alone.  An item's list is as long as the shapes allow;
 // the GPU runs kSms items at a time.
-//   * less than one round of items: all split, to fill it once;
+//   * less than one round of items: all split into as many parts as split_cost finds best.
+//     Measured against none, the best of all and what fits one round (us): causal, 4 heads of
+//     4,000 tokens, 64 items of 2 to 32 chunks: 33 (3 parts), 56, 33, 39; 8 heads, 128 items: 49
+//     (2), 58, 49, 58; 1,000 tokens, 4 heads: 18 (4), 23, 18; one token over 2,000 keys, 8 heads
+//     on 1: 14 (8), 31, 14;
 //   * more, of lists of about one length (mean at least 0.65 of the longest): those behind the
 //     last whole round are split to fill one more, where that shortens it by at least 8 chunks
-//     (12,480 tokens of 4 heads, 196 items of 30 chunks: 110 us against 128 unsplit, all split in
-//     two 137, the partial sums cost more; 512 items of 11 chunks: 94 against 87, so not there);
+//     (12,480 tokens of 4 heads, 196 items of 28 chunks: 88 us against 109 unsplit, all split in
+//     two 111, the partial sums cost more; 512 items of 9 chunks: 80 against 76, so not there);
 //   * nothing from eight rounds on, nor where a causal list without a window makes lengths run
 //     from 1 to the longest: those are launched longest first and pack by themselves.
-// A part keeps at least kMinChunksPerSplit chunks.
+// A part of the second kind keeps at least kMinChunksPerSplit chunks.
+
+// The time of n < kSms items split into k parts each, in chunks: a CTA's start and end cost 3, the
+// join 3 and a quarter a part; past one round of CTAs the SMs share the sum, and the last
+// CTAs leave half a part's time unused.
+double split_cost(long long n, int k, double longest, double mean)
+{
+    constexpr double kCta = 3, kJoin = 3, kPart = 0.25;
+    double t = longest / k + kCta;
+    if (n * k > kSms)
+        t = std::max(t, n * (mean + k * kCta) / kSms + 0.5 * (mean / k + kCta));
+    return k > 1 ? t + kJoin + kPart * k : t;
+}
+
 Split choose_split(const svga_window_problem *p)
 {
     const long long pairs = (p->q_tokens + 2 * kBlockM - 1) / (2 * kBlockM);
@@ -679,11 +696,14 @@ Split choose_split(const svga_window_problem *p)
         longest = std::max<long long>(longest, len);
         sum += len;
     }
-    const long long most = std::max(1ll, longest / kMinChunksPerSplit);
     if (n < kSms) {
-        s.k1 = (int)std::min<long long>(kSms / n, most);
+        const double mean = (double)sum / pairs;
+        for (int k = 2; k <= std::min(longest, 64ll); ++k)
+            if (split_cost(n, k, longest, mean) < split_cost(n, s.k1, longest, mean)) s.k1 = k;
     } else if (20 * sum >= 13 * longest * pairs) {
-        const int tail = (int)(n % kSms), k = (int)std::min<long long>(kSms / tail, most);
+        const int tail = (int)(n % kSms);
+        const int k = (int)std::min<long long>(kSms / tail,
+                                               std::max(1ll, longest / kMinChunksPerSplit));
         if (longest - longest / k >= 8) {
             s.n1 = (int)n - tail;
             s.k2 = k;
