@@ -698,8 +698,16 @@ Split choose_split(const svga_window_problem *p)
     }
     if (n < kSms) {
         const double mean = (double)sum / pairs;
-        for (int k = 2; k <= std::min(longest, 64ll); ++k)
-            if (split_cost(n, k, longest, mean) < split_cost(n, s.k1, longest, mean)) s.k1 = k;
+        double best = split_cost(n, 1, longest, mean);
+        for (int k = 2; k <= std::min(longest, 64ll); ++k) {
+            const double t = split_cost(n, k, longest, mean);
+            if (t < best) {
+                best = t;
+                s.k1 = k;
+            } else if (t > best + 2) {  // past the minimum: the parts' own cost grows from here
+                break;
+            }
+        }
     } else if (20 * sum >= 13 * longest * pairs) {
         const int tail = (int)(n % kSms);
         const int k = (int)std::min<long long>(kSms / tail,
