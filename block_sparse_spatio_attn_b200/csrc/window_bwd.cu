@@ -1199,7 +1199,8 @@ static size_t stats_bytes(const svga_window_problem *p)
 // at about three quarters of the time): a longer item holds up the whole launch, while parts
 // cost their sums in memory and a join.  Sinks are split above per_sm, others, which overlap
 // less, above 1.25 of it, and nothing into parts of fewer than 8 steps, unless the whole launch
-// is less than one round of CTAs: then as finely as still fits in one.  Measured (backward in
+// is less than one round of CTAs: then as finely as still fits in one, where that is not much
+// coarser (3 x 1,176 tokens, 3 heads of 64 on 1, 30 items of 30 steps: in three 40 us, whole 52).  Measured (backward in
 // all, us): 8,192 tokens causal, 8 heads on 2, per_sm 200: in two 367, unsplit 450; 13 frames of
 // 960 tokens, per_sm 129, sinks of 98 steps: unsplit 252, sinks in two 260, in four 265; 2,048
 // tokens causal, 4 heads, per_sm 6: unsplit 34, in two 37; 2 x 2,001 tokens in a window, per_sm
@@ -1244,10 +1245,15 @@ static Split choose_bwd_split(const svga_window_problem *p)
     s.k1 = parts(top[0], std::max(per_sm, 8.0));
     s.k2 = parts(top[1], std::max(1.25 * per_sm, 8.0));
     const long long free = kSms - (long long)p->batch * p->q_heads * ((p->q_tokens + kT - 1) / kT);
+    Split one = s;
     for (double most = 2.0; n <= free; most *= 1.25) {  // one round in all: fill it
-        s.k1 = parts(top[0], most);
-        s.k2 = parts(top[1], most);
-        if (s.ctas() <= free) break;
+        one.k1 = parts(top[0], most);
+        one.k2 = parts(top[1], most);
+        if (one.ctas() <= free) {
+            // (unless that leaves parts of more than twice the length)
+            if (s.k1 <= 2 * one.k1 && s.k2 <= 2 * one.k2) s = one;
+            break;
+        }
     }
     return s;
 }

@@ -157,6 +157,21 @@ def test_split_key_lists(B, H, G, nq, nk):
     assert e.value.status == 5
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,G,nq,nk", [(1, 1, 1, 700), (8, 1, 1, 2000), (3, 1, 200, 1000), (1, 1, 256, 4097),
+                                       (2, 2, 1500, 1500), (6, 3, 700, 1400), (1, 1, 600, 500), (16, 8, 90, 2100)])
+def test_short_launches_split_into_small_parts(H, G, nq, nk, d):
+    """Parts of a chunk or two: some have no key for one of a CTA's two query blocks, or for
+    either, and padded sequences leave parts empty."""
+    q = values(2, H, nq, d, dtype=BF, seed=nq)
+    k, v = (values(2, G, nk, d, dtype=BF, seed=s) for s in (1, 2))
+    assert svga.svga_window_attention_size(q, k, M())["fwd_bytes"] > 0 or nk <= 512  # (four chunks: whole)
+    for mask in (M(), M(window=300, sinks=200), M(causal=False, window=0, block=400)):
+        for k_lens in (None, [nk, max(nk // 7, 1)]):
+            o, lse = forward(q, k, v, mask, 0.1, None, k_lens)
+            check(q, k, v, mask, 0.1, o, lse, None, k_lens)
+
+
 @pytest.mark.parametrize("mask,dtype,split", [(M(window=1800, sinks=100), BF, True), (M(window=700, sinks=100), BF, False), (M(), FP, False)],
                          ids=str)
 def test_launches_split_in_part(mask, dtype, split):
