@@ -126,7 +126,7 @@ struct Barriers {
     uint32_t tmem_base;
     int abort;
     int some;   // the item has queries
-    Item item;  // worked out by warp 0 for all: by every warp it took 2,000 cycles more
+    Item item;  // worked out by warp 3 for all: by every warp it took 2,000 cycles more
 };
 
 // The merged chunk list of two consecutive runs of queries.  The windows of consecutive
@@ -223,8 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // warp 0 sets up what the first loads need, works out the item and starts them; warp 2 sets
-    // up the rest
+    // warps 0 and 3 set up what the first loads need and start them, warp 2 the rest
     if (threadIdx.x == 64) {
         for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&bar->kv_empty[s]), 1);
         for (int i = 0; i < 2; ++i) {
@@ -253,39 +252,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_5d(smem_u32(sKV + s * C::kKVBytes), t ? &tmV : &tmK, fb, 0, row, 0,
                     hk * (t ? p.v_mh : p.k_mh), it.b * (t ? p.v_mb : p.k_mb));
     };
-    // Q and the first K and V are on their way before the CTA meets, Q before the list of keys
-    // is known (behind both, the first S came 600 cycles later).
-    int fetched = 0;
+    // Q and the first K and V are on their way before the CTA meets: warp 0 loads Q, which needs
+    // only the item's place, while warp 3 works out the list of keys (one warp for both takes 500
+    // cycles more).
     if (warp == 0) {
         const uint32_t qf = smem_u32(&bar->q_full);
-        if (lane == 0) {
+        if (threadIdx.x == 0) {
             prefetch_tmap(&tmQ);
+            mbar_init(qf, 1);
+            fence_barrier_init();
+        }
+        __syncwarp();  // (or what follows is run for one lane and for the others one after the other)
+        int part;
+        if (make_item(p, it, part) && threadIdx.x == 0) {
+            const int nq_tiles = it.valid1 ? 2 : 1;
+            mbar_arrive_expect_tx(qf, nq_tiles * C::kQBytes);
+            for (int i = 0; i < nq_tiles; ++i)
+                tma_load_5d(smem_u32(sQ + i * C::kQBytes), &tmQ, qf, 0,
+                            (it.b0 + (p.by_heads ? 0 : i)) * kBlockM, 0,
+                            (it.h + (p.by_heads ? i : 0)) * p.q_mh, it.b * p.q_mb);
+        }
+    } else if (warp == 3) {
+        if (elect_one()) {
             prefetch_tmap(&tmK);
             prefetch_tmap(&tmV);
-            mbar_init(qf, 1);
             for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&bar->kv_full[s]), 1);
             fence_barrier_init();
         }
-        __syncwarp();  // (or what follows is run for lane 0 and for the others one after the other)
+        __syncwarp();
         int part;
         const bool some = make_item(p, it, part);
-        if (lane == 0) bar->some = some;
-        if (some) {
-            if (threadIdx.x == 0) {
-                const int nq_tiles = it.valid1 ? 2 : 1;
-                mbar_arrive_expect_tx(qf, nq_tiles * C::kQBytes);
-                for (int i = 0; i < nq_tiles; ++i)
-                    tma_load_5d(smem_u32(sQ + i * C::kQBytes), &tmQ, qf, 0,
-                                (it.b0 + (p.by_heads ? 0 : i)) * kBlockM, 0,
-                                (it.h + (p.by_heads ? i : 0)) * p.q_mh, it.b * p.q_mb);
+        if (some) make_lists(p, it, part);
+        if (elect_one()) {
+            if (some && it.E > 0) {
+                fetch(0);
+                fetch(1);
             }
-            __syncwarp();
-            make_lists(p, it, part);
-            if (lane == 0) {
-                if (it.E > 0)
-                    while (fetched < 2) fetch(fetched++);
-                bar->item = it;
-            }
+            bar->item = it;
+            bar->some = some;
         }
     }
     pdl_start();  // the join, if there is one
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsLow>();
-        if (warp != 0) it = bar->item;
+        it = bar->item;
         // the chunk whose last rows lie past the sequence's end but inside the tensor
         const int ragged = (p.s.k_lens && it.nk < p.s.tk && it.nk % kKN) ? it.nk / kKN : -1;
         // Two threads issue the products: warp 1's S = Q K^T, warp 3's O += P V.  Each waits on its
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) {
             // -------------------------------------------------------- TMA producer
             const uint32_t qf = smem_u32(&bar->q_full);
-            int issued = fetched;
+            int issued = min(2, 2 * it.E);  // the first K and V are on their way
             for (; issued < 2 * it.E; ++issued) {
                 const int s = issued % C::kStages, round = issued / C::kStages;
                 if (round > 0 && !mbar_wait(smem_u32(&bar->kv_empty[s]), (round - 1) & 1, abort_flag)) break;
