@@ -142,8 +142,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         bar->abort = 0;
         fence_barrier_init();
     }
+    pdl_wait();  // before anything in memory is looked at
+    pdl_start();
     // the sequence, its kept keys and this CTA's share of their chunks
-    int len = __ldg(p.lens + b);
+    int len = p.lens[b];
     if (len < 0 || len > p.max_pages * p.page_size) {
         if (threadIdx.x == 0 && rank == 0 && p.status)
             atomicCAS(p.status, 0, (int32_t)SVGA_ERR_INVALID_ARG);
@@ -163,10 +165,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     const int rows = min(kRows, p.group - tile * kRows);
     for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
         const int r = i / (D / 8), u = i - r * (D / 8);
-        const uint4 x = r < rows ? __ldg(reinterpret_cast<const uint4 *>(
-                                             p.q + 2 * (b * p.q_sb + (head0 + r) * p.q_sh)) +
-                                         u)
-                                 : make_uint4(0u, 0u, 0u, 0u);
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows)
+            x = reinterpret_cast<const uint4 *>(p.q + 2 * (b * p.q_sb + (head0 + r) * p.q_sh))[u];
         st_shared_v4(sQ + r * (D * 2) + ((u ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
     }
     __syncthreads();
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
             const int j = chunk_of(e) * kChunk + g * p.box, slot = j / p.page_size;
             // any kept key: in [lo, hi), or below the end of the sinks
             if (j >= mr.hi || !(j + p.box > mr.lo || j < mr.sk)) return -1;
-            const int page = __ldg(p.page_table + (long long)b * p.max_pages + slot);
+            const int page = p.page_table[(long long)b * p.max_pages + slot];
             if (page < 0 || page >= p.pages) {
                 if (p.status) atomicCAS(p.status, 0, (int32_t)SVGA_ERR_INVALID_ARG);
                 return -1;
@@ -446,12 +447,14 @@ svga_status launch(const svga_paged_cache *c, const DecodeParams &p, int ranks, 
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kAlloc;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = ranks;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, tk, tv, p);
     if (e != cudaSuccess) {
         cudaGetLastError();

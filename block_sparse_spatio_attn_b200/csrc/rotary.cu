@@ -89,7 +89,7 @@ __device__ __forceinline__ float2 pair_cs(const RotParams &p, int i, int f, int 
         at = p.F * p.pf + r * p.ph + (i - p.pf);
     else
         at = p.F * p.pf + p.gh * p.ph + c * pw + (i - p.pf - p.ph);
-    return __ldg(p.table + at);
+    return p.table[at];
 }
 
 // The two values of a packed pair, and back.
@@ -152,6 +152,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
                                                           const __grid_constant__ Ord ord)
 {
     constexpr int V = Vec<T>::N;  // values of a piece
+    pdl_wait();   // before anything in memory is looked at
+    pdl_start();
     const long long idx = blockIdx.x * (long long)kThreads + threadIdx.x;
     // 32-bit divisions where the piece index fits (64-bit ones cost a tenth of the kernel)
     const bool small = (long long)p.batch * p.tokens * p.units <= 0x7fffffffll;
@@ -166,8 +168,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
     // the token's place in the grid
     long long pos;
     if (DST == DST_PAGED) {
-        const int n = p.new_lens ? __ldg(p.new_lens + b) : p.tokens;
-        const int len = __ldg(p.lens + b);
+        const int n = p.new_lens ? p.new_lens[b] : p.tokens;
+        const int len = p.lens[b];
         if (n < 0 || n > p.tokens || len < 0) {
             if (unit == 0) set_status(p.status);
             return;
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
         if (t >= n) return;
         pos = (long long)len - n + t;
     } else {
-        pos = p.positions ? (long long)__ldg(p.positions + tok_all) : p.first + t;
+        pos = p.positions ? (long long)p.positions[tok_all] : p.first + t;
     }
     int f = 0, s = 0, row = 0, col = 0;
     if (p.turn || DST == DST_ORDERED) {  // (a value goes where its key does, or neither)
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
     if (DST == DST_PAGED) {
         const long long slot = pos < 0 ? -1 : pos / p.page_size;
         const int page = slot >= 0 && slot < p.max_pages
-                             ? __ldg(p.page_table + (long long)b * p.max_pages + slot)
+                             ? p.page_table[(long long)b * p.max_pages + slot]
                              : -1;
         if (page < 0 || page >= p.pages) {
             if (unit == 0) set_status(p.status);
@@ -364,8 +366,7 @@ svga_status launch(RotParams &p, const Ord &ord, cudaStream_t st)
     p.heads_per_thread = hpt;
     const dim3 grid((unsigned)blocks, (unsigned)((p.heads + hpt - 1) / hpt),
                     DST == DST_PAGED ? 2 : 1);
-    rotary_kernel<T, LAY, DST, Ord><<<grid, kThreads, 0, st>>>(p, ord);
-    return check_launch_of("rotary");
+    return launch_after(rotary_kernel<T, LAY, DST, Ord>, grid, kThreads, 0, st, "rotary", p, ord);
 }
 
 template <typename T, int DST, typename Ord>

@@ -232,11 +232,11 @@ svga_status check_launch_of(const char *what);  // cudaGetLastError as a status
 // Launch of a kernel that begins while the one before it in the stream is still running and
 // waits for it itself (pdl_wait, in every CTA, before it touches what that one writes).
 template <typename... Params, typename... Args>
-svga_status launch_after(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem,
+svga_status launch_after(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem,
                          cudaStream_t st, const char *what, const Args &...args)
 {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;

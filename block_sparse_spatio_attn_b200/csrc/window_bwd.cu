@@ -109,7 +109,7 @@ struct Cfg {
 
 __device__ __forceinline__ int clamped_len(const int32_t *lens, int b, int most)
 {
-    return lens ? min(max(__ldg(lens + b), 0), most) : most;
+    return lens ? min(max(lens[b], 0), most) : most;
 }
 
 __device__ __forceinline__ uint32_t bits_below(int n)
@@ -141,6 +141,9 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) bwd_rows_kernel(const BwdParams p)
 {
+    pdl_wait();
+    // not before: the next kernel reads this call's inputs at once, and then all that came before
+    // this kernel is known to be done
     pdl_start();
     constexpr int kPer = D / 8;
     const long long i = blockIdx.x * 256ll + threadIdx.x;
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(256) bwd_rows_kernel(const BwdParams p)
 #pragma unroll
     for (int k = kPer / 2; k > 0; k /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, k);
     if (c != 0) return;
-    const float lse = there ? __ldg(p.lse + bh * p.s.tq + t) : -INFINITY;
+    const float lse = there ? p.lse[bh * p.s.tq + t] : -INFINITY;
     float *out = p.stats + ((bh * p.n_qblk + t / kT) * 2) * kT + t % kT;
     out[0] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // an empty row keeps nothing
     out[kT] = -sum;
@@ -392,8 +395,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
             }
         }
     }
-    pdl_start();  // the join, if there is one
-    pdl_wait();   // the rows' statistics
+    if (warp == 1) pdl_start();  // the next kernel, once this one has its TMEM
+    pdl_wait();                  // the rows' statistics
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -695,6 +698,7 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(256) bwd_join_kernel(const BwdParams p)
 {
     pdl_wait();  // the parts
+    pdl_start();
     constexpr int kPer = D / 8;
     const long long i = blockIdx.x * 256ll + threadIdx.x;
     const int c = 8 * (int)(i % kPer);
@@ -711,9 +715,8 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const BwdParams p)
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int j = 0; j < k; ++j) {
-        const float4 u = __ldg(reinterpret_cast<const float4 *>(src + (long long)j * 2 * kT * D));
-        const float4 v =
-            __ldg(reinterpret_cast<const float4 *>(src + (long long)j * 2 * kT * D) + 1);
+        const float4 *at = reinterpret_cast<const float4 *>(src + (long long)j * 2 * kT * D);
+        const float4 u = at[0], v = at[1];
         x[0] += u.x;
         x[1] += u.y;
         x[2] += u.z;
@@ -846,8 +849,8 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
             }
         }
     }
-    pdl_start();  // the join, if there is one
-    pdl_wait();   // the rows' statistics
+    if (warp == 1) pdl_start();  // the next kernel, once this one has its TMEM
+    pdl_wait();                  // the rows' statistics
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -973,7 +976,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
         MaskRange mr = {0, 0, 0};
         if (qrow < nq) mr = mask_range(p.s.mask, qrow + off, nk);
         const float *st = p.stats + (((long long)b * p.s.hq + h) * p.n_qblk + blk) * 2 * kT + row;
-        const float nl = __ldg(st), nd = __ldg(st + kT);
+        const float nl = st[0], nd = st[kT];
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl),
                      nd2 = make_float2(nd, nd);
         bool ok = true;
@@ -1104,7 +1107,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ BwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    if (smem_misplaced(smem, p.s.status)) return;
+    if (smem_misplaced(smem, p.s.status)) {
+        pdl_wait();
+        return;
+    }
     if ((int)blockIdx.x < p.n_dkdv)
         dkdv_cta<D, F16>(tmQ, tmO, tmK, tmV, p, smem, blockIdx.x);
     else
@@ -1157,8 +1163,9 @@ svga_status launch(const svga_view &d_o, const svga_view &q, const svga_view &k,
     }
     if (hq) {
         const long long n = (long long)p->batch * p->q_heads * kp.n_qblk * kT * (D / 8);
-        bwd_rows_kernel<D, F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(kp);
-        if ((rc = check_launch_of("window backward rows")) != SVGA_OK) return rc;
+        rc = launch_after(bwd_rows_kernel<D, F16>, (unsigned)((n + 255) / 256), 256, 0, st,
+                          "window backward rows", kp);
+        if (rc != SVGA_OK) return rc;
     }
     kp.n_dkdv = hk ? (int)kp.split.ctas() : 0;
     const long long n_dq = hq ? (long long)p->batch * p->q_heads * kp.n_qblk : 0;
@@ -1166,7 +1173,7 @@ svga_status launch(const svga_view &d_o, const svga_view &q, const svga_view &k,
     if (hq) {
         rc = launch_after(bwd_kernel<D, F16>, grid, kThreads, kAlloc, st, "window backward", tq, to,
                           tk, tv, kp);
-    } else {  // no rows kernel before it
+    } else {  // no rows kernel before it, whose wait would cover the inputs it reads at once
         bwd_kernel<D, F16><<<grid, kThreads, kAlloc, st>>>(tq, to, tk, tv, kp);
         rc = check_launch_of("window backward");
     }

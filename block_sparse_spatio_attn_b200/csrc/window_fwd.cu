@@ -149,7 +149,7 @@ __host__ __device__ __forceinline__ void merge_lists(const ChunkList &l0, const 
 
 __device__ __forceinline__ int clamped_len(const int32_t *lens, int b, int most)
 {
-    return lens ? min(max(__ldg(lens + b), 0), most) : most;
+    return lens ? min(max(lens[b], 0), most) : most;
 }
 
 // Item `i` in launch order: its sequence, first head and first 128-row block.
@@ -242,6 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&bar->tmem_base), 512);
         tmem_relinquish();
     }
+    pdl_wait();                  // before anything in memory is looked at
+    if (warp == 1) pdl_start();  // (the next kernel's CTAs find no TMEM left to wait for)
     Item it;
     // K (idx even) or V of entry idx / 2 into its stage
     auto fetch = [&](int idx) {
@@ -292,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar->some = some;
         }
     }
-    pdl_start();  // the join, if there is one
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -602,6 +603,7 @@ template <bool F16>
 __global__ void __launch_bounds__(256) join_kernel(const FwdParams p, int d)
 {
     pdl_wait();  // the parts
+    pdl_start();
     const int per = d / 8;
     const long long i = blockIdx.x * 256ll + threadIdx.x;
     const long long all = i / per;
@@ -619,15 +621,15 @@ __global__ void __launch_bounds__(256) join_kernel(const FwdParams p, int d)
     constexpr int kStep = 2 * kBlockM;  // rows from one part's slot to the next
     float m = -INFINITY;
 #pragma unroll 4
-    for (int r = 0; r < k; ++r) m = fmaxf(m, __ldg(&p.part_ml[at + r * kStep].x));
+    for (int r = 0; r < k; ++r) m = fmaxf(m, p.part_ml[at + r * kStep].x);
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int r = 0; r < k; ++r) {
-        const float2 ml = __ldg(&p.part_ml[at + r * kStep]);
+        const float2 ml = p.part_ml[at + r * kStep];
         const float4 *src =
             reinterpret_cast<const float4 *>(p.part_o + (at + r * kStep) * d + c);
-        const float4 u = __ldg(src), v = __ldg(src + 1);
+        const float4 u = src[0], v = src[1];
         const float w = exp2f(ml.x - ref);
         l += w * ml.y;
         x[0] += w * u.x;
@@ -758,8 +760,8 @@ svga_status launch(const svga_view &q, const svga_view &k, const svga_view &v, F
         set_error("cudaFuncSetAttribute(max dynamic shared memory) failed");
         return SVGA_ERR_CUDA;
     }
-    kfn<<<(unsigned)kp.split.ctas(), kThreads, C::kSmemLaunch, st>>>(tq, tk, tv, kp);
-    svga_status rc = check_launch_of("window attention");
+    svga_status rc = launch_after(kfn, (unsigned)kp.split.ctas(), kThreads, C::kSmemLaunch, st,
+                                  "window attention", tq, tk, tv, kp);
     if (rc != SVGA_OK || kp.split.slots() == 0) return rc;
     const long long n = (long long)(kp.split.split_to() - kp.split.split_from()) * 2 * kBlockM *
                         (D / 8);
