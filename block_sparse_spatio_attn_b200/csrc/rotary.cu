@@ -17,8 +17,8 @@
 // still covers the GPU.
 //
 // Bound by HBM.  Measured: 75,600 tokens of 10 heads of 128 (bf16) into each head's order, 387 MB:
-// 69 us, 5.6 TB/s (86 % of the measured copy); append of 2 x 12,480 tokens of 10 heads, 256 MB:
-// 45 us, 5.7 TB/s; 64 single tokens of 16 heads: 4 us, the time of a launch.
+// 65 us in a loop, 6.0 TB/s (91 % of the measured copy); append of 2 x 12,480 tokens of 10 heads,
+// 256 MB: 43 us, 6.0 TB/s; 64 single tokens of 16 heads: 3.6 us, the time of a launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

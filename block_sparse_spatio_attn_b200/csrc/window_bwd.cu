@@ -46,7 +46,8 @@
 //   * shared memory holds, beside the resident tiles, three stages of the operand that is
 //     needed longest (dkdv: Q, dq: K) and two of the other.
 // Measured: 12,480 tokens, 4 heads of 128, frames of 960, window 2 and a sink frame: 250 us, 870
-// TFLOP/s of the five products of kept pairs; 2 x 2,001 tokens, 8 heads on 2, window of 512: 49 us.
+// TFLOP/s of the five products of kept pairs (291 under sustained load); 2 x 2,001 tokens, 8 heads
+// on 2, window of 512: 46 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -455,7 +455,9 @@ SVGA_API svga_status svga_unpermute_tokens_mapped(const void *src, void *dst,
  *     [batch, tokens, heads, head_dim] output of a projection needs no copy;
  *   - a status word (DEVICE int32 or NULL) is not cleared by a call: it keeps the first
  *     failure found on the device since the caller set it to 0;
- *   - nothing synchronises and nothing is allocated: every call can be captured. */
+ *   - nothing synchronises and nothing is allocated: every call can be captured.  Kernels
+ *     may start while earlier ones of the stream end (programmatic dependent launch), but
+ *     none looks at memory before those are done. */
 
 typedef enum { SVGA_BF16 = 0, SVGA_F16 = 1, SVGA_F32 = 2 } svga_dtype;
 
