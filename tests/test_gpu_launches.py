@@ -148,3 +148,28 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in zip(alone, both):
         same(a.state(), b.state())
+
+
+@pytest.mark.parametrize("d,T", [(64, 70), (128, 33)])
+def test_one_chain_passed_between_two_streams(d, T):
+    """Every call on the other stream than the one before it, joined by events only."""
+    slow, fast = Chain(d, T), Chain(d, T)
+    for _ in range(10):
+        slow.step(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    at = [0]
+    before = torch.cuda.current_stream()
+
+    def turn():
+        now, then = streams[at[0]], streams[1 - at[0]]
+        then.wait_event(now.record_event())
+        at[0] = 1 - at[0]
+        torch.cuda.set_stream(then)
+
+    torch.cuda.set_stream(streams[0])
+    for _ in range(10):
+        fast.step(turn)
+    torch.cuda.synchronize()
+    torch.cuda.set_stream(before)
+    same(slow.state(), fast.state())
