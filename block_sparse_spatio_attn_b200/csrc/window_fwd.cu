@@ -243,8 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&bar->tmem_base), 512);
         tmem_relinquish();
     }
-    pdl_wait();                  // before anything in memory is looked at
-    if (warp == 1) pdl_start();  // (the next kernel's CTAs find no TMEM left to wait for)
+    // Before anything in memory is looked at: the lengths, where sequences have their own, then
+    // the tensors.
+    if (p.s.q_lens || p.s.k_lens) pdl_wait();
     Item it;
     // K (idx even) or V of entry idx / 2 into its stage
     auto fetch = [&](int idx) {
@@ -267,7 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();  // (or what follows is run for one lane and for the others one after the other)
         int part;
-        if (make_item(p, it, part) && threadIdx.x == 0) {
+        const bool some = make_item(p, it, part);
+        pdl_wait();
+        if (some && threadIdx.x == 0) {
             const int nq_tiles = it.valid1 ? 2 : 1;
             mbar_arrive_expect_tx(qf, nq_tiles * C::kQBytes);
             for (int i = 0; i < nq_tiles; ++i)
@@ -286,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int part;
         const bool some = make_item(p, it, part);
         if (some) make_lists(p, it, part);
+        pdl_wait();
         if (elect_one()) {
             if (some && it.E > 0) {
                 fetch(0);
@@ -295,6 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar->some = some;
         }
     }
+    pdl_wait();
+    if (warp == 1) pdl_start();  // (the next kernel's CTAs find no TMEM left to wait for)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
