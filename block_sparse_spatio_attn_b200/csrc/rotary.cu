@@ -152,8 +152,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
                                                           const __grid_constant__ Ord ord)
 {
     constexpr int V = Vec<T>::N;  // values of a piece
-    pdl_wait();   // before anything in memory is looked at
-    pdl_start();
+    // before anything in memory is looked at: tokens' places, where they are there, else the rows
+    // (the host has checked the other places, so that only the last block's idle threads leave
+    // in between)
+    const bool placed = DST == DST_PAGED || p.positions;
+    if (placed) pdl_wait();
     const long long idx = blockIdx.x * (long long)kThreads + threadIdx.x;
     // 32-bit divisions where the piece index fits (64-bit ones cost a tenth of the kernel)
     const bool small = (long long)p.batch * p.tokens * p.units <= 0x7fffffffll;
@@ -267,6 +270,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
         }
         cp_async_commit();  // (an empty group where no head is left keeps the count)
     };
+    if (!placed) pdl_wait();
+    pdl_start();
     for (int u = 0; u < kDepth; ++u) fetch(h0 + u);
 
     // np of the piece's NP angles turn something; with odd halves one angle a value, and the
