@@ -153,8 +153,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
 {
     constexpr int V = Vec<T>::N;  // values of a piece
     // before anything in memory is looked at: tokens' places, where they are there, else the rows
-    // (the host has checked the other places, so that only the last block's idle threads leave
-    // in between)
+    // (in between only threads without a token leave)
     const bool placed = DST == DST_PAGED || p.positions;
     if (placed) pdl_wait();
     const long long idx = blockIdx.x * (long long)kThreads + threadIdx.x;
@@ -185,6 +184,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
     int f = 0, s = 0, row = 0, col = 0;
     if (p.turn || DST == DST_ORDERED) {  // (a value goes where its key does, or neither)
         if (pos < 0 || pos >= (long long)p.F * p.S) {
+            if (!placed) pdl_wait();  // (the host refuses such a first token: a CTA waits all the same)
             if (unit == 0) set_status(p.status);
             return;
         }

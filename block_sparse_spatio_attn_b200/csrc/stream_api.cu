@@ -293,7 +293,7 @@ svga_status svga_rotary(const svga_view *src, const svga_view *dst, int batch, i
     if (inverse != 0 && inverse != 1)
         return bad(SVGA_ERR_INVALID_ARG, "%sinverse must be 0 or 1");
     const long long grid = (long long)spec->num_frames * spec->grid_h * spec->grid_w;
-    if (!positions && (first_token < 0 || first_token + tokens > grid))
+    if (!positions && (first_token < 0 || first_token > grid - tokens))  // (a sum could wrap)
         return bad(SVGA_ERR_SHAPE, "%stokens from first_token %lld on pass the grid's %lld", "",
                    first_token, grid);
     if (spec->order) {
