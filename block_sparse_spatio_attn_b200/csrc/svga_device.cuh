@@ -569,19 +569,19 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// Programmatic dependent launch.  Every kernel of the streaming calls is launched so, within a
-// call and from call to call: its CTAs start, and set up what needs no memory, while the kernel
-// before it in the stream ends (single calls of a few microseconds take 15-40 % less).  For
-// that to change nothing but time,
+// Programmatic dependent launch.  Every kernel of the streaming calls but the one that fills
+// rotary's table is launched so, within a call and from call to call: its CTAs start, and set up
+// what needs no memory, while the kernel before it in the stream ends (single calls of a few
+// microseconds take 15-40 % less).  For that to change nothing but time,
 //   * every CTA calls pdl_wait, before its first access to global memory and on every way out:
-//     so a kernel's end implies the end of all before it;
-//   * pdl_start comes after pdl_wait where the next kernel reads inputs before its own wait (the
-//     backward kernel behind its rows kernel, the only one that does);
+//     so a kernel's end implies the end of all before it, and a wait for that end makes their
+//     writes readable (the start of a kernel, behind another's pdl_start, promises nothing);
 //   * what an earlier kernel may have written is read with plain loads, never __ldg, which asks
 //     for memory that does not change while the kernel runs.
-// pdl_start lets the next kernel of the stream be launched once
-// every CTA of this one has called it; pdl_wait, which that kernel calls, returns when this one
-// has completed and its writes can be read (at once, if it was launched the ordinary way).
+// pdl_start, anywhere in a kernel that needs no TMEM and behind its allocation in one that does,
+// lets the next kernel of the stream be launched once every CTA of this one has called it;
+// pdl_wait, which that kernel calls, returns when this one has completed and its writes can be
+// read (at once, if it was launched the ordinary way).
 __device__ __forceinline__ void pdl_start()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

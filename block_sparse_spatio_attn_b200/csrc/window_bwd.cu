@@ -47,7 +47,7 @@
 //     needed longest (dkdv: Q, dq: K) and two of the other.
 // Measured: 12,480 tokens, 4 heads of 128, frames of 960, window 2 and a sink frame: 250 us, 870
 // TFLOP/s of the five products of kept pairs (291 under sustained load); 2 x 2,001 tokens, 8 heads
-// on 2, window of 512: 46 us.
+// on 2, window of 512: 47 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -143,8 +143,6 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(256) bwd_rows_kernel(const BwdParams p)
 {
     pdl_wait();
-    // not before: the next kernel reads this call's inputs at once, and then all that came before
-    // this kernel is known to be done
     pdl_start();
     constexpr int kPer = D / 8;
     const long long i = blockIdx.x * 256ll + threadIdx.x;
@@ -244,6 +242,7 @@ __device__ __forceinline__ void product_tk(uint32_t d, uint32_t a, uint64_t b, u
 __device__ __forceinline__ bool smem_misplaced(const void *base, int32_t *status)
 {
     if ((smem_u32(base) & 1023u) == 0) return false;
+    pdl_wait();  // before anything in memory is touched
     if (threadIdx.x == 0 && status) atomicCAS(status, 0, (int32_t)SVGA_ERR_ALIGNMENT);
     return true;
 }
@@ -379,10 +378,16 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
         tma_load_5d(smem_u32((o ? sO : sQ) + st * C::kTile), o ? &tmO : &tmQ, fb, 0, row, 0,
                     h * (o ? p.o_mh : p.q_mh), b * (o ? p.o_mb : p.q_mb));
     };
+    if (warp == 1) pdl_start();  // the next kernel, once this one has its TMEM
+    // Before anything in memory is looked at: the lengths, where sequences have their own, then
+    // the tensors.  (The rows kernel has waited for all that came before it when this one starts,
+    // but only its end, which is waited for here, promises that their writes can be read.)
+    if (p.s.q_lens || p.s.k_lens) pdl_wait();
     if (warp == 0) {
         __syncwarp();  // (or the item is worked out for lane 0 and for the others, one after the other)
         KvItem mine;
         const bool some = make_item(p, block, mine);  // false: past the sequence's keys
+        pdl_wait();
         if (threadIdx.x == 0) {
             bar->item = mine;
             bar->some = some;
@@ -396,8 +401,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
             }
         }
     }
-    if (warp == 1) pdl_start();  // the next kernel, once this one has its TMEM
-    pdl_wait();                  // the rows' statistics
+    pdl_wait();  // (every thread: the rows' statistics)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -833,10 +837,13 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
         tma_load_5d(smem_u32((v ? sV : sK) + st * C::kTile), v ? &tmV : &tmK, fb, 0, c * kT, 0,
                     hk * (v ? p.v_mh : p.k_mh), b * (v ? p.v_mb : p.k_mb));
     };
+    if (warp == 1) pdl_start();  // the next kernel, once this one has its TMEM
+    if (p.s.q_lens || p.s.k_lens) pdl_wait();  // as in dkdv_cta
     if (warp == 0) {
         __syncwarp();
         DqItem mine;
         const bool some = make_item(p, block, mine);  // false: past the sequence's queries
+        pdl_wait();
         if (threadIdx.x == 0) {
             bar->item = mine;
             bar->some = some;
@@ -850,8 +857,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
             }
         }
     }
-    if (warp == 1) pdl_start();  // the next kernel, once this one has its TMEM
-    pdl_wait();                  // the rows' statistics
+    pdl_wait();  // (every thread: the rows' statistics)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1108,10 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ BwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    if (smem_misplaced(smem, p.s.status)) {
-        pdl_wait();
-        return;
-    }
+    if (smem_misplaced(smem, p.s.status)) return;
     if ((int)blockIdx.x < p.n_dkdv)
         dkdv_cta<D, F16>(tmQ, tmO, tmK, tmV, p, smem, blockIdx.x);
     else
@@ -1171,13 +1174,8 @@ svga_status launch(const svga_view &d_o, const svga_view &q, const svga_view &k,
     kp.n_dkdv = hk ? (int)kp.split.ctas() : 0;
     const long long n_dq = hq ? (long long)p->batch * p->q_heads * kp.n_qblk : 0;
     const unsigned grid = (unsigned)(kp.n_dkdv + n_dq);
-    if (hq) {
-        rc = launch_after(bwd_kernel<D, F16>, grid, kThreads, kAlloc, st, "window backward", tq, to,
-                          tk, tv, kp);
-    } else {  // no rows kernel before it, whose wait would cover the inputs it reads at once
-        bwd_kernel<D, F16><<<grid, kThreads, kAlloc, st>>>(tq, to, tk, tv, kp);
-        rc = check_launch_of("window backward");
-    }
+    rc = launch_after(bwd_kernel<D, F16>, grid, kThreads, kAlloc, st, "window backward", tq, to, tk,
+                      tv, kp);
     if (rc != SVGA_OK) return rc;
     if (hk && kp.split.slots() > 0) {
         const long long n =
