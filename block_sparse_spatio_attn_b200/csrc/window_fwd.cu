@@ -16,9 +16,15 @@
 //   * tensors are strided and batched (5-D tensor maps, one copy a tile), query heads share key
 //     heads, every sequence may have its own lengths; rows of V past a sequence's end are set
 //     to 0 in shared memory before they meet P (0 times a NaN left there is not 0);
-//   * bf16 or fp16.  P reaches at most the tile-sum limit: 2^16 in bf16, 2^15 in fp16 (65504
-//     is its largest value); what underflows in fp16 (below 2^-24 of a sum >= 1) is lost
-//     below the rounding of O;
+//   * bf16 or fp16.  P is rounded to the tensors' type for its product with V, as the tensor
+//     cores take operands of one type: half a step relative, the weight of one rounding of O.  It
+//     reaches at most the tile-sum limit: 2^16 in bf16, 65504, the largest value, in fp16.  fp16
+//     has few exponents below 1 (steps of 2^-24), and a long tail of keys that all round to 0
+//     would be missing from O while it stays in the sum; there the reference lies 2^6 below the
+//     first tile's maximum, so that a P is off by at most 2^-31 of the row's largest: n keys by
+//     n 2^-31 together, half a step of O at 2^20 keys.  (2^8 would
+//     still fit a tile of equal scores, but hardly any later rise: 2 x 4,000 tokens, 16 heads of 64
+//     on 4, four sinks first: 84 us against 72);
 //   * with few items for the GPU's SMs some or all key lists are split over CTAs that leave
 //     fp32 partial rows in the workspace, joined in a fixed order by a second kernel, whose
 //     launch overlaps the first (programmatic dependent launch);
@@ -214,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tmV, const FwdParams p)
 {
     using C = Cfg<D>;
-    constexpr float kSumLimit = F16 ? 32768.f : 65536.f;
+    constexpr float kSumLimit = F16 ? 65504.f : 65536.f;
+    constexpr float kBelow = F16 ? 6.f : 0.f;  // log2: the reference lies this far below a maximum
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -491,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sl2;
             };
-            if (m_used == -INFINITY) m_used = tile_max();
+            if (m_used == -INFINITY) m_used = tile_max() - kBelow;
             if (visit > 0) {  // the previous P V reads the P columns this tile writes
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->o_done[wg]),
                                                        (visit - 1) & 1, abort_flag));
@@ -524,8 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lt = (s0.x + s0.y) + (s1.x + s1.y);
                 const bool need = !(lt <= kSumLimit);
                 if (attempt > 0 || !__any_sync(0xffffffffu, need)) break;
-                // rare: O is rescaled to the tile's exact maximum and the tile is done again
-                const float m_new = need ? fmaxf(m_used, tile_max()) : m_used;
+                // rare: O is rescaled to the tile's exact maximum and the tile is done again (of 128
+                // terms whose sum passes the limit one is above 2^kBelow: the reference rises)
+                const float m_new = need ? fmaxf(m_used, tile_max() - kBelow) : m_used;
                 const float fac = need ? fast_exp2(m_used - m_new) : 1.f;
                 l *= fac;
                 m_used = m_new;
