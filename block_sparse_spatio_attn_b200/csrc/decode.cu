@@ -25,6 +25,10 @@
 // Measured: 8 sequences of 16,384 to 32,768 keys, 32 heads on 4, 385 MB: 70 us, 5.5 TB/s (84 %
 // of the measured copy); 16 sequences, 10 heads, 1,040 keys kept of up to 8,191, 85 MB: 23 us.
 // The running maximum moves only when a tile raises it (a warp vote), so O is rarely rescaled.
+// P is rounded to the cache's type for its product with V (operands of one type; half a step
+// relative, the weight of one rounding of O).  In fp16 it is held times 2^15 of the running
+// maximum, the most its largest value allows: of smaller ones none is off by more than 2^-40 of
+// the row's largest, so that a long tail of keys does not vanish (2^24 keys: 2^-16 of O).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -125,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
                                                           const DecodeParams p)
 {
     using S = DecodeSmem<D>;
+    constexpr float kBelow = F16 ? 15.f : 0.f;  // log2: the reference lies below the maximum
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
                             o[n][2 * r + 1] *= f;
                         }
                     }
-                    const float ref = m[r] == -INFINITY ? 0.f : m[r];
+                    const float ref = m[r] == -INFINITY ? 0.f : m[r] - kBelow;
                     float e[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
                     make_float2(o[n][2 * r], o[n][2 * r + 1]);
             if ((lane & 3) == 0)
                 *reinterpret_cast<float2 *>(ml + 2 * (warp * kRows + row)) =
-                    make_float2(m[r], l[r]);
+                    make_float2(m[r] - kBelow, l[r]);  // (sums are relative to the reference)
         }
     }
     __syncthreads();

@@ -629,9 +629,11 @@ SVGA_API svga_status svga_cache_append(const svga_view *k, const svga_view *v, i
  * causal flag changes nothing there).  q, o: [batch, q_heads, head_dim] of the cache's
  * type, q_heads a multiple of kv_heads; strides of batch and head as in svga_view
  * (stride_token is not read); o must not overlap q or the cache.  lse: fp32 contiguous
- * [batch, q_heads] or NULL.  An empty sequence gives O = 0 and lse = -inf.  Rows of a page past the length are read but change
- * nothing, NaN included.  One launch, no workspace: the CTAs of a cluster split the keys
- * and join over distributed shared memory, in a fixed order. */
+ * [batch, q_heads] or NULL.  An empty sequence gives O = 0 and lse = -inf.  Rows of a
+ * page past the length are read but change nothing, NaN included.  P is rounded as in
+ * svga_window_attention_fwd (fp16: up to 2^-40 of the largest).  One launch, no workspace:
+ * the CTAs of a cluster split the keys and join over distributed shared memory, in a fixed
+ * order. */
 SVGA_API svga_status svga_cache_decode(const svga_view *q, const svga_view *o, float *lse,
                                        int q_heads, const svga_paged_cache *cache,
                                        const svga_window_mask *mask, float scale,

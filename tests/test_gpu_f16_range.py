@@ -4,7 +4,7 @@ long tail of keys far below one key.
 
 Bounds.  u = 2^-11, half a step relative.
   * P is held relative to 2^6 times the largest of the first tile in the forward call, so a value
-    below fp16's normal range is off by at most 2^-25 / 2^6 = 2^-31 of the row's largest."""
+    below fp16's normal range is off by at most 2^-25 / 2^6 = 2^-31 of the row's largest (decode: less)."""
 import pytest
 import torch
 
@@ -59,3 +59,21 @@ def test_forward_keeps_a_long_tail_far_below_one_key(d, n, heads, rows):
         for h in (0, heads - 1):
             within(o[0, h], want.expand(rows, d), tol.expand(rows, d))
         assert (lse - torch.logsumexp(k.double() @ q.double(), 0).item()).abs().max() < 2.0 ** -15
+
+
+@pytest.mark.parametrize("d,n,page", [(64, 16_384, 16), (128, 16_384, 64), (128, 3001, 48), (64, 32_768, 256)])
+def test_decode_keeps_a_long_tail_far_below_one_key(d, n, page):
+    q, k, v, p = tail(d, n, 17.6875)
+    want, tol = tail_bound(p, v)
+    assert want.min() > 2 * tol.max()
+    need = -(-n // page)
+    kp, vp = (torch.zeros(need * page, d, dtype=FP) for _ in range(2))
+    kp[:n], vp[:n] = k, v
+    kp, vp = (x.view(need, 1, page, d).expand(need, 2, page, d).contiguous().cuda() for x in (kp, vp))
+    table = torch.arange(need, dtype=torch.int32, device="cuda").expand(3, need).contiguous()
+    lens = torch.full((3,), n, dtype=torch.int32, device="cuda")
+    dev_q = q.cuda().expand(3, 6, d).contiguous()
+    o, lse = torch.empty_like(dev_q), torch.empty(3, 6, device="cuda")
+    svga.svga_cache_decode(dev_q, kp, vp, table, lens, o, lse, M(), 1.0)
+    within(o, want.expand(3, 6, d), tol.expand(3, 6, d))
+    assert (lse - torch.logsumexp(k.double() @ q.double(), 0).item()).abs().max() < 2.0 ** -15
