@@ -43,10 +43,10 @@ __device__ __forceinline__ void put_row_16(uint32_t taddr, uint32_t tile, uint32
     }
 }
 
-// NCOL fp32 columns of this lane's TMEM row as they are into units 0 and up.
+// NCOL fp32 columns of this lane's TMEM row, times f, in fp32 into units 0 and up.
 template <int NCOL>
 __device__ __forceinline__ void put_row_32(uint32_t taddr, uint32_t tile, uint32_t half_step,
-                                           int row, bool any)
+                                           int row, float f, bool any)
 {
 #pragma unroll 1
     for (int j = 0; j < NCOL / 32; ++j) {
@@ -58,6 +58,8 @@ __device__ __forceinline__ void put_row_32(uint32_t taddr, uint32_t tile, uint32
 #pragma unroll
             for (int c = 0; c < 32; ++c) o[c] = 0u;
         }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             st_shared_v4(unit_addr(tile, half_step, row, 8 * j + c), o[4 * c], o[4 * c + 1],

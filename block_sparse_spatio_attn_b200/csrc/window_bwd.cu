@@ -5,7 +5,8 @@
 //
 // Three launches, each begun while the one before it ends (programmatic dependent launch): the
 // rows, one of dkdv's and dq's CTAs together, and a join where some of dkdv's items were split.
-//   rows    D and lse of every query row in the exp2 domain, negated, 1 KB per 128 rows;
+//   rows    D and lse of every query row in the exp2 domain, negated, 1 KB per 128 rows (fp16:
+//           and the norms of dO and V);
 //   dkdv    one CTA per 128 keys of a key head; walks the query blocks that keep any of
 //           them, over all query heads of the group, with dK and dV in TMEM throughout, so
 //           shared heads are summed without atomics and the order is fixed.  Sinks, which
@@ -23,6 +24,18 @@
 //
 // Warps 4-7 (group A) hold a lane's columns 0-63, warps 8-11 (B) columns 64-127, P staying in
 // registers in fp32 between the two steps of a tile.
+//
+// P and dS are rounded to the tensors' type for their products (operands of one type): half a step
+// relative.  fp16 has few exponents: dS is about |dO| |V| over the number of keys, which falls
+// below its smallest step (2^-24) for small output gradients, and passes its largest value
+// (65504) for large ones; and P is small where there are many keys.  So in fp16 both are held
+// times powers of two that the sums are divided by at the end:
+//   * P <= 1 times 2^14, by an addition to the exponent;
+//   * |dS_ij| = P_ij |dO_i V_j - D_i| <= |dO_i| max_j |V_j| + |D_i|, a bound that is brought to
+//     2^13 .. 2^14: in dq a query's own, in dkdv one for all the queries that a CTA visits.  The rows
+//     kernel finds the norms (of V too), which every CTA takes the largest of before its loop.
+// What falls below the normal range then is 2^-28 of the bound.  Rows that are not finite are left
+// out of the norms, so that they do not reach other tiles than those that visit them.
 //
 // What bounds them.  A product of 128 x 128 tiles with both operands in shared memory reads
 // 128 bytes a cycle there, all it has, so that barrier operations and loads of the other
@@ -47,7 +60,7 @@
 //     needed longest (dkdv: Q, dq: K) and two of the other.
 // Measured: 12,480 tokens, 4 heads of 128, frames of 960, window 2 and a sink frame: 250 us, 870
 // TFLOP/s of the five products of kept pairs (291 under sustained load); 2 x 2,001 tokens, 8 heads
-// on 2, window of 512: 47 us.
+// on 2, window of 512, fp16: 50 us (47.5 without the norms and powers of two).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -73,9 +86,12 @@ static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "regis
 
 struct BwdParams {
     WindowShape s;
-    View d_o, o, dq, dk, dv;
+    View d_o, o, v, dq, dk, dv;
     const float *lse;
-    float *stats;  // [batch * hq][query block][2][128]: -lse log2(e), -D
+    float *stats;  // [batch * hq][query block][kStatRows][128]: -lse log2(e), -D and |dO|
+    // fp16: the largest |dO| and |D| of parts of the query blocks, |V| of the key blocks
+    float2 *most_q;  // [batch * hq][query block][kParts]
+    float *most_v;   // [batch * hk][key block][kParts]
     float scale, scale_log2;
     int n_qblk, n_kblk;
     int n_dkdv;    // CTAs of dkdv
@@ -90,7 +106,8 @@ template <int D>
 struct Cfg {
     static constexpr int kTile = kT * D * 2;   // a 128-row tile of Q, K, V or dO
     static constexpr int kChunk = kT * 128;    // 64 columns of it
-    static constexpr int kStats = 2 * kT * 4;  // a query block's statistics
+    static constexpr int kStats = 2 * kT * 4;  // a query block's statistics for dkdv
+    static constexpr int kParts = kT * (D / 8) / 256;  // CTAs of the rows kernel to a block
     // dkdv: K, V, three stages of Q, two of dO with the block's statistics
     static constexpr int kQStages = 3, kOStages = 2;
     static constexpr int kKvData = (2 + kQStages + kOStages) * kTile + kOStages * kStats;
@@ -107,6 +124,27 @@ struct Cfg {
     static constexpr int kKvAlloc = alloc(kKvData), kDqAlloc = alloc(kDqData);
     static_assert(kKvAlloc <= 227 * 1024 && kDqAlloc <= 227 * 1024, "shared memory budget");
 };
+
+// fp16 holds P times 2^kPBits and dS times the power of two that brings its bound below 2^14.
+constexpr int kPBits = 14;
+template <bool F16>
+constexpr int kStatRows = F16 ? 3 : 2;
+
+// k with bound * 2^k in [2^13, 2^14) (a bound of 0, whose dS are 0, takes any)
+__device__ __forceinline__ int bits_to_2_14(float bound)
+{
+    const int e = (__float_as_int(bound) >> 23) - 127;  // 2^e <= bound < 2^(e + 1)
+    return min(max(13 - e, -64), 64);                   // (finite ones lie in -27 .. 61)
+}
+
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }
+
+__device__ __forceinline__ float warp_max(float x)
+{
+#pragma unroll
+    for (int k = 16; k > 0; k /= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+    return x;
+}
 
 __device__ __forceinline__ int clamped_len(const int32_t *lens, int b, int most)
 {
@@ -137,40 +175,77 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
 }
 
 // ----------------------------------------------------------------------------- rows
-// D / 8 threads a row.  Bound by HBM: dO and O are read once.  Rows past the sequence's
-// end get -inf and 0: their P and dS are 0.
+// D / 8 threads a row, kParts CTAs a block of 128.  Bound by HBM: dO and O are read once (fp16: and
+// V, whose CTAs come last).  Rows past the sequence's end get -inf and 0: their P and dS are 0.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) bwd_rows_kernel(const BwdParams p)
 {
     pdl_wait();
     pdl_start();
-    constexpr int kPer = D / 8;
-    const long long i = blockIdx.x * 256ll + threadIdx.x;
-    const long long row = i / kPer, bh = row / (p.n_qblk * kT);
-    if (bh >= (long long)p.s.batch * p.s.hq) return;
-    const int b = (int)(bh / p.s.hq), h = (int)(bh - (long long)b * p.s.hq);
-    const int t = (int)(row - bh * p.n_qblk * kT), c = 8 * (int)(i % kPer);
-    const bool there = t < clamped_len(p.s.q_lens, b, p.s.tq);
-    float sum = 0.f;
+    constexpr int kPer = D / 8, kParts = Cfg<D>::kParts;
+    const int q_ctas = p.s.batch * p.s.hq * p.n_qblk * kParts;
+    const bool values = F16 && (int)blockIdx.x >= q_ctas;
+    const int cta = blockIdx.x - (values ? q_ctas : 0), n_blk = values ? p.n_kblk : p.n_qblk;
+    const int heads = values ? p.s.hk : p.s.hq;
+    const long long row = (cta * 256ll + threadIdx.x) / kPer, bh = row / (n_blk * kT);
+    const int b = (int)(bh / heads), h = (int)(bh - (long long)b * heads);
+    const int t = (int)(row - bh * n_blk * kT), c = 8 * (int)(threadIdx.x % kPer);
+    const bool there = t < (values ? clamped_len(p.s.k_lens, b, p.s.tk)
+                                   : clamped_len(p.s.q_lens, b, p.s.tq));
+    float sum = 0.f, square = 0.f;
     if (there) {
+        const View &xv = values ? p.v : p.d_o;
         const uint4 x = *reinterpret_cast<const uint4 *>(
-            p.d_o.p + 2 * (b * p.d_o.sb + h * p.d_o.sh + t * p.d_o.st + c));
-        const uint4 y = *reinterpret_cast<const uint4 *>(
-            p.o.p + 2 * (b * p.o.sb + h * p.o.sh + t * p.o.st + c));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            xv.p + 2 * (b * xv.sb + h * xv.sh + t * xv.st + c));
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        if (!values) {
+            const uint4 y = *reinterpret_cast<const uint4 *>(
+                p.o.p + 2 * (b * p.o.sb + h * p.o.sh + t * p.o.st + c));
+            const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 u = unpack_16x2<F16>(xs[k]), v = unpack_16x2<F16>(ys[k]);
-            sum += u.x * v.x + u.y * v.y;
+            for (int k = 0; k < 4; ++k) {
+                const float2 u = unpack_16x2<F16>(xs[k]), v = unpack_16x2<F16>(ys[k]);
+                sum += u.x * v.x + u.y * v.y;
+            }
+        }
+        if constexpr (F16) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 u = unpack_16x2<F16>(xs[k]);
+                square += u.x * u.x + u.y * u.y;
+            }
         }
     }
 #pragma unroll
-    for (int k = kPer / 2; k > 0; k /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    if (c != 0) return;
-    const float lse = there ? p.lse[bh * p.s.tq + t] : -INFINITY;
-    float *out = p.stats + ((bh * p.n_qblk + t / kT) * 2) * kT + t % kT;
-    out[0] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // an empty row keeps nothing
-    out[kT] = -sum;
+    for (int k = kPer / 2; k > 0; k /= 2) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        if constexpr (F16) square += __shfl_xor_sync(0xffffffffu, square, k);
+    }
+    const float norm = sqrtf(square);
+    if (c == 0 && !values) {
+        const float lse = there ? p.lse[bh * p.s.tq + t] : -INFINITY;
+        float *out =
+            p.stats + (bh * p.n_qblk + t / kT) * kStatRows<F16> * kT + t % kT;
+        // (an empty row keeps nothing)
+        out[0] = lse == -INFINITY ? -INFINITY : -lse * kLog2e + (F16 ? (float)kPBits : 0.f);
+        out[kT] = -sum;
+        if constexpr (F16) out[2 * kT] = norm;
+    }
+    if constexpr (F16) {  // the CTA's largest norms
+        __shared__ float2 most[8];
+        const bool finite = norm < INFINITY && fabsf(sum) < INFINITY;
+        const float2 m = {warp_max(finite ? norm : 0.f), warp_max(finite ? fabsf(sum) : 0.f)};
+        if (threadIdx.x % 32 == 0) most[threadIdx.x / 32] = m;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float2 x = most[0];
+            for (int w = 1; w < 8; ++w) x = {fmaxf(x.x, most[w].x), fmaxf(x.y, most[w].y)};
+            if (values)
+                p.most_v[cta] = x.x;
+            else
+                p.most_q[cta] = x;
+        }
+    }
 }
 
 // Rows [first, 128) of a swizzled 128-row tile read as 0 (whole rows: the swizzle permutes
@@ -436,7 +511,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                 const uint32_t fb = smem_u32(&bar->st_full[os]);
                 mbar_arrive_expect_tx(fb, C::kStats);
                 bulk_load(smem_u32(sStats + os * C::kStats),
-                          p.stats + (((long long)b * p.s.hq + h) * p.n_qblk + qb0 + blk) * 2 * kT,
+                          p.stats + (((long long)b * p.s.hq + h) * p.n_qblk + qb0 + blk) *
+                                        kStatRows<F16> * kT,
                           C::kStats, fb);
                 st_issued = i + 1;
                 if (++blk == n_blk) {
@@ -573,6 +649,32 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
         bool ok = true;
         const int all_first = it.all_first, all_end = it.all_end;
         int blk = it.blk0;
+        int s_bits = 0;  // fp16: dS is held times 2^s_bits
+        if constexpr (F16) {
+            if (steps > 0) {
+                float most_o = 0.f, most_d = 0.f, most_v = 0.f;
+                for (int i = lane; i < steps; i += 32) {
+                    const int at = it.blk0 + i, g = at / n_blk;
+                    const float4 *m = reinterpret_cast<const float4 *>(
+                        p.most_q + (((long long)b * p.s.hq + hk * p.s.group + it.g0 + g) * p.n_qblk +
+                                    qb0 + at - g * n_blk) *
+                                       C::kParts);
+#pragma unroll
+                    for (int j = 0; j < C::kParts / 2; ++j) {
+                        const float4 y = m[j];
+                        most_o = fmaxf(most_o, fmaxf(y.x, y.z));
+                        most_d = fmaxf(most_d, fmaxf(y.y, y.w));
+                    }
+                }
+                if (lane < C::kParts)
+                    most_v = p.most_v[(((long long)b * p.s.hk + hk) * p.n_kblk + k0 / kT) * C::kParts +
+                                      lane];
+                s_bits = bits_to_2_14(warp_max(most_o) * warp_max(most_v) + warp_max(most_d));
+            }
+        }
+        // dS from P 2^kPBits, and back from either sum
+        const float2 to_s = make_float2(pow2(s_bits - kPBits), pow2(s_bits - kPBits));
+        const float back = F16 ? pow2(wg ? -s_bits : -kPBits) : 1.f;
         for (int i = 0; i < steps; ++i) {
             const int r0 = (qb0 + blk) * kT;
             if (++blk == n_blk) blk = 0;
@@ -644,6 +746,10 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                         make_float2(n.z, n.w));
                     u = ffma2(u, make_float2(pr[c], pr[c + 1]), make_float2(0.f, 0.f));
                     v = ffma2(v, make_float2(pr[c + 2], pr[c + 3]), make_float2(0.f, 0.f));
+                    if constexpr (F16) {
+                        u = ffma2(u, to_s, make_float2(0.f, 0.f));
+                        v = ffma2(v, to_s, make_float2(0.f, 0.f));
+                    }
                     pk[c / 2] = pack_16x2<F16>(u.x, u.y);
                     pk[c / 2 + 1] = pack_16x2<F16>(v.x, v.y);
                 }
@@ -675,13 +781,14 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
                     p.parts + ((it.slot * 2 + wg) * kT + row - lane) * D);
 #pragma unroll 1
                 for (int j = 0; j < 2; ++j) {
-                    put_row_32<D / 2>(acc + j * (D / 2), tile, C::kChunk, row, steps > 0);
+                    put_row_32<D / 2>(acc + j * (D / 2), tile, C::kChunk, row, back, steps > 0);
                     copy_rows_out<D / 8>(tile, C::kChunk, row - lane, 0, dst + 2 * D * j, 4 * D,
                                          valid, lane);
                 }
             } else {
                 const View &w = wg ? p.dk : p.dv;
-                put_row_16<D, F16>(acc, tile, C::kChunk, row, 0, wg ? p.scale : 1.f, steps > 0);
+                put_row_16<D, F16>(acc, tile, C::kChunk, row, 0, wg ? p.scale * back : back,
+                                   steps > 0);
                 copy_rows_out<D / 8>(tile, C::kChunk, row - lane, 0,
                                      w.p + 2 * (b * w.sb + hk * w.sh + (key - lane) * w.st),
                                      2 * w.st, valid, lane);
@@ -982,10 +1089,11 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
         const int qrow = r0 + row;
         MaskRange mr = {0, 0, 0};
         if (qrow < nq) mr = mask_range(p.s.mask, qrow + off, nk);
-        const float *st = p.stats + (((long long)b * p.s.hq + h) * p.n_qblk + blk) * 2 * kT + row;
-        const float nl = st[0], nd = st[kT];
-        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl),
-                     nd2 = make_float2(nd, nd);
+        const float *st =
+            p.stats + (((long long)b * p.s.hq + h) * p.n_qblk + blk) * kStatRows<F16> * kT + row;
+        float nl = st[0];
+        const float nd = st[kT];
+        float back = 1.f;
         bool ok = true;
         if (E > 0) {  // this lane's row of Q to TMEM as packed pairs, each group half of it
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->q_full), 0, abort_flag));
@@ -1008,6 +1116,25 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(smem_u32(&bar->a_ready));
         }
+        // fp16: this query's dS is held times 2^k, by way of P's exponent (after Q is on its way: S
+        // is computed meanwhile)
+        if constexpr (F16) {
+            float most_v = 0.f;
+            for (int i = lane; i < E; i += 32) {
+                const float4 *m = reinterpret_cast<const float4 *>(
+                    p.most_v + (((long long)b * p.s.hk + hk) * p.n_kblk + chunk_of(i)) * C::kParts);
+#pragma unroll
+                for (int j = 0; j < C::kParts / 4; ++j) {
+                    const float4 y = m[j];
+                    most_v = fmaxf(most_v, fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)));
+                }
+            }
+            const int k = bits_to_2_14(st[2 * kT] * warp_max(most_v) + fabsf(nd));
+            nl += (float)(k - kPBits);
+            back = pow2(-k);
+        }
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl),
+                     nd2 = make_float2(nd, nd);
         const ChunkList list = it.list;
         for (int i = 0; ok && i < E; ++i) {
             const int c = chunk_of(i), base = c * kT + 64 * wg;
@@ -1088,7 +1215,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
         }
         if (ok) {  // through Q's tile, which went to TMEM before the first step
             put_row_16<D / 2, F16>(tmem + lane_base + kDQ + wg * (D / 2), smem_u32(sQ), C::kChunk,
-                                   row, wg * (D / 16), p.scale, E > 0);
+                                   row, wg * (D / 16), p.scale * back, E > 0);
             copy_rows_out<D / 16>(smem_u32(sQ), C::kChunk, row - lane, wg * (D / 16),
                                   p.dq.p + 2 * (b * p.dq.sb + h * p.dq.sh + (qrow - lane) * p.dq.st +
                                                 wg * (D / 2)),
@@ -1166,8 +1293,9 @@ svga_status launch(const svga_view &d_o, const svga_view &q, const svga_view &k,
         return SVGA_ERR_CUDA;
     }
     if (hq) {
-        const long long n = (long long)p->batch * p->q_heads * kp.n_qblk * kT * (D / 8);
-        rc = launch_after(bwd_rows_kernel<D, F16>, (unsigned)((n + 255) / 256), 256, 0, st,
+        const long long n = (long long)p->batch * p->q_heads * kp.n_qblk +
+                            (F16 ? (long long)p->batch * p->kv_heads * kp.n_kblk : 0);
+        rc = launch_after(bwd_rows_kernel<D, F16>, (unsigned)(n * C::kParts), 256, 0, st,
                           "window backward rows", kp);
         if (rc != SVGA_OK) return rc;
     }
@@ -1193,10 +1321,19 @@ View to_view(const svga_view &v)
 
 }  // namespace
 
-static size_t stats_bytes(const svga_window_problem *p)
+// Floats of the workspace before the parts: the rows' statistics and, in fp16, the largest norms.
+struct RowFloats {
+    size_t stats, most_q, most_v;
+    size_t all() const { return stats + most_q + most_v; }
+};
+
+static RowFloats row_floats(const svga_window_problem *p)
 {
-    const size_t blocks = (size_t)(p->q_tokens + kT - 1) / kT;
-    return (size_t)p->batch * p->q_heads * blocks * 2 * kT * sizeof(float);
+    const size_t q = (size_t)p->batch * p->q_heads * ((p->q_tokens + kT - 1) / kT);
+    const size_t k = (size_t)p->batch * p->kv_heads * ((p->k_tokens + kT - 1) / kT);
+    if (p->dtype != SVGA_F16) return {q * kStatRows<false> * kT, 0, 0};
+    const int parts = p->head_dim == 128 ? Cfg<128>::kParts : Cfg<64>::kParts;
+    return {q * kStatRows<true> * kT, q * parts * 2, k * parts};
 }
 
 // How dkdv's items are split.  Items are key blocks; the ones that hold sinks, first in launch
@@ -1266,8 +1403,8 @@ static Split choose_bwd_split(const svga_window_problem *p)
 
 size_t window_bwd_workspace(const svga_window_problem *p)
 {
-    return stats_bytes(p) +
-           (size_t)choose_bwd_split(p).slots() * 2 * kT * p->head_dim * sizeof(float);
+    return (row_floats(p).all() + (size_t)choose_bwd_split(p).slots() * 2 * kT * p->head_dim) *
+           sizeof(float);
 }
 
 svga_status launch_window_bwd(const svga_view &d_o, const svga_view &q, const svga_view &k,
@@ -1279,6 +1416,7 @@ svga_status launch_window_bwd(const svga_view &d_o, const svga_view &q, const sv
     kp.s = to_shape(p);
     kp.d_o = to_view(d_o);
     kp.o = to_view(o);
+    kp.v = to_view(v);
     kp.dq = to_view(dq);
     kp.dk = to_view(dk);
     kp.dv = to_view(dv);
@@ -1296,7 +1434,10 @@ svga_status launch_window_bwd(const svga_view &d_o, const svga_view &q, const sv
     kp.by_bq = fast_div(p->batch * p->q_heads);
     kp.by_hq = fast_div(p->q_heads);
     kp.by_group = fast_div(p->q_heads / p->kv_heads);
-    kp.parts = kp.stats + stats_bytes(p) / sizeof(float);
+    const RowFloats n = row_floats(p);
+    kp.most_q = reinterpret_cast<float2 *>(kp.stats + n.stats);
+    kp.most_v = kp.stats + n.stats + n.most_q;
+    kp.parts = kp.stats + n.all();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (p->head_dim == 128)
         return p->dtype == SVGA_F16 ? launch<128, true>(d_o, q, k, v, kp, p, st)

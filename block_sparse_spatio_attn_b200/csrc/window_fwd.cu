@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {  // the tile holds half of a row of fp32
 #pragma unroll 1
                 for (int j = 0; j < 2; ++j) {
-                    put_row_32<D / 2>(tO + j * (D / 2), tile, C::kQChunk, row, visit > 0);
+                    put_row_32<D / 2>(tO + j * (D / 2), tile, C::kQChunk, row, 1.f, visit > 0);
                     copy_rows_out<D / 8>(tile, C::kQChunk, row - lane, 0,
                                          reinterpret_cast<char *>(p.part_o + (part - lane) * D +
                                                                   j * (D / 2)),

@@ -573,9 +573,11 @@ SVGA_API svga_status svga_window_attention_fwd(const svga_view *q, const svga_vi
  * pairs, D = rowsum(dO o O) and dS = P o (dO V^T - D),
  *   dV = P^T dO,   dQ = scale dS K,   dK = scale dS^T Q,
  * dK and dV summed over the query heads that share a key head.  o and lse are the forward
- * call's.  P and dS are rounded to the tensors' type for the products, sums are fp32, and
- * the order of every sum is fixed: the same inputs give the same bits.  dq, dk, dv have
- * the shapes of q, k, v; rows past a sequence's lengths are left as they were. */
+ * call's.  P and dS are rounded to the tensors' type for the products (in fp16 times powers
+ * of two taken from the norms of dO, V and D, so that output gradients of any size keep
+ * their accuracy), sums are fp32, and the order of every sum is fixed: the same inputs give
+ * the same bits.  dq, dk, dv have the shapes of q, k, v; rows past a sequence's lengths are
+ * left as they were. */
 SVGA_API svga_status svga_window_attention_bwd(const svga_view *d_o, const svga_view *q,
                                                const svga_view *k, const svga_view *v,
                                                const svga_view *o, const float *lse,
