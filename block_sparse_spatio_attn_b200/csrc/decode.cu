@@ -152,8 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     // the sequence, its kept keys and this CTA's share of their chunks
     int len = p.lens[b];
     if (len < 0 || len > p.max_pages * p.page_size) {
-        if (threadIdx.x == 0 && rank == 0 && p.status)
-            atomicCAS(p.status, 0, (int32_t)SVGA_ERR_INVALID_ARG);
+        if (threadIdx.x == 0 && rank == 0) report(p.status, SVGA_ERR_INVALID_ARG);
         len = 0;
     }
     const MaskRange mr = mask_range(p.mask, len - 1, len);
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
             if (j >= mr.hi || !(j + p.box > mr.lo || j < mr.sk)) return -1;
             const int page = p.page_table[(long long)b * p.max_pages + slot];
             if (page < 0 || page >= p.pages) {
-                if (p.status) atomicCAS(p.status, 0, (int32_t)SVGA_ERR_INVALID_ARG);
+                report(p.status, SVGA_ERR_INVALID_ARG);
                 return -1;
             }
             return (page * p.hk + kvh) * p.page_size + j - slot * p.page_size;
@@ -423,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
                 sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
     }
     if (ranks > 1) cluster_sync_all();  // no CTA leaves while another reads its shared memory
-    if (threadIdx.x == 0 && failed && p.status) atomicExch(p.status, (int32_t)SVGA_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && failed) report(p.status, SVGA_ERR_TIMEOUT);
 }
 
 template <int D, bool F16>

@@ -73,11 +73,6 @@ __device__ __forceinline__ void from_f(float &y, float x) { y = x; }
 __device__ __forceinline__ void from_f(__half &y, float x) { y = __float2half_rn(x); }
 __device__ __forceinline__ void from_f(__nv_bfloat16 &y, float x) { y = __float2bfloat16_rn(x); }
 
-__device__ __forceinline__ void set_status(int32_t *status)
-{
-    if (status) atomicCAS(status, 0, (int32_t)SVGA_ERR_INVALID_ARG);
-}
-
 // cos and sin of pair i at place (f, r, c)
 __device__ __forceinline__ float2 pair_cs(const RotParams &p, int i, int f, int r, int c)
 {
@@ -173,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
         const int n = p.new_lens ? p.new_lens[b] : p.tokens;
         const int len = p.lens[b];
         if (n < 0 || n > p.tokens || len < 0) {
-            if (unit == 0) set_status(p.status);
+            if (unit == 0) report(p.status, SVGA_ERR_INVALID_ARG);
             return;
         }
         if (t >= n) return;
@@ -185,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
     if (p.turn || DST == DST_ORDERED) {  // (a value goes where its key does, or neither)
         if (pos < 0 || pos >= (long long)p.F * p.S) {
             if (!placed) pdl_wait();  // (the host refuses such a first token: a CTA waits all the same)
-            if (unit == 0) set_status(p.status);
+            if (unit == 0) report(p.status, SVGA_ERR_INVALID_ARG);
             return;
         }
         f = (int)(pos / p.S);
@@ -200,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p,
                              ? p.page_table[(long long)b * p.max_pages + slot]
                              : -1;
         if (page < 0 || page >= p.pages) {
-            if (unit == 0) set_status(p.status);
+            if (unit == 0) report(p.status, SVGA_ERR_INVALID_ARG);
             return;
         }
         paged_row = (long long)page * p.heads * p.page_size + (pos - slot * p.page_size);

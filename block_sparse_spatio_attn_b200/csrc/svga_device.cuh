@@ -569,6 +569,12 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// A failure found by a streaming call: its status word keeps the first one.
+__device__ __forceinline__ void report(int32_t *status, int32_t code)
+{
+    if (status) atomicCAS(status, 0, code);
+}
+
 // Programmatic dependent launch.  Every kernel of the streaming calls but the one that fills
 // rotary's table is launched so, within a call and from call to call: its CTAs start, and set up
 // what needs no memory, while the kernel before it in the stream ends (single calls of a few

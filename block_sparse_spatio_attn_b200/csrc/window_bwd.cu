@@ -318,7 +318,7 @@ __device__ __forceinline__ bool smem_misplaced(const void *base, int32_t *status
 {
     if ((smem_u32(base) & 1023u) == 0) return false;
     pdl_wait();  // before anything in memory is touched
-    if (threadIdx.x == 0 && status) atomicCAS(status, 0, (int32_t)SVGA_ERR_ALIGNMENT);
+    if (threadIdx.x == 0) report(status, SVGA_ERR_ALIGNMENT);
     return true;
 }
 
@@ -801,8 +801,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap &tmQ, const CUtensorM
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (threadIdx.x == 0 && bar->abort && p.s.status)
-        atomicExch(p.s.status, (int32_t)SVGA_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && bar->abort) report(p.s.status, SVGA_ERR_TIMEOUT);
 }
 
 // Adds the parts of dkdv's split items in part order: one thread per 8 values of a row.
@@ -1228,8 +1227,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap &tmQ, const CUtensorMap
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (threadIdx.x == 0 && bar->abort && p.s.status)
-        atomicExch(p.s.status, (int32_t)SVGA_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && bar->abort) report(p.s.status, SVGA_ERR_TIMEOUT);
 }
 
 // dkdv's CTAs, the longer ones, then dq's: the two need nothing of each other, and in one launch

@@ -608,8 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (threadIdx.x == 0 && bar->abort && p.s.status)
-        atomicExch(p.s.status, (int32_t)SVGA_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && bar->abort) report(p.s.status, SVGA_ERR_TIMEOUT);
 }
 
 // Join of the split items: one thread per 8 values of a row; the parts' maxima give the
