@@ -21,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(os.path.dirname(HERE), "_build")
 LIB = os.path.join(HERE, "libsvga.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding_for.txt")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -56,15 +57,33 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def binding_for() -> str:
+    """What the binding is compiled against, and so good for: this torch, this Python."""
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _built_for() -> str:
+    """What the binding that is there was compiled against ("" when that is not known)."""
+    try:
+        with open(BINDING_FOR) as f:
+            return f.read()
+    except FileNotFoundError:
+        return ""
+
+
 def _build_binding(force: bool, verbose: bool) -> str:
     """csrc/binding.cpp: finds libsvga.so beside itself, torch's libraries are loaded by the
-    time it is imported."""
+    time it is imported.  Another torch or Python than it was compiled against makes it stale,
+    as a change of its sources does."""
     import sysconfig
 
     import torch
     src = os.path.join(CSRC, "binding.cpp")
     header = os.path.join(os.path.dirname(HERE), "include", "svga.h")
-    if not force and not _stale(BINDING, [src, header]):
+    if not force and not _stale(BINDING, [src, header]) and _built_for() == binding_for():
         return BINDING
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api",
@@ -73,7 +92,7 @@ def _build_binding(force: bool, verbose: bool) -> str:
            sysconfig.get_paths()["include"]]
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-fvisibility=hidden", f'-DSVGA_BUILT_FOR="{binding_for()}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-isystem{d}" for d in inc), src, "-o", tmp, f"-L{HERE}", "-l:libsvga.so",
            f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
@@ -83,6 +102,8 @@ def _build_binding(force: bool, verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(binding_for())
     return BINDING
 
 

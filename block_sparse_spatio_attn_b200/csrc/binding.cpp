@@ -456,4 +456,10 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding",
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__binding()
+{
+    PyObject *m = PyModule_Create(&g_module);
+    // the torch and Python it was compiled against: the importer refuses any other
+    if (m && PyModule_AddStringConstant(m, "built_for", SVGA_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}

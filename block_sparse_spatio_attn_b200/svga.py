@@ -543,7 +543,16 @@ def _binding():
             raise SvgaError(6, f"{BINDING_PATH} not built; run python -m "
                                "block_sparse_spatio_attn_b200.build")
         load()
-        from . import _binding as native
+        from .build import binding_for
+        try:
+            from . import _binding as native
+        except ImportError as e:  # its symbols are another torch's
+            raise SvgaError(6, f"{BINDING_PATH} does not fit {binding_for()} ({e}); run python -m "
+                               "block_sparse_spatio_attn_b200.build") from e
+        if native.built_for != binding_for():
+            raise SvgaError(6, f"{BINDING_PATH} is built for {native.built_for}, this is "
+                               f"{binding_for()}; run python -m "
+                               "block_sparse_spatio_attn_b200.build")
         native.set_error_class(SvgaError)
         _native = native
     return _native
