@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 from typing import Optional, Sequence
 
 import torch
@@ -238,6 +238,12 @@ class _Args:
                 raise SvgaError(1, f"{name} must be on a CUDA device")
 
 
+def _from_fields(spec):
+    """__reduce__ of a spec: a copy or an unpickled one is made from the fields anew, as the C
+    struct's pointers cannot be copied."""
+    return type(spec), tuple(getattr(spec, f.name) for f in fields(spec))
+
+
 @dataclass
 class ProblemSpec:
     """A problem with its host arrays kept alive for the C struct."""
@@ -262,6 +268,9 @@ class ProblemSpec:
         self.c = Problem(H, self.num_frames, self.grid_h, self.grid_w, self.head_dim,
                          self._ht, self._bd, self._od, self.anchor_frame0, self.tile_q,
                          self.tile_k, self.frame_pad)
+
+    def __reduce__(self):
+        return _from_fields(self)
 
     @property
     def tokens(self) -> int:
@@ -579,6 +588,10 @@ class RotarySpec:
     order: Optional[Sequence[int]] = None
 
     def __post_init__(self):
+        # tuples: a list could change behind the C struct, and has no hash
+        object.__setattr__(self, "pairs", tuple(self.pairs))
+        if self.order is not None:
+            object.__setattr__(self, "order", tuple(self.order))
         if len(self.pairs) != 3:
             raise SvgaError(2, f"pairs names {len(self.pairs)} axes, not 3")
         _int32("RotarySpec", self.num_frames, self.grid_h, self.grid_w, *self.pairs,
@@ -592,6 +605,9 @@ class RotarySpec:
         for name, x in (("_od", od), ("c", c), ("rows", rows),
                         ("ordered_heads", -1 if od is None else len(self.order))):
             object.__setattr__(self, name, x)
+
+    def __reduce__(self):
+        return _from_fields(self)
 
     @property
     def table_shape(self):
