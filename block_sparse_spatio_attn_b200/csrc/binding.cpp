@@ -224,6 +224,15 @@ int64_t integer(PyObject *o)
     return x;
 }
 
+int integer32(PyObject *o, const char *name)
+{
+    const int64_t x = integer(o);
+    if (x < INT32_MIN || x > INT32_MAX)
+        refuse(SVGA_ERR_INVALID_ARG, std::string(name) + ": " + std::to_string(x) +
+                                         " does not fit 32 bits");
+    return (int)x;
+}
+
 double real(PyObject *o)
 {
     const double x = PyFloat_AsDouble(o);
@@ -266,6 +275,7 @@ void rotary(PyObject *const *a)
     const float *table = table_of(t, a[5], integer(a[3]));
     const void *pos = t.optional(a[6], "positions", at::kInt, {n[0], n[2]});
     void *status = t.optional(a[9], "status", at::kInt, {1});
+    const int inverse = integer32(a[8], "inverse");
     const int64_t named = integer(a[4]);
     if (named >= 0 && named != n[1])
         refuse(SVGA_ERR_SHAPE, "order names " + std::to_string(named) + " heads, src has " +
@@ -273,7 +283,7 @@ void rotary(PyObject *const *a)
     t.done();
     check(svga_rotary(&vs, &vd, dim32(n[0], "src"), dim32(n[1], "src"), dim32(n[2], "src"),
                       dim32(n[3], "src"), dt, address<svga_rotary_spec>(a[2]), table,
-                      static_cast<const int32_t *>(pos), integer(a[7]), (int)integer(a[8]),
+                      static_cast<const int32_t *>(pos), integer(a[7]), inverse,
                       static_cast<int32_t *>(status), t.stream(a[10])));
 }
 

@@ -595,7 +595,7 @@ class RotarySpec:
         if len(self.pairs) != 3:
             raise SvgaError(2, f"pairs names {len(self.pairs)} axes, not 3")
         _int32("RotarySpec", self.num_frames, self.grid_h, self.grid_w, *self.pairs,
-               *(self.order or ()))
+               *(self.order or ()), int(self.interleaved))
         od = None if self.order is None else (ctypes.c_int32 * len(self.order))(*self.order)
         c = RotarySpecC(self.num_frames, self.grid_h, self.grid_w, (ctypes.c_int * 3)(*self.pairs),
                         int(self.interleaved), od)
@@ -647,7 +647,7 @@ class WindowMask:
     block: int = 1
 
     def __post_init__(self):
-        _int32("WindowMask", self.window, self.sinks, self.block)
+        _int32("WindowMask", int(self.causal), self.window, self.sinks, self.block)
         object.__setattr__(self, "c", WindowMaskC(int(self.causal), self.window, self.sinks,
                                                   self.block))
 
@@ -656,7 +656,11 @@ def svga_window_attention_size(q, k, mask: WindowMask) -> dict:
     """Bytes of workspace of the forward and the backward call on tensors shaped like q and k."""
     if q.dim() != 4 or k.dim() != 4:
         raise SvgaError(2, "q and k must be tensors of 4 dimensions")
-    (B, H, Tq, d), (_, G, Tk, _) = q.shape, k.shape
+    (B, H, Tq, d), (Bk, G, Tk, dk) = q.shape, k.shape
+    if (Bk, dk, k.dtype) != (B, d, q.dtype):
+        raise SvgaError(2, f"k has shape {tuple(k.shape)} of {k.dtype}, expected "
+                           f"{(B, G, Tk, d)} of {q.dtype}")
+    _int32("q and k", B, H, G, Tq, Tk, d)
     c = WindowProblemC(B, H, G, Tq, Tk, d,
                        {torch.bfloat16: 0, torch.float16: 1}.get(q.dtype, 2), mask.c)
     n = [ctypes.c_size_t() for _ in range(2)]
