@@ -424,6 +424,8 @@ svga_status svga_cache_append(const svga_view *k, const svga_view *v, int tokens
         return bad(SVGA_ERR_INVALID_ARG, "%sa table without a spec");
     }
     if (c->batch == 0 || tokens == 0) return SVGA_OK;
+    if (c->k_pages == c->v_pages)
+        return bad(SVGA_ERR_INVALID_ARG, "%sk_pages and v_pages start together: both are written");
     return launch_append(*k, *v, tokens, new_lens, c, spec, table, stream);
 }
 

@@ -620,7 +620,8 @@ typedef struct {
  * `tokens` when new_lens is NULL; rows n and up are not read.  With spec and table
  * (spec->order NULL) keys are rotated at their position on the way, as svga_rotary does;
  * both NULL: copied.  Two sequences must not append to one page (a page shared by a fork
- * is copied first); the same row written twice holds one of the two. */
+ * is copied first); the same row written twice holds one of the two.  k_pages and v_pages
+ * must not overlap (the same start is refused), nor the rows written with k and v. */
 SVGA_API svga_status svga_cache_append(const svga_view *k, const svga_view *v, int tokens,
                                        const int32_t *new_lens, const svga_paged_cache *cache,
                                        const svga_rotary_spec *spec, const float *table,

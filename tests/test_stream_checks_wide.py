@@ -6,7 +6,7 @@ import torch
 
 from block_sparse_spatio_attn_b200 import svga
 
-SHAPE = 2
+ARG, SHAPE = 1, 2
 A, Z = 1 << 20, 1 << 30  # addresses that are never touched
 
 
@@ -53,3 +53,12 @@ def test_workspace_size_of_tensors_that_no_call_takes():
     wide = q.expand(2**32 + 1, 2, 3, 64)  # ctypes would make it a batch of 1
     rejected(lambda: size(wide, wide, svga.WindowMask()), 2, "does not fit 32 bits")
     assert size(q, q[:, :1], svga.WindowMask())["bwd_bytes"] > 0
+
+
+def test_pages_that_keys_and_values_would_both_be_written_to_are_refused(lib):
+    """Decoding from one tensor as K and V is fine; appending writes both."""
+    c = svga.PagedCacheC(Z, Z, 4, 2, 16, 64, 0, 2, 2, A, A, None)
+    v = ctypes.byref(view())
+    rc = lib.svga_cache_append(v, v, 3, None, ctypes.byref(c), None, None, None)
+    assert rc == ARG and "start together" in lib.svga_last_error().decode(), (rc, lib.svga_last_error())
+    assert lib.svga_cache_append(v, v, 0, None, ctypes.byref(c), None, None, None) == 0
