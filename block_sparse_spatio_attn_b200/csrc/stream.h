@@ -110,6 +110,51 @@ __host__ __device__ __forceinline__ ChunkList chunk_list(const Mask &m, int p0, 
     return chunk_list<KN>(mask_range(m, p0, nk), mask_range(m, p1, nk));
 }
 
+// The merged chunk list of two consecutive runs of queries.  The windows of consecutive
+// positions touch or overlap, so every chunk of the list is visited by one of the runs.
+__host__ __device__ __forceinline__ void merge_lists(const ChunkList &l0, const ChunkList &l1,
+                                                     bool valid1, int &a, int &skip, int &end)
+{
+    a = l0.a;
+    int w0 = l0.w0, w1 = l0.w1;
+    if (valid1) {
+        a = l1.a > a ? l1.a : a;
+        if (l1.w1 > l1.w0) {
+            if (w1 <= w0 || l1.w0 < w0) w0 = l1.w0;
+            if (l1.w1 > w1) w1 = l1.w1;
+        }
+    }
+    skip = w0 > a ? w0 : a;
+    end = w1 > skip ? w1 : skip;
+}
+
+// The queries that keep any of the keys [k0, k1), in [first, end), and the ones that keep all of
+// them, [all_first, all_end), from the queries of three keys: the first (a sink, if one is
+// among them), the last, and the first that is no sink.  Each key's queries are contiguous, a
+// sink's run to the end, and first rows and (sinks aside) ends never decrease with the key.
+struct BlockRows {
+    int first, end, all_first, all_end;
+};
+
+__host__ __device__ __forceinline__ int block_key(const Mask &m, int k0, int k1, int e)
+{
+    if (e == 0) return k0;
+    if (e == 1) return k1 - 1;
+    const int key = m.sinks < k1 - 1 ? m.sinks : k1 - 1;
+    return key > k0 ? key : k0;
+}
+
+__host__ __device__ __forceinline__ BlockRows block_rows(const Mask &m, int k1, int nq, int first0,
+                                                         int end0, int first1, int end1, int end2)
+{
+    BlockRows r;
+    r.first = first0;
+    r.end = end0 > end1 ? end0 : end1;
+    r.all_first = first0 > first1 ? first0 : first1;
+    r.all_end = m.window < 0 ? end0 : (m.sinks < k1 ? end2 : nq);
+    return r;
+}
+
 #ifdef __CUDACC__
 __device__ __forceinline__ MaskRange range_of_lane(const MaskRange &r, int lane)
 {

@@ -351,20 +351,16 @@ __device__ __forceinline__ bool make_item(const BwdParams &p, int block, KvItem 
     const int nq = it.nq, off = it.off = it.nk - nq;
     const int k0 = it.k0 = kblk * kT, k1 = it.k1 = min(k0 + kT, it.nk);
     if (k0 >= it.nk) return false;
-    // the rows that keep the first key (a sink, if one is among them), the last, and the first
-    // that is no sink: a lane each
-    const int e = threadIdx.x & 3;
-    const int key = e == 0 ? k0 : (e == 1 ? k1 - 1 : max(k0, min(p.s.mask.sinks, k1 - 1)));
-    int first, end;
-    mask_rows(p.s.mask, key, nq, off, first, end);
+    int first, end;  // of three keys, a lane each
+    mask_rows(p.s.mask, block_key(p.s.mask, k0, k1, threadIdx.x & 3), nq, off, first, end);
     const int first0 = __shfl_sync(0xffffffffu, first, 0), end0 = __shfl_sync(0xffffffffu, end, 0);
     const int first1 = __shfl_sync(0xffffffffu, first, 1), end1 = __shfl_sync(0xffffffffu, end, 1);
     const int end2 = __shfl_sync(0xffffffffu, end, 2);
-    // rows that keep all: each key's are contiguous, and a sink's run to the end
-    it.all_first = max(first0, first1);
-    it.all_end = p.s.mask.window < 0 ? end0 : (p.s.mask.sinks < k1 ? end2 : nq);
-    first = first0;
-    end = max(end0, end1);
+    const BlockRows rows = block_rows(p.s.mask, k1, nq, first0, end0, first1, end1, end2);
+    it.all_first = rows.all_first;
+    it.all_end = rows.all_end;
+    first = rows.first;
+    end = rows.end;
     it.qb0 = first / kT;
     it.n_blk = end > first ? (end + kT - 1) / kT - it.qb0 : 0;
     const long long all = (long long)it.n_blk * p.s.group;

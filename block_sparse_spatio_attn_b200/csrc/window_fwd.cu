@@ -136,24 +136,6 @@ struct Barriers {
     Item item;  // worked out by warp 3 for all: by every warp it took 2,000 cycles more
 };
 
-// The merged chunk list of two consecutive runs of queries.  The windows of consecutive
-// positions touch or overlap, so every chunk of the list is visited by one of the runs.
-__host__ __device__ __forceinline__ void merge_lists(const ChunkList &l0, const ChunkList &l1,
-                                                     bool valid1, int &a, int &skip, int &end)
-{
-    a = l0.a;
-    int w0 = l0.w0, w1 = l0.w1;
-    if (valid1) {
-        a = l1.a > a ? l1.a : a;
-        if (l1.w1 > l1.w0) {
-            if (w1 <= w0 || l1.w0 < w0) w0 = l1.w0;
-            if (l1.w1 > w1) w1 = l1.w1;
-        }
-    }
-    skip = w0 > a ? w0 : a;
-    end = w1 > skip ? w1 : skip;
-}
-
 __device__ __forceinline__ int clamped_len(const int32_t *lens, int b, int most)
 {
     return lens ? min(max(lens[b], 0), most) : most;
