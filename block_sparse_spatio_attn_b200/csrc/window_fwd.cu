@@ -22,9 +22,11 @@
 //     has few exponents below 1 (steps of 2^-24), and a long tail of keys that all round to 0
 //     would be missing from O while it stays in the sum; there the reference lies 2^6 below the
 //     first tile's maximum, so that a P is off by at most 2^-31 of the row's largest: n keys by
-//     n 2^-31 together, half a step of O at 2^20 keys.  (2^8 would
-//     still fit a tile of equal scores, but hardly any later rise: 2 x 4,000 tokens, 16 heads of 64
-//     on 4, four sinks first: 84 us against 72);
+//     n 2^-31 together, half a step of O at 2^20 keys.  (2^8 would still fit a tile of equal
+//     scores, but hardly any later rise: 2 x 4,000 tokens, 16 heads of 64 on 4, four sinks first: 84
+//     us against 72.)  A maximum of few keys is soon passed by that of 128, so it is 2^5 below that
+//     of two or three and 2^3 below a single key's (a P off by 2^-28; the same with one sink
+//     first: 85 us with 2^6, 79 with 2^5, 72.8 so and with none);
 //   * with few items for the GPU's SMs some or all key lists are split over CTAs that leave
 //     fp32 partial rows in the workspace, joined in a fixed order by a second kernel, whose
 //     launch overlaps the first (programmatic dependent launch);
@@ -203,7 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using C = Cfg<D>;
     constexpr float kSumLimit = F16 ? 65504.f : 65536.f;
-    constexpr float kBelow = F16 ? 6.f : 0.f;  // log2: the reference lies this far below a maximum
+    // log2: the reference lies this far below a maximum of `keys` scores
+    auto below = [](int keys) {
+        return !F16 ? 0.f : (keys >= 4 ? 6.f : (keys >= 2 ? 5.f : 3.f));
+    };
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -457,13 +462,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();  // S is in registers: its columns may take another visit's
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar->s_free));
+            int keys = kKN;  // the row keeps, of the chunk
             if (!list.full(chunk)) {
                 const int k0 = chunk * kKN;
+                keys = 0;
 #pragma unroll
                 for (int w = 0; w < kKN / 32; ++w) {
                     const int x = k0 + 32 * w;
                     const uint32_t keep = (bits_below(mr.hi - x) & ~bits_below(mr.lo - x)) |
                                           bits_below(mr.sk - x);
+                    if (F16) keys += __popc(keep);
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
                         if (!((keep >> c) & 1u)) r[32 * w + c] = kNegInfBits;
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sl2;
             };
-            if (m_used == -INFINITY) m_used = tile_max() - kBelow;
+            if (m_used == -INFINITY) m_used = tile_max() - below(keys);
             if (visit > 0) {  // the previous P V reads the P columns this tile writes
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->o_done[wg]),
                                                        (visit - 1) & 1, abort_flag));
@@ -514,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool need = !(lt <= kSumLimit);
                 if (attempt > 0 || !__any_sync(0xffffffffu, need)) break;
                 // rare: O is rescaled to the tile's exact maximum and the tile is done again (of 128
-                // terms whose sum passes the limit one is above 2^kBelow: the reference rises)
-                const float m_new = need ? fmaxf(m_used, tile_max() - kBelow) : m_used;
+                // terms whose sum passes the limit one is above 2^8: the reference rises)
+                const float m_new = need ? fmaxf(m_used, tile_max() - below(kKN)) : m_used;
                 const float fac = need ? fast_exp2(m_used - m_new) : 1.f;
                 l *= fac;
                 m_used = m_new;

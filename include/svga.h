@@ -560,8 +560,8 @@ SVGA_API svga_status svga_window_attention_size(const svga_window_problem *probl
 
 /* O = softmax(scale Q K^T) V over the kept keys and lse = ln sum exp (fp32, contiguous
  * [batch, q_heads, q_tokens], or NULL).  P is rounded to the tensors' type for the P V
- * product (half a step, and in fp16 up to 2^-31 of the row's largest P), everything else is
- * fp32.  workspace: DEVICE scratch of at least fwd_bytes,
+ * product (half a step; in fp16 also up to 2^-31 of the row's largest P, or 2^-28 where the
+ * first 128-key chunk that a query visits keeps one key), everything else is fp32.  workspace: DEVICE scratch of at least fwd_bytes,
  * 256-byte aligned (NULL when fwd_bytes is 0); calls that may overlap need one each. */
 SVGA_API svga_status svga_window_attention_fwd(const svga_view *q, const svga_view *k,
                                                const svga_view *v, const svga_view *o, float *lse,

@@ -4,7 +4,8 @@ long tail of keys far below one key, key lists so long that each P is small, gra
 
 Bounds.  u = 2^-11, half a step relative.
   * P is held relative to 2^6 times the largest of the first tile in the forward call, so a value
-    below fp16's normal range is off by at most 2^-25 / 2^6 = 2^-31 of the row's largest (decode: less);
+    below fp16's normal range is off by at most 2^-25 / 2^6 = 2^-31 of the row's largest (2^3 and 2^-28
+    where that tile keeps one key; decode: 2^15 and 2^-40);
   * in the backward call P and dS are held times powers of two that bring their bounds to 2^14, so
     only what is 2^-28 of that bound leaves the normal range, and each is off by u relative;
   * errors of roundings that fall independently add like their squares: a sum of n of them, each
@@ -49,12 +50,12 @@ def tail(d, n, depth, seed=0):
     return q, k, v, p
 
 
-def tail_bound(p, v):
-    """P off by u, or 2^-31 of the largest; sums of 16 products each a step of 2^-23; the result's
+def tail_bound(p, v, least=2.0 ** -31):
+    """P off by u, or `least` of the largest; sums of 16 products each a step of 2^-23; the result's
     rounding."""
     v = v.double()
     o = p @ v
-    return o, (p @ v.abs()) * (U + len(p) / 16 * 2.0 ** -23 + 2.0 ** -17) + 2.0 ** -31 * v.abs().sum(0) + U * o.abs() + 2.0 ** -25
+    return o, (p @ v.abs()) * (U + len(p) / 16 * 2.0 ** -23 + 2.0 ** -17) + least * v.abs().sum(0) + U * o.abs() + 2.0 ** -25
 
 
 # 17.6875 nats: each key has 2^-25.5 of the first one's weight, which fp16 would round to 0
@@ -72,6 +73,27 @@ def test_forward_keeps_a_long_tail_far_below_one_key(d, n, heads, rows):
         for h in (0, heads - 1):
             within(o[0, h], want.expand(rows, d), tol.expand(rows, d))
         assert (lse - torch.logsumexp(k.double() @ q.double(), 0).item()).abs().max() < 2.0 ** -15
+
+
+@pytest.mark.parametrize("d,n,heads,rows", [(64, 16_384, 2, 1), (128, 20_000, 1, 200), (64, 9000, 160, 300)])
+def test_forward_keeps_the_tail_behind_a_single_sink(d, n, heads, rows):
+    """The first chunk keeps the sink alone; the window starts some chunks later."""
+    q, k, v, p = tail(d, n, 17.6875)
+    gap = 640
+    mask = M(window=n - rows - gap, sinks=1)   # the last row keeps keys gap + rows - 1 and up, the first gap
+    dev_q = q.cuda().expand(1, heads, rows, d).contiguous()
+    dev_k, dev_v = (x.cuda().expand(1, heads, n, d) for x in (k, v))
+    o, lse = torch.empty_like(dev_q), torch.empty(1, heads, rows, device="cuda")
+    svga.svga_window_attention_fwd(dev_q, dev_k, dev_v, o, lse, mask, 1.0)
+    keep = kept(mask, rows, n)
+    x = torch.where(keep, (k.double() @ q.double()).expand(rows, n), -math.inf)
+    for r in {0, rows // 2, rows - 1}:
+        assert keep[r, 0] and not keep[r, 1:gap].any()
+        want, tol = tail_bound(torch.softmax(x[r], 0), torch.where(keep[r][:, None], v, torch.zeros_like(v)), 2.0 ** -28)
+        assert want.max() > 4 * tol.max()
+        for h in (0, heads - 1):
+            within(o[0, h, r], want, tol)
+    assert (lse[0].double().cpu() - torch.logsumexp(x, 1)).abs().max() < 2.0 ** -15
 
 
 @pytest.mark.parametrize("d,n,page", [(64, 16_384, 16), (128, 16_384, 64), (128, 3001, 48), (64, 32_768, 256)])
