@@ -2,9 +2,10 @@
 //
 //   o = sum_j exp(x_j - m) v_j / sum_j exp(x_j - m),  x_j = scale q . k_j, over the kept keys.
 //
-// Bound by HBM: every kept key and value row is read once, 4 d bytes a key and key head.
+// Bound by HBM: every kept key and value row is read once, 4 d bytes a key and key head (by groups
+// above 16 query heads once for every 16 of them).
 //   * The query heads that share a key head are the 16 rows of one mma.sync tile (padded;
-//     a group above 16 takes several tiles), so a key row is read once for all of them and
+//     a group above 16 takes several tiles), so a key row is read once for 16 of them and
 //     the FP32 pipe does not limit shared heads.  tcgen05 has nothing to add here: its
 //     smallest tile has 64 query rows and the operand bytes, not the products, set the time.
 //   * A cluster of CTAs splits the keys of one (sequence, key head): CTA r takes the r-th
@@ -23,7 +24,9 @@
 //     streams 59 GB/s, but what 160 or 256 CTAs gain by it they lose in their second round
 //     (34 against 23 us, 80 against 70 us); chunks of 32 keys change nothing.
 // Measured: 8 sequences of 16,384 to 32,768 keys, 32 heads on 4, 385 MB: 70 us, 5.5 TB/s (84 %
-// of the measured copy); 16 sequences, 10 heads, 1,040 keys kept of up to 8,191, 85 MB: 23 us.
+// of the measured copy); 16 sequences, 10 heads, 1,040 keys kept of up to 8,191, 85 MB: 23.5 us
+// (160 CTAs, one a pair of sequence and head; its 17 or 18 chunks, one after the other, take 14.5
+// us at the rate of a CTA alone).
 // The running maximum moves only when a tile raises it (a warp vote), so O is rarely rescaled.
 // P is rounded to the cache's type for its product with V (operands of one type; half a step
 // relative, the weight of one rounding of O).  In fp16 it is held times 2^15 of the running
@@ -468,8 +471,10 @@ svga_status launch(const svga_paged_cache *c, const DecodeParams &p, int ranks, 
     return SVGA_OK;
 }
 
-// CTAs per (sequence, key head): as many as fill the GPU's two slots an SM, while every CTA
-// keeps at least 128 keys of the longest sequence the page table could hold.
+// CTAs per (sequence, key head): doubled while the launch still fits the GPU's two slots an SM
+// and every CTA keeps at least 128 keys of the longest sequence the page table could hold.  From
+// 149 pairs of sequence and head on that is one each, whatever the lengths: a sequence much longer
+// than the others is then one CTA's alone.
 int choose_ranks(const svga_paged_cache *c, const Mask &m, int tiles)
 {
     const int cap = c->max_pages * c->page_size;

@@ -58,8 +58,9 @@
 //     the shared memory's reads;
 //   * shared memory holds, beside the resident tiles, three stages of the operand that is
 //     needed longest (dkdv: Q, dq: K) and two of the other.
-// Measured: 12,480 tokens, 4 heads of 128, frames of 960, window 2 and a sink frame: 250 us, 870
-// TFLOP/s of the five products of kept pairs (291 under sustained load); 2 x 2,001 tokens, 8 heads
+// Measured: 12,480 tokens, 4 heads of 128, frames of 960, window 2 and a sink frame: 295 us, 735
+// TFLOP/s of the five products of kept pairs (in a loop; one launch alone 265); 75,600 tokens, 10
+// heads, frames of 3,600, window 3 and a sink frame: 19.0 ms, 832 TFLOP/s; 2 x 2,001 tokens, 8 heads
 // on 2, window of 512, fp16: 50 us (47.5 without the norms and powers of two).
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -39,9 +39,10 @@
 // cycles), barriers tested ahead of need and a quarter of the exponentials as polynomials
 // (3,300) did not help.  A CTA's start and end take 8,000 cycles (2,700 until its loads are
 // out, 2,000 to the first S, 1,000 for the last P V, 2,000 for the rows).
-// Measured: 12,480 tokens, 4 heads of 128, frames of 960, window 2 and a sink frame: 86 us, 1,010
-// TFLOP/s of kept pairs (98 under sustained load, when the power limit holds the clock near
-// 1.3 GHz); 2 x 4,000 tokens, 16 heads of 64 on 4, window of 1,024 tokens: 73 us.
+// Measured: 12,480 tokens, 4 heads of 128, frames of 960, window 2 and a sink frame: 97 us, 900
+// TFLOP/s of kept pairs (in a loop, where the power limit holds the clock near 1.3 GHz; one launch
+// alone 90); 75,600 tokens, 10 heads of 128, frames of 3,600, window 3 and a sink frame: 4.94
+// ms, 1,276 TFLOP/s; 2 x 4,000 tokens, 16 heads of 64 on 4, window of 1,024 tokens: 73 us.
 // Query blocks are launched last first: under a causal mask those are the longest, and the
 // hardware hands CTAs out in index order.  Neighbouring CTAs are heads of one group, so
 // the K and V chunks they share meet in L2.

@@ -462,7 +462,8 @@ SVGA_API svga_status svga_unpermute_tokens_mapped(const void *src, void *dst,
 typedef enum { SVGA_BF16 = 0, SVGA_F16 = 1, SVGA_F32 = 2 } svga_dtype;
 
 /* Strided view of [batch, heads, tokens, head_dim]; strides in elements.  A stride of 0
- * (a broadcast dimension) is allowed where the view is only read. */
+ * over batch or heads (a broadcast dimension) is allowed where the view is only read; tokens
+ * lie at least head_dim apart. */
 typedef struct {
     void *data;
     int64_t stride_batch, stride_head, stride_token;
